@@ -335,6 +335,105 @@ bl_status bitlinear_grad_x_i8(const uint16_t* dy, const uint8_t* codes, const fl
 bl_status bitlinear_mask_threshold_hist(const float* w_latent, const uint8_t* mask, const float* w_scale, int64_t n_out,
                                         int64_t k_in, int m_group, unsigned long long* hist_out, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Projections kept out of the ternary scheme, the output head first of all.
+ * No counterpart on the pages (they keep such layers in higher precision).
+ *
+ * 8-bit float linear. Codes are e4m3 (largest value 448) or e5m2 (57344), with one
+ * power-of-two scale per block of 128 along the reduction:
+ *
+ *   amax = largest |value| of the block = m * 2^E, 1 <= m < 2; top = 8 (e4m3), 15 (e5m2)
+ *   e    = E - top + (m > 1.75), at least -127: the least scale that fits the block
+ *   code = value * 2^-e rounded to the format (nearest, ties to even); scale byte e + 127.
+ *
+ * Blocks of activations and gradients are 1 x 128, of weights 128 x 128 (the last ones
+ * smaller). A power of two scales exactly, so codes and scales are determined bit for
+ * bit. An all-zero block has byte 0; a block with an infinity or NaN has byte 255 and
+ * codes 0x7F, and every result it enters is NaN.
+ *
+ *   codes  uint8 [rows, cols].
+ *   scales uint8 [ceil(cols / 512), rows, 4]: block b of row r at [b / 4, r, b % 4]
+ *          (weights repeat a block's byte over its rows); bytes past the last block 0.
+ *   transposed copy (qt, scales_t): codes uint8 [cols, rows16], rows16 = rows rounded up
+ *          to 16, zero behind the rows; scales uint8 [ceil(rows / 512), cols, 4], blocks
+ *          of 128 along the rows. The backward products reduce along it.
+ * --------------------------------------------------------------------------- */
+typedef enum { BL_FP8_E4M3 = 0, BL_FP8_E5M2 = 1 } bl_fp8_format;
+typedef enum { BL_X_E4M3 = 0, BL_X_E5M2 = 1, BL_X_BF16 = 2 } bl_x_type;
+
+/*
+ * Codes of x [t, cols] bf16 (cols % 16 == 0, cols >= 16), activations or output
+ * gradients, in 1 x 128 blocks. qt_out and scales_t_out (both or neither) also get the
+ * transposed copy, quantised in its own blocks of 128 tokens, in the same pass over x.
+ */
+bl_status bitlinear_fp8_quant(const uint16_t* x, int64_t t, int64_t cols, int format, uint8_t* q_out,
+                              uint8_t* scales_out, uint8_t* qt_out, uint8_t* scales_t_out, void* stream);
+
+/*
+ * Codes of w [n_out, k_in] fp32 in 128 x 128 blocks; with qt_out and scales_t_out the
+ * transposed copy too (the same codes and blocks). Laid out once for serving, after
+ * every optimizer step for training.
+ */
+bl_status bitlinear_fp8_quant_weight(const float* w, int64_t n_out, int64_t k_in, int format, uint8_t* q_out,
+                                     uint8_t* scales_out, uint8_t* qt_out, uint8_t* scales_t_out, void* stream);
+
+/*
+ * y [t, n_out] = x . w^T from the codes, fp32 accumulation, one rounding to y_dtype
+ * (bl_dtype).
+ *   x, x_type    codes [t, k_in] of bitlinear_fp8_quant with x_scales, or bf16 [t, k_in]
+ *                (BL_X_BF16, x_scales unused), which the call quantises to e4m3 itself.
+ *   w_q, w_scales, w_format: from bitlinear_fp8_quant_weight.
+ *   workspace    bitlinear_fp8_fwd_workspace_size bytes (0 for 8-bit x and few tokens;
+ *                may then be NULL).
+ */
+size_t bitlinear_fp8_fwd_workspace_size(int64_t t, int64_t k_in, int x_type);
+bl_status bitlinear_fp8_fwd(const void* x, int x_type, const uint8_t* x_scales, const uint8_t* w_q, int w_format,
+                            const uint8_t* w_scales, int64_t t, int64_t k_in, int64_t n_out, void* y_out, int y_dtype,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of the 8-bit float linear, either output may be NULL:
+ *   grad_x [t, k_in] bf16 = dy . w       from dy's codes and w's transposed copy.
+ *   grad_w [n_out, k_in] (grad_w_dtype)  = dy^T . x from both transposed copies; zero for
+ *                                          an empty batch.
+ * The operands of an output that is not requested may be NULL.
+ */
+bl_status bitlinear_fp8_bwd(const uint8_t* dy_q, const uint8_t* dy_scales, const uint8_t* dy_qt,
+                            const uint8_t* dy_scales_t, int dy_format, const uint8_t* x_qt, const uint8_t* x_scales_t,
+                            int x_format, const uint8_t* w_qt, const uint8_t* w_scales_t, int w_format, int64_t t,
+                            int64_t k_in, int64_t n_out, uint16_t* grad_x, void* grad_w, int grad_w_dtype,
+                            void* stream);
+
+/*
+ * Softmax cross entropy of the head's logits l = x . w^T, without storing them:
+ *
+ *   lse[t]  = log sum_v exp(l[t, v])
+ *   loss[t] = lse[t] - l[t, targets[t]], and 0 where targets[t] is outside [0, v): such
+ *             a token (padding, a prompt position) has no loss and no gradient.
+ *
+ *   x [t, k_in] bf16, w [v, k_in] bf16, any v >= 1; targets [t] int64.
+ *   loss_out, lse_out [t] fp32 (lse_out also for tokens without a loss).
+ * Logits are accumulated in fp32 and never rounded.
+ */
+size_t bitlinear_linear_ce_fwd_workspace_size(int64_t t, int64_t v);
+bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const int64_t* targets, int64_t t, int64_t k_in,
+                                  int64_t v, float* loss_out, float* lse_out, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
+ * Its gradients, given lse of the forward call and grad_loss [t] fp32, the derivative of
+ * the total with respect to each loss[t]; either output may be NULL:
+ *   dl[t, v] = (exp(l[t, v] - lse[t]) - [v == targets[t]]) * grad_loss[t], rounded to bf16
+ *   grad_x [t, k_in] bf16 = dl . w,   grad_w [v, k_in] (grad_w_dtype) = dl^T . x.
+ * The logits are computed again, one piece of the vocabulary after another, so the
+ * workspace holds one piece of dl (and an fp32 sum of grad_x), never [t, v]. Sums are
+ * fp32 and in a fixed order. An x row without a loss must still be finite.
+ */
+size_t bitlinear_linear_ce_bwd_workspace_size(int64_t t, int64_t k_in, int64_t v, int want_grad_x);
+bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const int64_t* targets, const float* lse,
+                                  const float* grad_loss, int64_t t, int64_t k_in, int64_t v, uint16_t* grad_x,
+                                  void* grad_w, int grad_w_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises the current device, then returns BL_OK; BL_ERR_TIMEOUT if a kernel
  * of this library gave up on a bounded wait since the last call (bits 0-3); or
  * BL_ERR_CUDA if the decode kernel found its dynamic shared memory at an address

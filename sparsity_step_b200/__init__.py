@@ -25,3 +25,17 @@ from .bitlinear import (  # noqa: F401
     bitlinear_grad_w_grouped,
     sp_meta_shape,
 )
+from .head import (  # noqa: F401
+    BL_FP8_E4M3,
+    BL_FP8_E5M2,
+    bitlinear_fp8_bwd,
+    bitlinear_fp8_fwd,
+    bitlinear_fp8_fwd_workspace_size,
+    bitlinear_fp8_quant,
+    bitlinear_fp8_quant_weight,
+    bitlinear_linear_ce_bwd,
+    bitlinear_linear_ce_bwd_workspace_size,
+    bitlinear_linear_ce_fwd,
+    bitlinear_linear_ce_fwd_workspace_size,
+    fp8_scales_shape,
+)

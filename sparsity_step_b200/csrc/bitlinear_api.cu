@@ -14,9 +14,13 @@
 #include "codes_tc.cuh"
 #include "common.cuh"
 #include "diag_kernels.cuh"
+#include "fp8_quant.cuh"
+#include "fp8_stream.cuh"
+#include "gemm_fp8.cuh"
 #include "gemm_tc.cuh"
 #include "gemm_sp2.cuh"
 #include "gemm_tc2.cuh"
+#include "linear_ce.cuh"
 #include "quant_mask.cuh"
 
 namespace {
@@ -102,21 +106,28 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 2-D row-major tensor [outer, inner], boxes of [box_outer, box_inner], 128-byte
-// swizzled unless `swizzle` is false.
-bl_status make_map(CUtensorMap* m, CUtensorMapDataType dt, size_t elem, const void* base, uint64_t inner, uint64_t outer,
-                   uint32_t box_inner, uint32_t box_outer, bool swizzle = true) {
+// 2-D row-major tensor [outer, inner] with rows `stride` elements apart, boxes of
+// [box_outer, box_inner].
+bl_status make_map_strided(CUtensorMap* m, CUtensorMapDataType dt, size_t elem, const void* base, uint64_t inner,
+                           uint64_t outer, uint64_t stride, uint32_t box_inner, uint32_t box_outer,
+                           CUtensorMapSwizzle swizzle) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return fail(BL_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
   cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {inner * elem};
+  cuuint64_t strides[1] = {stride * elem};
   cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = enc(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(BL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return BL_OK;
+}
+
+// Contiguous rows, 128-byte swizzled unless `swizzle` is false.
+bl_status make_map(CUtensorMap* m, CUtensorMapDataType dt, size_t elem, const void* base, uint64_t inner, uint64_t outer,
+                   uint32_t box_inner, uint32_t box_outer, bool swizzle = true) {
+  return make_map_strided(m, dt, elem, base, inner, outer, inner, box_inner, box_outer,
+                          swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // Output tensor map of the TMA-store epilogue: [M, N] row-major, boxes of 32 rows x
@@ -1195,3 +1206,5 @@ extern "C" bl_status bitlinear_quant_mask_noalloc(const float* w_latent, int64_t
   const QmOutputs o{mask_out, codes_out, w_i8_out, nullptr, nullptr, k_in / 8, k_in / 8};
   return enqueue_quant_mask(w_latent, n_out, k_in, n_keep, m_group, o, w_scale_out, scratch, as_stream(stream));
 }
+
+#include "head_api.cuh"

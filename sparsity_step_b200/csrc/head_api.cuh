@@ -1,0 +1,510 @@
+// C ABI of the block-scaled 8-bit float linear and of the linear cross entropy (declared
+// in include/bitlinear.h). Part of bitlinear_api.cu, whose checks, error text and TMA
+// descriptor helpers it uses.
+#pragma once
+
+namespace {
+
+inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+// ------------------------------------------------------------------ 8-bit float linear
+
+bl_status check_fp8_format(int f, const char* what) {
+  if (f != BL_FP8_E4M3 && f != BL_FP8_E5M2) return fail(BL_ERR_INVALID_ARG, "%s must be BL_FP8_E4M3 or BL_FP8_E5M2", what);
+  return BL_OK;
+}
+
+template <bool kWeight>
+bl_status enqueue_fp8_quant(const bl::Fp8QuantArgs& a, bool e5m2, cudaStream_t st) {
+  const int64_t tiles = ((a.rows + 127) / 128) * ((a.cols + 127) / 128);
+  if (tiles > INT32_MAX) return fail(BL_ERR_UNSUPPORTED_SHAPE, "too much work in one call");
+  const unsigned grid = static_cast<unsigned>(tiles);
+  if (a.qt) {
+    if (e5m2) bl::fp8_quant_kernel<kWeight, true, true><<<grid, bl::kFp8QuantThreads, 0, st>>>(a);
+    else bl::fp8_quant_kernel<kWeight, false, true><<<grid, bl::kFp8QuantThreads, 0, st>>>(a);
+  } else {
+    if (e5m2) bl::fp8_quant_kernel<kWeight, true, false><<<grid, bl::kFp8QuantThreads, 0, st>>>(a);
+    else bl::fp8_quant_kernel<kWeight, false, false><<<grid, bl::kFp8QuantThreads, 0, st>>>(a);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "fp8 quant launch");
+  return BL_OK;
+}
+
+// One operand of the pair product: K-major codes [rows, k] (row stride k) and their scales.
+struct Fp8Operand {
+  const uint8_t* q;
+  const uint8_t* scales;
+  int64_t rows;
+  int e5m2;
+};
+
+// Width of the pair product's tiles: the multiple of 32 with the least modelled time. Per
+// 128 of K a tile costs the larger of its MMAs (2 cycles a column) and its operand loads
+// (128 + n / 2 rows of 128 bytes a CTA at 64 bytes a cycle), so narrow tiles pay for the
+// 256 rows of A they drag along; whole waves of tiles over the pairs decide.
+int fp8_tile_width(int64_t m, int64_t n, int64_t k_blocks, int pairs) {
+  const int64_t mb = (m + 255) / 256;
+  int best = 32;
+  double best_cost = 0;
+  for (int w = 32; w <= bl::kF8MaxN; w += 32) {
+    const int64_t tiles = mb * ((n + w - 1) / w);
+    const int64_t waves = (tiles + pairs - 1) / pairs;
+    const double cost = double(waves) * (double(k_blocks) * (256 + w) + 1500.0);
+    if (w == 32 || cost <= best_cost) {
+      best = w;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+// out[m, n] = A B^T with both operands' reduction of length k (codes [rows, k], k % 16 == 0).
+bl_status enqueue_fp8_gemm(const Fp8Operand& A, const Fp8Operand& B, int64_t k, void* out, bool f32, cudaStream_t st) {
+  constexpr size_t smem = bl::gemm_fp8_smem_bytes();
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(bl::kF8Threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  static PerDeviceSetup setup;
+  int max_clusters = 0;
+  if (bl_status s = per_device_setup(setup, &max_clusters, [&](int* r) {
+        cudaError_t e = cudaFuncSetAttribute(bl::gemm_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(fp8 gemm)");
+        cudaLaunchConfig_t probe = cfg;
+        probe.gridDim = dim3(2 * (device_sm_count() / 2));
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, bl::gemm_fp8_kernel, &probe);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters(fp8 gemm)");
+        *r = n > 0 ? n : 0;
+        return BL_OK;
+      }))
+    return s;
+  if (max_clusters <= 0) return fail(BL_ERR_CUDA, "no CTA pair of the 8-bit float product fits on this device");
+  bl::Fp8GemmArgs g{};
+  g.sa = reinterpret_cast<const uint32_t*>(A.scales);
+  g.sb = reinterpret_cast<const uint32_t*>(B.scales);
+  g.M = static_cast<int>(A.rows);
+  g.N = static_cast<int>(B.rows);
+  g.num_k_blocks = static_cast<int>((k + 127) / 128);
+  g.n_tile = fp8_tile_width(A.rows, B.rows, g.num_k_blocks, max_clusters);
+  g.num_m_blocks = static_cast<int>((A.rows + 255) / 256);
+  g.num_n_blocks = static_cast<int>((B.rows + g.n_tile - 1) / g.n_tile);
+  g.a_e5m2 = A.e5m2;
+  g.b_e5m2 = B.e5m2;
+  g.out_f32 = f32 ? 1 : 0;
+  bl::GemmArgs order{};
+  set_raster(order, double(A.rows) * double(k), double(B.rows) * double(k));
+  g.m_fastest = order.m_fastest;
+  const int64_t tiles = int64_t(g.num_m_blocks) * g.num_n_blocks;
+  if (tiles > INT32_MAX) return fail(BL_ERR_UNSUPPORTED_SHAPE, "too much work in one call");
+  CUtensorMap ta, tb, to;
+  if (bl_status s = make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A.q, k, A.rows, 128, 128)) return s;
+  if (bl_status s = make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B.q, k, B.rows, 128, g.n_tile / 2)) return s;
+  if (bl_status s = make_map_strided(&to, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                     f32 ? 4 : 2, out, B.rows, A.rows, B.rows, 32, 32,
+                                     f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+    return s;
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < max_clusters ? tiles : max_clusters));
+  cudaError_t e = cudaLaunchKernelEx(&cfg, bl::gemm_fp8_kernel, ta, tb, to, g);
+  if (e != cudaSuccess) return cuda_fail(e, "fp8 gemm launch");
+  return BL_OK;
+}
+
+// Tokens up to which the streaming product runs instead of the pair product, and up to
+// which it makes the codes of bf16 activations itself.
+constexpr int64_t kFp8StreamMaxTokens = 32;
+constexpr int64_t kFp8StreamQuantTokens = 8;
+
+template <int NT, bool kXBf16, bool kW5, bool kX5>
+bl_status launch_fp8_stream(const bl::Fp8StreamArgs& a, cudaStream_t st) {
+  const int blocks = (a.k + 127) / 128;
+  const int warps = blocks >= 16 ? 16 : blocks >= 8 ? 8 : 4;
+  bl::fp8_stream_kernel<NT, kXBf16, kW5, kX5><<<a.n / 16, 32 * warps, 0, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "fp8 stream launch");
+  return BL_OK;
+}
+template <int NT>
+bl_status enqueue_fp8_stream_codes(const bl::Fp8StreamArgs& a, bool w5, bool x5, cudaStream_t st) {
+  if (w5) return x5 ? launch_fp8_stream<NT, false, true, true>(a, st) : launch_fp8_stream<NT, false, true, false>(a, st);
+  return x5 ? launch_fp8_stream<NT, false, false, true>(a, st) : launch_fp8_stream<NT, false, false, false>(a, st);
+}
+
+size_t fp8_scale_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>((cols + 511) / 512) * 4 * rows; }
+
+// ------------------------------------------------------------------ linear cross entropy
+
+constexpr int64_t kCePieceBytes = int64_t(64) << 20;   // dl of one piece of the vocabulary
+
+// Vocabulary rows per piece of the backward pass: a multiple of 256.
+int64_t ce_piece(int64_t t, int64_t v) {
+  int64_t p = kCePieceBytes / (2 * (t > 0 ? t : 1)) / 256 * 256;
+  if (p < 1024) p = 1024;
+  const int64_t all = round_up(v, 256);
+  return p < all ? p : all;
+}
+
+// Shapes of the head's operators: those of every entry point, with tokens up to 2^30 (the
+// kernels count padded tiles in 32 bits).
+bl_status check_head_shape(int64_t t, int64_t k_in, int64_t n_out) {
+  if (t > (int64_t(1) << 30)) return fail(BL_ERR_UNSUPPORTED_SHAPE, "t=%lld out of range", (long long)t);
+  return check_shape(t, k_in, n_out);
+}
+
+bl_status check_ce(int64_t t, int64_t k_in, int64_t v) {
+  if (bl_status s = check_head_shape(t, k_in, 16)) return s;
+  if (v < 1 || v > (int64_t(1) << 30)) return fail(BL_ERR_UNSUPPORTED_SHAPE, "v=%lld: need 1 <= v <= 2^30", (long long)v);
+  return BL_OK;
+}
+
+bl_status launch_ce(bl::CeGroup& G, cudaStream_t st) {
+  constexpr size_t smem = bl::gemm2_smem_bytes();
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(bl::kGemmThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  static PerDeviceSetup setup;
+  int max_clusters = 0;
+  if (bl_status s = per_device_setup(setup, &max_clusters, [&](int* r) {
+        cudaError_t e = cudaFuncSetAttribute(bl::ce_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear ce)");
+        cudaLaunchConfig_t probe = cfg;
+        probe.gridDim = dim3(2 * (device_sm_count() / 2));
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, bl::ce_gemm_kernel, &probe);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters(linear ce)");
+        *r = n > 0 ? n : 0;
+        return BL_OK;
+      }))
+    return s;
+  if (max_clusters <= 0) return fail(BL_ERR_CUDA, "no CTA pair of the linear cross entropy fits on this device");
+  int64_t tiles = 0;
+  for (int i = 0; i < G.count; ++i) {
+    G.p[i].tile_begin = static_cast<int>(tiles);
+    tiles += int64_t(G.p[i].num_m_blocks) * G.p[i].num_n_blocks;
+    if (tiles > INT32_MAX) return fail(BL_ERR_UNSUPPORTED_SHAPE, "too much work in one call");
+  }
+  G.total_tiles = static_cast<int>(tiles);
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < max_clusters ? tiles : max_clusters));
+  cudaError_t e = cudaLaunchKernelEx(&cfg, bl::ce_gemm_kernel, G);
+  if (e != cudaSuccess) return cuda_fail(e, "linear ce launch");
+  return BL_OK;
+}
+
+// A bf16 operand [outer, inner] (row stride `stride` elements) as the product's A or B:
+// K-major (inner is the reduction; boxes of 128 rows) or MN-major (outer is).
+bl_status ce_operand(CUtensorMap* m, const void* p, int64_t inner, int64_t outer, int64_t stride, bool mn) {
+  return make_map_strided(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, inner, outer, stride, 64, mn ? 64 : 128,
+                          CU_TENSOR_MAP_SWIZZLE_128B);
+}
+bl_status ce_output(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t stride, bool f32) {
+  return make_map_strided(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f32 ? 4 : 2, p, cols,
+                          rows, stride, f32 ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+void ce_shape(bl::CeProblem& P, int mode, int64_t m, int64_t n, int64_t k, bool a_mn, bool b_mn) {
+  P.mode = mode;
+  P.a_mn = a_mn ? 1 : 0;
+  P.b_mn = b_mn ? 1 : 0;
+  P.M = static_cast<int>(m);
+  P.N = static_cast<int>(n);
+  P.num_k_blocks = static_cast<int>((k + 63) / 64);
+  P.num_m_blocks = static_cast<int>((m + 255) / 256);
+  P.num_n_blocks = static_cast<int>((n + 255) / 256);
+  bl::GemmArgs order{};
+  set_raster(order, 2.0 * double(m) * double(k), 2.0 * double(n) * double(k));
+  P.m_fastest = order.m_fastest;
+}
+
+// Layout of the workspaces (every part 256-byte aligned).
+struct CeFwdSpace {
+  size_t strips, target_logit, total;
+};
+CeFwdSpace ce_fwd_space(int64_t t, int64_t v) {
+  CeFwdSpace s{};
+  const size_t n = 2 * static_cast<size_t>((v + 255) / 256) * static_cast<size_t>(t) * sizeof(float2);
+  s.strips = 0;
+  s.target_logit = round256(n);
+  s.total = s.target_logit + round256(static_cast<size_t>(t) * sizeof(float));
+  return s;
+}
+struct CeBwdSpace {
+  size_t dl, acc, total;
+};
+CeBwdSpace ce_bwd_space(int64_t t, int64_t k_in, int64_t v, bool want_grad_x) {
+  CeBwdSpace s{};
+  const int64_t piece = ce_piece(t, v);
+  s.dl = 0;
+  s.acc = round256(static_cast<size_t>(t) * static_cast<size_t>(piece) * 2);
+  s.total = s.acc + (want_grad_x && piece < v ? round256(static_cast<size_t>(t) * static_cast<size_t>(k_in) * 4) : 0);
+  return s;
+}
+
+}  // namespace
+
+extern "C" {
+
+bl_status bitlinear_fp8_quant(const uint16_t* x, int64_t t, int64_t cols, int format, uint8_t* q_out, uint8_t* scales_out,
+                              uint8_t* qt_out, uint8_t* scales_t_out, void* stream) {
+  g_err[0] = 0;
+  if (bl_status s = check_fp8_format(format, "format")) return s;
+  if ((qt_out == nullptr) != (scales_t_out == nullptr))
+    return fail(BL_ERR_INVALID_ARG, "give both qt_out and scales_t_out, or neither");
+  if (cols < 16 || cols % 16 || cols > (int64_t(1) << 30))
+    return fail(BL_ERR_UNSUPPORTED_SHAPE, "cols=%lld: need cols >= 16, cols %% 16 == 0", (long long)cols);
+  if (bl_status s = check_head_shape(t, 64, 16)) return s;
+  if (t == 0) return BL_OK;   // empty batch: the arrays may be NULL
+  if (!x || !q_out || !scales_out) return fail(BL_ERR_INVALID_ARG, "x, q_out, scales_out are required");
+  if (!aligned16(x) || !aligned16(q_out) || !aligned16(scales_out) || (qt_out && (!aligned16(qt_out) || !aligned16(scales_t_out))))
+    return fail(BL_ERR_ALIGNMENT, "every pointer must be 16-byte aligned");
+  const bl::Fp8QuantArgs a{x, t, cols, round_up(t, 16), q_out, scales_out, qt_out, scales_t_out};
+  return enqueue_fp8_quant<false>(a, format == BL_FP8_E5M2, as_stream(stream));
+}
+
+bl_status bitlinear_fp8_quant_weight(const float* w, int64_t n_out, int64_t k_in, int format, uint8_t* q_out,
+                                     uint8_t* scales_out, uint8_t* qt_out, uint8_t* scales_t_out, void* stream) {
+  g_err[0] = 0;
+  if (!w || !q_out || !scales_out) return fail(BL_ERR_INVALID_ARG, "w, q_out, scales_out are required");
+  if (bl_status s = check_fp8_format(format, "format")) return s;
+  if ((qt_out == nullptr) != (scales_t_out == nullptr))
+    return fail(BL_ERR_INVALID_ARG, "give both qt_out and scales_t_out, or neither");
+  if (bl_status s = check_shape(0, k_in, n_out)) return s;
+  if (!aligned16(w) || !aligned16(q_out) || !aligned16(scales_out) || (qt_out && (!aligned16(qt_out) || !aligned16(scales_t_out))))
+    return fail(BL_ERR_ALIGNMENT, "every pointer must be 16-byte aligned");
+  const bl::Fp8QuantArgs a{w, n_out, k_in, n_out, q_out, scales_out, qt_out, scales_t_out};
+  return enqueue_fp8_quant<true>(a, format == BL_FP8_E5M2, as_stream(stream));
+}
+
+size_t bitlinear_fp8_fwd_workspace_size(int64_t t, int64_t k_in, int x_type) {
+  if (x_type != BL_X_BF16 || t <= kFp8StreamQuantTokens || k_in <= 0) return 0;
+  return round256(static_cast<size_t>(t) * static_cast<size_t>(k_in)) + round256(fp8_scale_bytes(t, k_in));
+}
+
+bl_status bitlinear_fp8_fwd(const void* x, int x_type, const uint8_t* x_scales, const uint8_t* w_q, int w_format,
+                            const uint8_t* w_scales, int64_t t, int64_t k_in, int64_t n_out, void* y_out, int y_dtype,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  if (x_type != BL_X_BF16 && x_type != BL_X_E4M3 && x_type != BL_X_E5M2)
+    return fail(BL_ERR_INVALID_ARG, "x_type must be BL_X_BF16, BL_X_E4M3 or BL_X_E5M2");
+  if (bl_status s = check_fp8_format(w_format, "w_format")) return s;
+  if (y_dtype != BL_OUT_BF16 && y_dtype != BL_OUT_F32) return fail(BL_ERR_INVALID_ARG, "y_dtype must be BL_OUT_BF16 or BL_OUT_F32");
+  if (!w_q || !w_scales) return fail(BL_ERR_INVALID_ARG, "w_q and w_scales are required");
+  if (bl_status s = check_head_shape(t, k_in, n_out)) return s;
+  if (!aligned16(w_q) || !aligned16(w_scales)) return fail(BL_ERR_ALIGNMENT, "every pointer must be 16-byte aligned");
+  if (t == 0) return BL_OK;   // empty batch: the t-sized arrays may be NULL
+  const bool bf16 = x_type == BL_X_BF16;
+  if (!x || !y_out || (!bf16 && !x_scales)) return fail(BL_ERR_INVALID_ARG, "x, y_out and the scales of 8-bit x are required");
+  const size_t need = bitlinear_fp8_fwd_workspace_size(t, k_in, x_type);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(BL_ERR_WORKSPACE, "workspace too small: %zu < %zu", workspace ? workspace_bytes : size_t(0), need);
+  if (!aligned16(x) || !aligned16(y_out) || (!bf16 && !aligned16(x_scales)) || (need && !aligned16(workspace)))
+    return fail(BL_ERR_ALIGNMENT, "every pointer must be 16-byte aligned");
+  cudaStream_t st = as_stream(stream);
+  const bool w5 = w_format == BL_FP8_E5M2, x5 = x_type == BL_X_E5M2, f32 = y_dtype == BL_OUT_F32;
+  if (bf16 && t > kFp8StreamQuantTokens) {   // codes of x in the workspace first
+    uint8_t* xq = static_cast<uint8_t*>(workspace);
+    uint8_t* xs = xq + round256(static_cast<size_t>(t) * static_cast<size_t>(k_in));
+    const bl::Fp8QuantArgs a{x, t, k_in, round_up(t, 16), xq, xs, nullptr, nullptr};
+    if (bl_status s = enqueue_fp8_quant<false>(a, false, st)) return s;
+    x = xq;
+    x_scales = xs;
+  }
+  if (t > kFp8StreamMaxTokens)
+    return enqueue_fp8_gemm({static_cast<const uint8_t*>(x), x_scales, t, x5}, {w_q, w_scales, n_out, w5}, k_in, y_out, f32, st);
+  bl::Fp8StreamArgs a{};
+  a.x = x;
+  a.xs = reinterpret_cast<const uint32_t*>(x_scales);
+  a.wq = w_q;
+  a.ws = reinterpret_cast<const uint32_t*>(w_scales);
+  a.y = y_out;
+  a.t = static_cast<int>(t);
+  a.k = static_cast<int>(k_in);
+  a.n = static_cast<int>(n_out);
+  a.y_f32 = f32 ? 1 : 0;
+  if (bf16 && t <= kFp8StreamQuantTokens)
+    return w5 ? launch_fp8_stream<1, true, true, false>(a, st) : launch_fp8_stream<1, true, false, false>(a, st);
+  if (t <= 8) return enqueue_fp8_stream_codes<1>(a, w5, x5, st);
+  if (t <= 16) return enqueue_fp8_stream_codes<2>(a, w5, x5, st);
+  return enqueue_fp8_stream_codes<4>(a, w5, x5, st);
+}
+
+bl_status bitlinear_fp8_bwd(const uint8_t* dy_q, const uint8_t* dy_scales, const uint8_t* dy_qt, const uint8_t* dy_scales_t,
+                            int dy_format, const uint8_t* x_qt, const uint8_t* x_scales_t, int x_format, const uint8_t* w_qt,
+                            const uint8_t* w_scales_t, int w_format, int64_t t, int64_t k_in, int64_t n_out, uint16_t* grad_x,
+                            void* grad_w, int grad_w_dtype, void* stream) {
+  g_err[0] = 0;
+  if (!grad_x && !grad_w) return fail(BL_ERR_INVALID_ARG, "request grad_x, grad_w or both");
+  if (bl_status s = check_fp8_format(dy_format, "dy_format")) return s;
+  if (grad_x)
+    if (bl_status s = check_fp8_format(w_format, "w_format")) return s;
+  if (grad_w) {
+    if (bl_status s = check_fp8_format(x_format, "x_format")) return s;
+    if (grad_w_dtype != BL_OUT_BF16 && grad_w_dtype != BL_OUT_F32)
+      return fail(BL_ERR_INVALID_ARG, "grad_w_dtype must be BL_OUT_BF16 or BL_OUT_F32");
+  }
+  if (bl_status s = check_head_shape(t, k_in, n_out)) return s;
+  if (grad_x && (!w_qt || !w_scales_t || (t != 0 && (!dy_q || !dy_scales))))
+    return fail(BL_ERR_INVALID_ARG, "grad_x needs dy_q, dy_scales, w_qt and w_scales_t");
+  if (grad_w && t != 0 && (!dy_qt || !dy_scales_t || !x_qt || !x_scales_t))
+    return fail(BL_ERR_INVALID_ARG, "grad_w needs dy_qt, dy_scales_t, x_qt and x_scales_t");
+  const void* all[] = {dy_q, dy_scales, dy_qt, dy_scales_t, x_qt, x_scales_t, w_qt, w_scales_t, grad_x, grad_w};
+  for (const void* p : all)
+    if (p && !aligned16(p)) return fail(BL_ERR_ALIGNMENT, "every pointer must be 16-byte aligned");
+  cudaStream_t st = as_stream(stream);
+  const int d5 = dy_format == BL_FP8_E5M2;
+  if (t == 0) {
+    if (grad_w) {
+      cudaError_t e = cudaMemsetAsync(grad_w, 0, static_cast<size_t>(n_out) * k_in * (grad_w_dtype == BL_OUT_F32 ? 4 : 2), st);
+      if (e != cudaSuccess) return cuda_fail(e, "grad_w zero");
+    }
+    return BL_OK;
+  }
+  if (grad_x)
+    if (bl_status s = enqueue_fp8_gemm({dy_q, dy_scales, t, d5}, {w_qt, w_scales_t, k_in, w_format == BL_FP8_E5M2}, n_out,
+                                       grad_x, false, st))
+      return s;
+  if (grad_w)
+    if (bl_status s = enqueue_fp8_gemm({dy_qt, dy_scales_t, n_out, d5}, {x_qt, x_scales_t, k_in, x_format == BL_FP8_E5M2},
+                                       round_up(t, 16), grad_w, grad_w_dtype == BL_OUT_F32, st))
+      return s;
+  return BL_OK;
+}
+
+size_t bitlinear_linear_ce_fwd_workspace_size(int64_t t, int64_t v) {
+  if (t <= 0 || v <= 0) return 0;
+  return ce_fwd_space(t, v).total;
+}
+
+bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const int64_t* targets, int64_t t, int64_t k_in,
+                                  int64_t v, float* loss_out, float* lse_out, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  g_err[0] = 0;
+  if (!w) return fail(BL_ERR_INVALID_ARG, "w is required");
+  if (bl_status s = check_ce(t, k_in, v)) return s;
+  if (!aligned16(w)) return fail(BL_ERR_ALIGNMENT, "every pointer must be 16-byte aligned");
+  if (t == 0) return BL_OK;   // empty batch: the t-sized arrays may be NULL
+  if (!x || !targets || !loss_out || !lse_out) return fail(BL_ERR_INVALID_ARG, "x, targets, loss_out, lse_out are required");
+  const CeFwdSpace sp = ce_fwd_space(t, v);
+  if (!workspace || workspace_bytes < sp.total)
+    return fail(BL_ERR_WORKSPACE, "workspace too small: %zu < %zu", workspace ? workspace_bytes : size_t(0), sp.total);
+  if (!aligned16(x) || !aligned16(targets) || !aligned16(loss_out) || !aligned16(lse_out) || !aligned16(workspace))
+    return fail(BL_ERR_ALIGNMENT, "every pointer must be 16-byte aligned");
+  cudaStream_t st = as_stream(stream);
+  bl::CeGroup G{};
+  G.count = 1;
+  G.v = v;
+  G.targets = targets;
+  G.strips = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + sp.strips);
+  G.target_logit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.target_logit);
+  bl::CeProblem& P = G.p[0];
+  ce_shape(P, bl::CE_LSE, t, v, k_in, false, false);
+  if (bl_status s = ce_operand(&P.tmA, x, k_in, t, k_in, false)) return s;
+  if (bl_status s = ce_operand(&P.tmB, w, k_in, v, k_in, false)) return s;
+  if (bl_status s = launch_ce(G, st)) return s;
+  bl::ce_join_kernel<<<static_cast<unsigned>((t + 31) / 32), 256, 0, st>>>(G.strips, 2 * P.num_n_blocks, t, v, targets,
+                                                                          G.target_logit, loss_out, lse_out);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "linear ce join launch");
+  return BL_OK;
+}
+
+size_t bitlinear_linear_ce_bwd_workspace_size(int64_t t, int64_t k_in, int64_t v, int want_grad_x) {
+  if (t <= 0 || v <= 0 || k_in <= 0) return 0;
+  return ce_bwd_space(t, k_in, v, want_grad_x != 0).total;
+}
+
+bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const int64_t* targets, const float* lse,
+                                  const float* grad_loss, int64_t t, int64_t k_in, int64_t v, uint16_t* grad_x, void* grad_w,
+                                  int grad_w_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  if (!grad_x && !grad_w) return fail(BL_ERR_INVALID_ARG, "request grad_x, grad_w or both");
+  if (!w) return fail(BL_ERR_INVALID_ARG, "w is required");
+  if (grad_w && grad_w_dtype != BL_OUT_BF16 && grad_w_dtype != BL_OUT_F32)
+    return fail(BL_ERR_INVALID_ARG, "grad_w_dtype must be BL_OUT_BF16 or BL_OUT_F32");
+  if (bl_status s = check_ce(t, k_in, v)) return s;
+  if (t != 0 && (!x || !targets || !lse || !grad_loss))
+    return fail(BL_ERR_INVALID_ARG, "x, targets, lse, grad_loss are required");
+  const void* all[] = {x, w, targets, lse, grad_loss, grad_x, grad_w, workspace};
+  for (const void* p : all)
+    if (p && !aligned16(p)) return fail(BL_ERR_ALIGNMENT, "every pointer must be 16-byte aligned");
+  cudaStream_t st = as_stream(stream);
+  const bool w32 = grad_w_dtype == BL_OUT_F32;
+  if (t == 0) {
+    if (grad_w) {
+      cudaError_t e = cudaMemsetAsync(grad_w, 0, static_cast<size_t>(v) * k_in * (w32 ? 4 : 2), st);
+      if (e != cudaSuccess) return cuda_fail(e, "grad_w zero");
+    }
+    return BL_OK;
+  }
+  const CeBwdSpace sp = ce_bwd_space(t, k_in, v, grad_x != nullptr);
+  if (!workspace || workspace_bytes < sp.total)
+    return fail(BL_ERR_WORKSPACE, "workspace too small: %zu < %zu", workspace ? workspace_bytes : size_t(0), sp.total);
+  uint8_t* dl = static_cast<uint8_t*>(workspace) + sp.dl;
+  float* acc = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.acc);
+  const int64_t piece = ce_piece(t, v);
+  const bool one = piece >= v;   // a single piece: grad_X needs no fp32 sum in memory
+  bl::CeGroup G{};
+  G.v = v;
+  G.targets = targets;
+  G.lse = lse;
+  G.grad = grad_loss;
+  for (int64_t v0 = 0; v0 < v; v0 += piece) {
+    const int64_t n = v - v0 < piece ? v - v0 : piece;
+    const uint16_t* wp = w + v0 * k_in;
+    {   // dl of the piece [t, n], row stride `piece`
+      bl::CeProblem& P = G.p[0];
+      G.count = 1;
+      ce_shape(P, bl::CE_DLOGITS, t, n, k_in, false, false);
+      P.v0 = static_cast<int>(v0);
+      if (bl_status s = ce_operand(&P.tmA, x, k_in, t, k_in, false)) return s;
+      if (bl_status s = ce_operand(&P.tmB, wp, k_in, n, k_in, false)) return s;
+      if (bl_status s = ce_output(&P.tmOut, dl, t, n, piece, false)) return s;
+      if (bl_status s = launch_ce(G, st)) return s;
+    }
+    G.count = 0;
+    if (grad_x) {
+      bl::CeProblem& P = G.p[G.count++];
+      ce_shape(P, one ? bl::CE_BF16 : v0 == 0 ? bl::CE_F32 : bl::CE_ADD_F32, t, k_in, n, false, true);
+      if (bl_status s = ce_operand(&P.tmA, dl, n, t, piece, false)) return s;
+      if (bl_status s = ce_operand(&P.tmB, wp, k_in, n, k_in, true)) return s;
+      if (bl_status s = one ? ce_output(&P.tmOut, grad_x, t, k_in, k_in, false) : ce_output(&P.tmOut, acc, t, k_in, k_in, true))
+        return s;
+    }
+    if (grad_w) {
+      bl::CeProblem& P = G.p[G.count++];
+      ce_shape(P, w32 ? bl::CE_F32 : bl::CE_BF16, n, k_in, t, true, true);
+      if (bl_status s = ce_operand(&P.tmA, dl, n, t, piece, true)) return s;
+      if (bl_status s = ce_operand(&P.tmB, x, k_in, t, k_in, true)) return s;
+      if (bl_status s = ce_output(&P.tmOut, static_cast<uint8_t*>(grad_w) + v0 * k_in * (w32 ? 4 : 2), n, k_in, k_in, w32))
+        return s;
+    }
+    if (bl_status s = launch_ce(G, st)) return s;
+  }
+  if (grad_x && !one) {
+    const int64_t n8 = t * k_in / 8;
+    int64_t grid = (n8 + 255) / 256;
+    const int64_t cap = int64_t(device_sm_count()) * 16;
+    if (grid > cap) grid = cap;
+    bl::ce_round_kernel<<<static_cast<unsigned>(grid), 256, 0, st>>>(reinterpret_cast<const float4*>(acc), n8,
+                                                                    reinterpret_cast<uint4*>(grad_x));
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "linear ce round launch");
+  }
+  return BL_OK;
+}
+
+}  // extern "C"

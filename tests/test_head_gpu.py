@@ -1,0 +1,344 @@
+"""GPU parity of the head's operators against the oracle in 64 bits.
+
+Tolerances. Codes and scales are exact. A product of codes is exact in fp32 and each
+addition of the accumulation is off by at most 2^-23 of the magnitudes summed so far (a
+truncating adder; a rounding one is twice as good): with S = sum |a b| and one addition
+per MMA of depth d plus the adds inside it (log2 d levels), |error| <= (K / d + log2 d) 2^-23 S.
+bf16 outputs add half a step, 2^-8 relative. dl is rounded to bf16 once, half a step again.
+"""
+import numpy as np
+import pytest
+import torch
+
+import sparsity_step_b200 as B
+from oracle import head_oracle as H
+
+pytestmark = pytest.mark.gpu
+FMT = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+BF16 = 2.0 ** -8
+U = 2.0 ** -23
+
+
+def dev(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a))
+    return (t if dtype is None else t.to(dtype)).cuda()
+
+
+def bf16(rng, *shape, scale=1.0, outliers=True):
+    """bf16-valued fp32 array: N(0, scale) with 1% of entries 20 times as large."""
+    x = rng.normal(size=shape).astype(np.float32) * scale
+    if outliers:
+        x = np.where(rng.random(shape) < 0.01, x * 20, x)
+    return torch.from_numpy(x).to(torch.bfloat16).float().numpy()
+
+
+def u8(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def acc_bound(k, depth, s):
+    return (k / depth + np.log2(depth) + 1) * U * s
+
+
+def check_quant(got, want, with_t):
+    assert np.array_equal(u8(got["scales"]), want["scales"])
+    assert np.array_equal(u8(got["q"]), want["q"])
+    if with_t:
+        assert np.array_equal(u8(got["scales_t"]), want["scales_t"])
+        assert np.array_equal(u8(got["qt"]), want["qt"])
+
+
+# ------------------------------------------------------------------ quantisers
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("t,c", [(1, 16), (1, 64), (3, 2048), (16, 128), (17, 144), (100, 208), (128, 512), (129, 528),
+                                 (300, 1088), (513, 64)])
+def test_quant(t, c, fmt):
+    rng = np.random.default_rng(t * 1000 + c)
+    x = bf16(rng, t, c) * np.exp2(rng.integers(-6, 6, (t, 1))).astype(np.float32)
+    x[t // 2, c // 2:] = 0.0
+    want = H.fp8_quant_both(x, fmt)
+    xd = dev(x, torch.bfloat16)
+    check_quant(B.bitlinear_fp8_quant(xd, want_t=True, fmt=FMT[fmt]), want, True)
+    check_quant(B.bitlinear_fp8_quant(xd, fmt=FMT[fmt]), want, False)
+
+
+def test_quant_extremes():
+    # borders of the scale, denormals, the largest values, an all-zero block, infinities and NaN
+    x = np.zeros((9, 256), np.float32)
+    x[0, :2] = [448.0, -448.0]
+    x[1, :2] = [450.0, 1.0]
+    x[2, 0] = 1.75
+    x[3, 0] = 1.7578125
+    x[4, 0] = 2.0 ** -133
+    x[5, :128] = 3.3895314e38
+    x[6, 7] = np.inf
+    x[7, 200] = np.nan
+    x[8, 130:140] = 2.0 ** -126
+    x = torch.from_numpy(x).to(torch.bfloat16).float().numpy()
+    got = B.bitlinear_fp8_quant(dev(x, torch.bfloat16), want_t=True)
+    check_quant(got, H.fp8_quant(x, "e4m3") and dict(zip(("q", "scales"), H.fp8_quant(x, "e4m3")[:2])), False)
+    want = H.fp8_quant_both(x, "e4m3")
+    assert np.array_equal(u8(got["scales_t"]), want["scales_t"])
+    fine = want["scales_t"][0, :, 0] != 255
+    assert np.array_equal(u8(got["qt"])[fine], want["qt"][fine])
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("n,k", [(16, 64), (48, 128), (128, 192), (144, 576), (272, 1088)])
+def test_quant_weight(n, k, fmt):
+    rng = np.random.default_rng(n + k)
+    w = (rng.normal(size=(n, k)) * 0.02).astype(np.float32)
+    w[:, :64] *= 1e-3
+    want = H.fp8_quant_both(w, fmt, 128)
+    check_quant(B.bitlinear_fp8_quant_weight(dev(w), want_t=True, fmt=FMT[fmt]), want, True)
+    check_quant(B.bitlinear_fp8_quant_weight(dev(w), fmt=FMT[fmt]), want, False)
+
+
+# ------------------------------------------------------------------ 8-bit products
+
+def product_close(y, a, b, k):
+    """y against a . b^T of code values."""
+    want, s = a @ b.T, np.abs(a) @ np.abs(b).T
+    tol = acc_bound(k, 32, s) + (BF16 * np.abs(want) if y.dtype == torch.bfloat16 else 0.0)
+    err = np.abs(f64(y) - want)
+    worst = np.max(err / np.maximum(tol, 1e-300))
+    assert worst <= 1.0, f"worst error {worst:.3f} of its bound"
+
+
+SHAPES = [(1, 64, 16), (1, 2048, 48), (2, 192, 16), (7, 1088, 32), (8, 576, 64), (9, 128, 16), (16, 640, 80), (17, 64, 48),
+          (32, 1024, 240), (33, 64, 16), (33, 1088, 256), (100, 576, 224), (128, 192, 512), (255, 128, 240), (257, 704, 272),
+          (600, 2112, 1040)]
+
+
+@pytest.mark.parametrize("t,k,n", SHAPES)
+def test_fwd(t, k, n):
+    rng = np.random.default_rng(t + k + n)
+    x, w = bf16(rng, t, k), (rng.normal(size=(n, k)) * 0.02).astype(np.float32)
+    w[: n // 2] *= 30.0   # blocks and rows with scales of their own
+    xo, wo = H.fp8_quant(x, "e4m3")[2], H.fp8_quant(w, "e4m3", 128)[2]
+    xd, wq = dev(x, torch.bfloat16), B.bitlinear_fp8_quant_weight(dev(w))
+    y = B.bitlinear_fp8_fwd(xd, wq["q"], wq["scales"])
+    product_close(y, xo, wo, k)
+    xq = B.bitlinear_fp8_quant(xd)
+    y32 = B.bitlinear_fp8_fwd(xq["q"], wq["q"], wq["scales"], x_scales=xq["scales"], y_dtype=torch.float32)
+    product_close(y32, xo, wo, k)
+    assert B.bitlinear_device_status()[0] == 0
+
+
+@pytest.mark.parametrize("xf,wf", [("e5m2", "e4m3"), ("e4m3", "e5m2"), ("e5m2", "e5m2")])
+@pytest.mark.parametrize("t", [3, 12, 20, 150])
+def test_fwd_formats(t, xf, wf):
+    k, n = 704, 144
+    rng = np.random.default_rng(t)
+    x, w = bf16(rng, t, k), (rng.normal(size=(n, k)) * 0.02).astype(np.float32)
+    xo, wo = H.fp8_quant(x, xf)[2], H.fp8_quant(w, wf, 128)[2]
+    xd, wq = dev(x, torch.bfloat16), B.bitlinear_fp8_quant_weight(dev(w), fmt=FMT[wf])
+    xq = B.bitlinear_fp8_quant(xd, fmt=FMT[xf])
+    product_close(B.bitlinear_fp8_fwd(xq["q"], wq["q"], wq["scales"], x_scales=xq["scales"], y_dtype=torch.float32), xo, wo, k)
+    if xf == "e5m2":
+        product_close(B.bitlinear_fp8_fwd(xd, wq["q"], wq["scales"]), H.fp8_quant(x, "e4m3")[2], wo, k)
+
+
+@pytest.mark.parametrize("t", [2, 20, 64])
+def test_fwd_row_scales_and_not_finite_rows(t):
+    # every row and block of both operands with a scale of its own, one row with an infinity:
+    # that token's outputs are NaN, the others are what they would be without it
+    k, n = 1088, 272
+    rng = np.random.default_rng(9)
+    x = bf16(rng, t, k, outliers=False) * np.exp2(rng.integers(-20, 20, (t, 1))).astype(np.float32)
+    x[:, 128:256] *= 2.0 ** 9
+    w = (rng.normal(size=(n, k))).astype(np.float32) * np.exp2(np.repeat(rng.integers(-9, 9, (n + 127) // 128), 128)[:n, None]).astype(np.float32)
+    wq = B.bitlinear_fp8_quant_weight(dev(w))
+    clean = B.bitlinear_fp8_fwd(dev(x, torch.bfloat16), wq["q"], wq["scales"], y_dtype=torch.float32)
+    product_close(clean, H.fp8_quant(x, "e4m3")[2], H.fp8_quant(w, "e4m3", 128)[2], k)
+    x[1, 700] = np.inf
+    y = B.bitlinear_fp8_fwd(dev(x, torch.bfloat16), wq["q"], wq["scales"], y_dtype=torch.float32)
+    assert torch.isnan(y[1]).all()
+    keep = torch.arange(t, device="cuda") != 1
+    assert torch.equal(y[keep], clean[keep])
+
+
+@pytest.mark.parametrize("t,k,n,df", [(1, 64, 16, "e4m3"), (5, 128, 48, "e5m2"), (16, 576, 224, "e4m3"), (37, 192, 1040, "e5m2"),
+                                      (130, 1088, 256, "e4m3"), (600, 704, 272, "e5m2"), (1025, 320, 528, "e4m3")])
+def test_bwd(t, k, n, df):
+    rng = np.random.default_rng(t + n)
+    x, dy = bf16(rng, t, k), bf16(rng, t, n, scale=1e-2, outliers=False)
+    w = (rng.normal(size=(n, k)) * 0.02).astype(np.float32)
+    dyo, xo, wo = H.fp8_quant_both(dy, df), H.fp8_quant_both(x, "e4m3"), H.fp8_quant_both(w, "e4m3", 128)
+    dyq = B.bitlinear_fp8_quant(dev(dy, torch.bfloat16), want_t=True, fmt=FMT[df])
+    xq = B.bitlinear_fp8_quant(dev(x, torch.bfloat16), want_t=True)
+    wq = B.bitlinear_fp8_quant_weight(dev(w), want_t=True)
+    gx, gw = B.bitlinear_fp8_bwd(dyq, xq, wq, grad_w_dtype=torch.float32)
+    product_close(gx, dyo["values"], wo["values_t"], n)
+    product_close(gw, dyo["values_t"], xo["values_t"], t + 32)
+    gx2, none = B.bitlinear_fp8_bwd(dyq, None, wq, want_grad_w=False)
+    assert none is None and torch.equal(gx2, gx)
+    none, gw2 = B.bitlinear_fp8_bwd(dyq, xq, None, want_grad_x=False)
+    assert none is None and torch.equal(gw2, gw.to(torch.bfloat16))
+    assert B.bitlinear_device_status()[0] == 0
+
+
+def test_fp8_empty_batch():
+    w = B.bitlinear_fp8_quant_weight(torch.randn(32, 128, device="cuda"), want_t=True)
+    x = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")
+    xq = B.bitlinear_fp8_quant(x, want_t=True)
+    assert B.bitlinear_fp8_fwd(x, w["q"], w["scales"]).shape == (0, 32)
+    dyq = B.bitlinear_fp8_quant(torch.empty(0, 32, dtype=torch.bfloat16, device="cuda"), want_t=True)
+    gw = torch.ones(32, 128, dtype=torch.float32, device="cuda")
+    gx, gw = B.bitlinear_fp8_bwd(dyq, xq, w, grad_w=gw)
+    assert gx.shape == (0, 128) and not gw.any()
+
+
+# ------------------------------------------------------------------ linear cross entropy
+
+def ce_inputs(t, k, v, seed, logit_std=2.0):
+    rng = np.random.default_rng(seed)
+    x, w = bf16(rng, t, k, outliers=False), bf16(rng, v, k, scale=logit_std / np.sqrt(k), outliers=False)
+    y = rng.integers(0, v, t)
+    y[rng.random(t) < 0.2] = -100
+    if t > 4:
+        y[1], y[2], y[3] = v, v - 1, 0     # just outside, the last and the first
+    g = rng.normal(size=t).astype(np.float32)
+    return x, w, y.astype(np.int64), g
+
+
+def logit_errors(x, w, k):
+    """Bound on each token's largest logit error."""
+    return acc_bound(k, 16, np.abs(x).astype(np.float64) @ np.abs(w).astype(np.float64).T).max(axis=1)
+
+
+def check_loss(loss, lse, o, d):
+    # lse moves by at most the largest logit error; its exponentials and sums add a few
+    # units, its fp32 value and the base-2 scaling two units of its magnitude
+    tol = d + 2.0 ** -20 + 4 * U * np.maximum(np.abs(o["lse"]), np.abs(o["logits"]).max(axis=1))
+    assert np.all(np.abs(f64(lse) - o["lse"]) <= tol)
+    assert np.all(np.abs(f64(loss) - o["loss"]) <= 2 * tol)
+    assert np.all(f64(loss)[~o["live"]] == 0.0)
+
+
+CE_SHAPES = [(1, 64, 1), (1, 2048, 1000), (2, 128, 2), (3, 64, 255), (8, 192, 256), (9, 64, 257), (32, 576, 31), (33, 64, 33),
+             (100, 128, 5003), (255, 320, 640), (257, 1088, 1031), (300, 64, 12289)]
+
+
+@pytest.mark.parametrize("t,k,v", CE_SHAPES)
+def test_linear_ce(t, k, v):
+    x, w, y, g = ce_inputs(t, k, v, t + v)
+    o = H.linear_ce(x, w, y, g)
+    xd, wd, yd, gd = dev(x, torch.bfloat16), dev(w, torch.bfloat16), dev(y), dev(g)
+    loss, lse = B.bitlinear_linear_ce_fwd(xd, wd, yd)
+    d = logit_errors(x, w, k)
+    check_loss(loss, lse, o, d)
+    gx, gw = B.bitlinear_linear_ce_bwd(xd, wd, yd, lse, gd)
+    check_ce_grads(gx, gw, x, w, o, d, k, v, t)
+    gx2, none = B.bitlinear_linear_ce_bwd(xd, wd, yd, lse, gd, want_grad_w=False)
+    assert none is None and torch.equal(gx2, gx)
+    none, gw32 = B.bitlinear_linear_ce_bwd(xd, wd, yd, lse, gd, want_grad_x=False, grad_w_dtype=torch.float32)
+    assert none is None and torch.equal(gw32.to(torch.bfloat16), gw)
+    assert B.bitlinear_device_status()[0] == 0
+
+
+def check_ce_grads(gx, gw, x, w, o, d, k, v, t):
+    """dl: half a bf16 step, plus p times what the exponent is off by (logit and lse errors
+    and their base-2 scaling); then the products' accumulation and the outputs' rounding."""
+    spread = 2 * d + 2.0 ** -20 + 8 * U * np.abs(o["logits"]).max(axis=1) + 4 * U * np.abs(o["lse"])
+    ddl = BF16 * np.abs(o["dl"]) + (1 + BF16) * o["p"] * np.expm1(spread)[:, None]
+    for got, want, err, s, depth in ((gx, o["grad_x"], ddl @ np.abs(w), np.abs(o["dl"]) @ np.abs(w), v),
+                                     (gw, o["grad_w"], ddl.T @ np.abs(x), np.abs(o["dl"]).T @ np.abs(x), t)):
+        tol = err + acc_bound(depth + 256, 16, s) + BF16 * (np.abs(want) + err) + 1e-37
+        worst = np.max(np.abs(f64(got) - want) / tol)
+        assert worst <= 1.0, f"worst error {worst:.3f} of its bound"
+
+
+def test_linear_ce_pieces():
+    # more than one piece of the vocabulary, the last one ragged
+    t, k, v = 4500, 64, 9001
+    x, w, y, g = ce_inputs(t, k, v, 5)
+    o = H.linear_ce(x, w, y, g)
+    xd, wd, yd, gd = dev(x, torch.bfloat16), dev(w, torch.bfloat16), dev(y), dev(g)
+    assert B.bitlinear_linear_ce_bwd_workspace_size(t, k, v) < 2 * t * v
+    loss, lse = B.bitlinear_linear_ce_fwd(xd, wd, yd)
+    d = logit_errors(x, w, k)
+    check_loss(loss, lse, o, d)
+    check_ce_grads(*B.bitlinear_linear_ce_bwd(xd, wd, yd, lse, gd), x, w, o, d, k, v, t)
+
+
+@pytest.mark.parametrize("std", [0.0, 40.0])
+def test_linear_ce_flat_and_peaked(std):
+    # all logits equal (loss log v) and logits of some hundred (one column has all the mass)
+    t, k, v = 40, 128, 700
+    x, w, y, g = ce_inputs(t, k, v, 3, std)
+    o = H.linear_ce(x, w, y, g)
+    xd, wd, yd, gd = dev(x, torch.bfloat16), dev(w, torch.bfloat16), dev(y), dev(g)
+    loss, lse = B.bitlinear_linear_ce_fwd(xd, wd, yd)
+    check_loss(loss, lse, o, logit_errors(x, w, k))
+    check_ce_grads(*B.bitlinear_linear_ce_bwd(xd, wd, yd, lse, gd), x, w, o, logit_errors(x, w, k), k, v, t)
+
+
+def test_linear_ce_nothing_counts():
+    t, k, v = 70, 64, 300
+    x, w, _, g = ce_inputs(t, k, v, 4)
+    y = np.full(t, -100, np.int64)
+    xd, wd, yd, gd = dev(x, torch.bfloat16), dev(w, torch.bfloat16), dev(y), dev(g)
+    loss, lse = B.bitlinear_linear_ce_fwd(xd, wd, yd)
+    gx, gw = B.bitlinear_linear_ce_bwd(xd, wd, yd, lse, gd)
+    assert not loss.any() and not gx.any() and not gw.any() and torch.isfinite(lse).all()
+
+
+def test_linear_ce_empty_batch():
+    w = torch.randn(50, 64, device="cuda").to(torch.bfloat16)
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty(0, dtype=torch.int64, device="cuda")
+    loss, lse = B.bitlinear_linear_ce_fwd(x, w, y)
+    gw = torch.ones(50, 64, dtype=torch.bfloat16, device="cuda")
+    gx, gw = B.bitlinear_linear_ce_bwd(x, w, y, lse, torch.empty(0, device="cuda"), grad_w=gw)
+    assert loss.shape == (0,) and gx.shape == (0, 64) and not gw.any()
+
+
+# ------------------------------------------------------------------ as they are used
+
+def test_head_training_step_runs_together():
+    """A ternary layer, an 8-bit float projection and the head's loss, forward and back, on
+    a stream of their own, twice into the same buffers and once as a replayed graph: the
+    three runs agree bit for bit."""
+    t, k, n, v = 200, 256, 512, 1003
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(t, k, generator=gen, device="cuda").to(torch.bfloat16)
+    w1 = torch.randn(n, k, generator=gen, device="cuda") * 0.02
+    w2 = torch.randn(k, n, generator=gen, device="cuda") * 0.02
+    head = (torch.randn(v, k, generator=gen, device="cuda") * 0.1).to(torch.bfloat16)
+    y = torch.randint(0, v, (t,), generator=gen, device="cuda")
+    g = torch.full((t,), 1.0 / t, device="cuda")
+
+    def step():
+        qm = B.bitlinear_quant_mask(w1, 6, 8)
+        xq, a = B.bitlinear_act_quant(x)
+        h, _ = B.bitlinear_fwd(xq, a, qm["w_scale"], w_i8=qm["w_i8"])
+        wq = B.bitlinear_fp8_quant_weight(w2, want_t=True)
+        hq = B.bitlinear_fp8_quant(h, want_t=True)
+        z = B.bitlinear_fp8_fwd(hq["q"], wq["q"], wq["scales"], x_scales=hq["scales"])
+        loss, lse = B.bitlinear_linear_ce_fwd(z, head, y)
+        dz, dhead = B.bitlinear_linear_ce_bwd(z, head, y, lse, g)
+        dzq = B.bitlinear_fp8_quant(dz, want_t=True, fmt=torch.float8_e5m2)
+        dh, dw2 = B.bitlinear_fp8_bwd(dzq, hq, wq)
+        dx, dw1 = B.bitlinear_bwd(dh, x, qm["codes"], qm["w_scale"])
+        return loss, dhead, dw2, dx, dw1
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        first = step()
+        again = step()
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            captured = step()
+        graph.replay()
+        s.synchronize()
+    for a, b, c in zip(first, again, captured):
+        assert torch.equal(a, b) and torch.equal(a, c) and torch.isfinite(a.float()).all()
+    assert float(first[0].mean()) > 1.0
