@@ -12,15 +12,21 @@
 // the input gradient (dY x W^T's codes) and the weight gradient (dY^T's x X^T's) are all
 // this one kernel on different operands.
 //
-// A cluster of two CTAs computes one 256 x n_tile tile (n_tile a multiple of 32, at most
-// 224): CTA r loads 128 rows of A and n_tile / 2 rows of B per 128-byte K step, six stages.
-// Why 224 and not the 256 of the other pair kernels: the scales live in TMEM beside the
-// two accumulators, 2 x 224 + 64 = 512 columns.
+// A cluster of two CTAs computes one tile of 256 rows x kHalves * n_half columns (n_half a
+// multiple of 32, at most 224). Why 224 and not the 256 of the other pair kernels: the
+// scales live in TMEM beside the accumulators, 2 x 224 + 64 = 512 columns. What bounds the
+// product is the operands' way from L2 to the SMs (about 40 bytes a cycle and SM), so
+//   kHalves = 2 (the wide tile): both accumulators belong to one tile, whose two column
+//     halves share every load of A: 44 KB per 128 of K for 896 MMA cycles. With no
+//     accumulator to spare, the next tile's first four K blocks run on half 0 alone while
+//     the epilogue still drains half 1, then on half 1, so the tensor cores do not wait.
+//   kHalves = 1: one accumulator per tile, the other one drained meanwhile; 30 KB per 448
+//     MMA cycles. For products with too few wide tiles to fill the SMs evenly.
 //
 // Scales. A 32-bit word holds a row's bytes of four consecutive K blocks ([K / 512, rows, 4]
-// in memory), so one copy serves 16 MMAs, which select their byte by the instruction
-// descriptor's scale ids. Warp 10 gathers the words of the CTA's 128 rows of A and of the
-// tile's n_tile rows of B (both CTAs need all of them) into the order that
+// in memory), so one copy serves 16 MMAs per half, which select their byte by the
+// instruction descriptor's scale ids. Warp 10 gathers the words of the CTA's 128 rows of A
+// and of the tile's rows of B (both CTAs need all of them) into the order that
 // tcgen05.cp.32x128b.warpx4 takes: row r of a 128-row group at 16 (r % 32) + 4 (r / 32).
 // The leader's MMA thread copies them to both CTAs' TMEM in issue order with its MMAs.
 //
@@ -34,24 +40,40 @@
 
 namespace bl {
 
-constexpr int kF8MaxN = 224;
-constexpr int kF8Stages = 6;
-constexpr int kF8ABytes = 128 * 128;
-constexpr int kF8BBytes = kF8MaxN / 2 * 128;
-constexpr int kF8StageBytes = kF8ABytes + kF8BBytes;      // 30 KB
-constexpr int kF8SfSlots = 4;
-constexpr int kF8SfBytes = 3 * 512;                       // A: 128 rows; B: 2 x 128 rows
+constexpr int kF8MaxN = 224;                              // columns of one accumulator
+constexpr int kF8ABytes = 128 * 128;                      // one K block (128 bytes) of the CTA's rows
+constexpr int kF8BBytes = kF8MaxN / 2 * 128;              // and of its columns of one accumulator
+// A stage: two K blocks of a narrow tile (3 x 60 KB), one of a wide tile (4 x 44 KB). Eight
+// MMAs each: a stage's wait and commit cost the issuing warp about 120 cycles (measured
+// with four MMAs a stage and no loads: 128 us against 109 us with eight).
+template <int kHalves>
+struct F8Stage {
+  static constexpr int kCount = kHalves == 2 ? 4 : 3;
+  static constexpr int kBlocks = 3 - kHalves;             // K blocks of a stage
+  static constexpr int kBlockBytes = kF8ABytes + kHalves * kF8BBytes;
+  static constexpr int kBytes = kBlocks * kBlockBytes;
+  static constexpr int kSfGroups = 1 + 2 * kHalves;       // 128-row groups of scales: A, then B by halves
+  static constexpr int kSfSlots = kHalves == 2 ? 3 : 4;
+};
+constexpr int kF8RingBytes = 3 * 2 * (kF8ABytes + kF8BBytes);   // 180 KB
+constexpr int kF8SfRingBytes = 3 * 5 * 512;
 constexpr int kF8EpiWarps = 8;
 constexpr int kF8SfWarp = 2 + kF8EpiWarps;
 constexpr int kF8Threads = 32 * (kF8SfWarp + 1);          // 352
-constexpr int kF8StgBytes = 32 * 128;                     // per epilogue warp: 32 rows x 32 columns (<= 4 B)
+constexpr int kF8StgBytes = 32 * 128;                     // per epilogue warp: 32 rows x 32 columns fp32, or two of bf16
 constexpr uint32_t kF8SfCol0 = 2 * kF8MaxN;               // TMEM: scales after the accumulators
 constexpr int kF8BarBytes = 512;
-static_assert(kF8StageBytes % 1024 == 0 && kF8ABytes % 1024 == 0, "128B-swizzle atoms need 1 KB alignment");
-static_assert(kF8SfCol0 + 16 * kF8SfSlots <= 512, "accumulators and scales exceed the TMEM of a CTA");
+static_assert(kF8ABytes % 1024 == 0 && kF8BBytes % 1024 == 0, "128B-swizzle atoms need 1 KB alignment");
+static_assert(F8Stage<1>::kCount * F8Stage<1>::kBytes <= kF8RingBytes && F8Stage<2>::kCount * F8Stage<2>::kBytes <= kF8RingBytes,
+              "stages");
+static_assert(F8Stage<1>::kSfSlots * F8Stage<1>::kSfGroups * 512 <= kF8SfRingBytes &&
+                  F8Stage<2>::kSfSlots * F8Stage<2>::kSfGroups * 512 <= kF8SfRingBytes,
+              "scale slots");
+static_assert(kF8SfCol0 + 4 * F8Stage<1>::kSfSlots * F8Stage<1>::kSfGroups <= 512 &&
+                  kF8SfCol0 + 4 * F8Stage<2>::kSfSlots * F8Stage<2>::kSfGroups <= 512,
+              "accumulators and scales exceed the TMEM of a CTA");
 constexpr size_t gemm_fp8_smem_bytes() {
-  return 1024 + static_cast<size_t>(kF8Stages) * kF8StageBytes + kF8EpiWarps * kF8StgBytes + kF8SfSlots * kF8SfBytes +
-         kF8BarBytes;
+  return 1024 + static_cast<size_t>(kF8RingBytes) + kF8EpiWarps * kF8StgBytes + kF8SfRingBytes + kF8BarBytes;
 }
 static_assert(gemm_fp8_smem_bytes() <= 232448, "fp8 GEMM exceeds the shared memory of a CTA");
 
@@ -59,9 +81,9 @@ struct Fp8GemmArgs {
   const uint32_t* sa;   // [ceil(K / 512), M] words of A's scale bytes
   const uint32_t* sb;   // [ceil(K / 512), N]
   int M, N;
-  int n_tile;           // multiple of 32, <= kF8MaxN
+  int n_half;           // columns of one accumulator: multiple of 32, <= kF8MaxN
   int num_k_blocks;     // ceil(K / 128)
-  int num_m_blocks, num_n_blocks;   // 256-row and n_tile-column blocks
+  int num_m_blocks, num_n_blocks;   // 256-row blocks and tiles of kHalves * n_half columns
   int m_fastest;
   int a_e5m2, b_e5m2;
   int out_f32;
@@ -72,6 +94,22 @@ struct Fp8GemmArgs {
 // (1 = UE8M0), M >> 4 [24,29), a scale id [29,31). Both operands K-major.
 __device__ __forceinline__ uint32_t make_idesc_mxf8(uint32_t a_fmt, uint32_t b_fmt, uint32_t n, uint32_t m, uint32_t sf_id) {
   return (sf_id << 4) | (a_fmt << 7) | (b_fmt << 10) | ((n >> 3) << 17) | (1u << 23) | ((m >> 4) << 24) | (sf_id << 29);
+}
+// One lane of a converged warp, always the same one. The MMA and producer warps run their
+// loops with all 32 lanes and branch on this only around the instructions themselves: from
+// such a branch the compiler issues them with descriptors and addresses kept in uniform
+// registers, where they take them. Measured (8192 tokens, eight MMAs): 300 cycles to issue;
+// 570 by a lane chosen once and a predicate on each instruction, 670 from a branch on that
+// lane, which made the issuing warp slower than the tensor cores (11008 -> 2048: 171 us
+// against 145).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(on));
+  return on != 0;
 }
 __device__ __forceinline__ void tc_mma_mxf8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                  uint32_t sfa, uint32_t sfb, uint32_t acc) {
@@ -91,22 +129,35 @@ __device__ __forceinline__ uint64_t make_sf_desc(uint32_t saddr) {   // 8-row co
   return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(1) << 16 |
          static_cast<uint64_t>(128 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
 }
-// As mbar_wait, for a barrier that the other CTA's threads arrive on too after writing
-// what they hand over: acquires at cluster scope.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, const volatile int* abort) {
-  const uint64_t t0 = global_timer_ns();
-  for (;;) {
+// Wait of a whole warp, bounded like mbar_wait. `live` is 0 once a wait has given up, and
+// every later wait returns at once; the first to give up raises the pair's abort flags. The
+// loops around it do not branch on the outcome (their trip counts stay uniform), they only
+// stop issuing. kCluster: acquire at cluster scope, for a barrier that the other CTA's
+// threads arrive on after writing what they hand over.
+template <bool kCluster>
+__device__ __forceinline__ uint32_t wait_live(uint32_t live, uint32_t bar, uint32_t parity, volatile int* abort, uint32_t peer_flag) {
+  auto poll = [&]() {
     uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if (*abort || global_timer_ns() - t0 > kWaitTimeoutNs) return false;
-  }
+    if (kCluster)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(done)
+          : "r"(bar), "r"(parity)
+          : "memory");
+    else done = mbar_try_wait(bar, parity) ? 1u : 0u;
+    return __all_sync(0xffffffffu, done != 0) != 0;
+  };
+  if (poll()) return live;
+  if (!live) return 0;
+  const uint64_t t0 = global_timer_ns();
+  while (!poll())
+    if (__any_sync(0xffffffffu, *abort != 0 || global_timer_ns() - t0 > kWaitTimeoutNs)) {
+      pair_abort(abort, peer_flag);
+      return 0;
+    }
+  return live;
 }
 
 __device__ __forceinline__ void fp8_tile_coords(const Fp8GemmArgs& g, int tile, int& mb, int& nb) {
@@ -119,36 +170,39 @@ __device__ __forceinline__ void fp8_tile_coords(const Fp8GemmArgs& g, int tile, 
   }
 }
 
+template <int kHalves>
 __global__ void __launch_bounds__(kF8Threads, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmOut, const Fp8GemmArgs g) {
+  using S = F8Stage<kHalves>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
-  auto st_a = [&](int s) { return base + static_cast<uint32_t>(s * kF8StageBytes); };
-  auto st_b = [&](int s) { return base + static_cast<uint32_t>(s * kF8StageBytes + kF8ABytes); };
-  constexpr int kOutOff = kF8Stages * kF8StageBytes;
+  // K block h of stage s: the CTA's rows of A, then its columns of B for each half
+  auto st_a = [&](int s, int h) { return base + static_cast<uint32_t>(s * S::kBytes + h * S::kBlockBytes); };
+  auto st_b = [&](int s, int h, int half) { return st_a(s, h) + static_cast<uint32_t>(kF8ABytes + half * kF8BBytes); };
+  constexpr int kOutOff = kF8RingBytes;
   constexpr int kSfOff = kOutOff + kF8EpiWarps * kF8StgBytes;
   const uint32_t sOut = base + kOutOff, sSf = base + kSfOff;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kSfOff + kF8SfSlots * kF8SfBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kSfOff + kF8SfRingBytes);
   const uint32_t bar0 = smem_u32(bars);
   // full[S] | empty[S] | sffull[F] | sfempty[F] | tfull[2] | tempty[2] | done
-  const uint32_t full0 = bar0, empty0 = full0 + 8u * kF8Stages;
-  const uint32_t sffull0 = empty0 + 8u * kF8Stages, sfempty0 = sffull0 + 8u * kF8SfSlots;
-  const uint32_t tfull0 = sfempty0 + 8u * kF8SfSlots, tempty0 = tfull0 + 16u, done_bar = tempty0 + 16u;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kF8Stages + 2 * kF8SfSlots + 5);
+  const uint32_t full0 = bar0, empty0 = full0 + 8u * S::kCount;
+  const uint32_t sffull0 = empty0 + 8u * S::kCount, sfempty0 = sffull0 + 8u * S::kSfSlots;
+  const uint32_t tfull0 = sfempty0 + 8u * S::kSfSlots, tempty0 = tfull0 + 16u, done_bar = tempty0 + 16u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S::kCount + 2 * S::kSfSlots + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // warp-uniform
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kF8Stages; ++s) {
+    for (int s = 0; s < S::kCount; ++s) {
       mbar_init(full0 + 8u * s, 1);
       mbar_init(empty0 + 8u * s, 1);
     }
-    for (int s = 0; s < kF8SfSlots; ++s) {
+    for (int s = 0; s < S::kSfSlots; ++s) {
       mbar_init(sffull0 + 8u * s, 2);    // the scale warps of both CTAs
       mbar_init(sfempty0 + 8u * s, 1);
     }
@@ -170,117 +224,173 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   tc_fence_before_sync();
   cluster_sync();   // barriers of both CTAs initialised, TMEM allocated in both
   tc_fence_after_sync();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = __reduce_or_sync(0xffffffffu, *tmem_slot);   // the same in every lane: a uniform register
   const uint32_t peer_abort = map_to_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
   const int num_tiles = g.num_m_blocks * g.num_n_blocks;
   const int num_k_groups = (g.num_k_blocks + 3) >> 2;
   const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  const int n_tile = kHalves * g.n_half;
 
   if (warp == 0) {
     // ------------------------------------------------------------- TMA producer (both CTAs)
-    if (lane == 0) {
-      const uint32_t full_leader0 = map_to_rank(full0, 0);
-      const int half_n = g.n_tile >> 1;
-      const uint32_t pair_bytes = 2u * static_cast<uint32_t>(kF8ABytes + half_n * 128);
-      int s = 0;
-      uint32_t ph = 0;
-      long long issued = 0;
-      bool ok = true;
-      for (int tile = cluster; tile < num_tiles && ok; tile += nclusters) {
-        int mb, nb;
-        fp8_tile_coords(g, tile, mb, nb);
-        const int m0 = mb * 256 + 128 * static_cast<int>(rank);
-        const int n0 = nb * g.n_tile + half_n * static_cast<int>(rank);
-        for (int kb = 0; kb < g.num_k_blocks; ++kb) {
-          if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb = full_leader0 + 8u * s;
-          if (leader) mbar_arrive_expect_tx(full0 + 8u * s, pair_bytes);
-          tma_load_2d_pair(st_a(s), &tmA, fb, kb * 128, m0);
-          tma_load_2d_pair(st_b(s), &tmB, fb, kb * 128, n0);
-          ++issued;
-          if (++s == kF8Stages) {
-            s = 0;
-            ph ^= 1u;
-          }
+    const uint32_t full_leader0 = __reduce_or_sync(0xffffffffu, map_to_rank(full0, 0));
+    const int my_n = g.n_half >> 1;   // columns of each half that this CTA loads
+    const uint32_t block_bytes = 2u * static_cast<uint32_t>(kF8ABytes + kHalves * my_n * 128);   // of both CTAs
+    uint32_t live = 1;   // 0 after a wait gave up: the loops run out without issuing or waiting
+    int s = 0;
+    uint32_t ph = 0;
+    uint32_t issued = 0;
+    for (int tile = cluster; tile < num_tiles; tile += nclusters) {
+      int mb, nb;
+      fp8_tile_coords(g, tile, mb, nb);
+      const int m0 = mb * 256 + 128 * static_cast<int>(rank);
+      const int n0 = nb * n_tile + my_n * static_cast<int>(rank);
+      for (int kb = 0; kb < g.num_k_blocks; kb += S::kBlocks) {
+        live = wait_live<false>(live, empty0 + 8u * s, ph ^ 1u, abort_flag, peer_abort);
+        const uint32_t fb = full_leader0 + 8u * s;
+        const bool both = S::kBlocks == 2 && kb + 1 < g.num_k_blocks;
+        if (elect_one() && live) {
+          if (leader) mbar_arrive_expect_tx(full0 + 8u * s, both ? 2 * block_bytes : block_bytes);
+#pragma unroll
+          for (int h = 0; h < S::kBlocks; ++h)
+            if (h == 0 || both) {
+              tma_load_2d_pair(st_a(s, h), &tmA, fb, (kb + h) * 128, m0);
+#pragma unroll
+              for (int half = 0; half < kHalves; ++half)
+                tma_load_2d_pair(st_b(s, h, half), &tmB, fb, (kb + h) * 128, n0 + half * g.n_half);
+            }
+        }
+        issued += live;
+        if (++s == S::kCount) {
+          s = 0;
+          ph ^= 1u;
         }
       }
-      if (!ok) {
-        pair_abort(abort_flag, peer_abort);
-        atomicOr(&g_device_status, DEV_ST_TIMEOUT_PRODUCER);
-        if (leader) {   // the leader's full barriers count both CTAs' copies: drain them
-          const long long first = issued > kF8Stages ? issued - kF8Stages : 0;
-          for (long long i = first; i < issued; ++i)
-            if (!mbar_wait_plain(full0 + 8u * static_cast<uint32_t>(i % kF8Stages), static_cast<uint32_t>((i / kF8Stages) & 1)))
-              atomicOr(&g_device_status, DEV_ST_TIMEOUT_DRAIN);
-        }
+    }
+    if (!live && elect_one()) {
+      atomicOr(&g_device_status, DEV_ST_TIMEOUT_PRODUCER);
+      // the leader's full barriers count both CTAs' copies: drain the last ring of them
+      if (leader) {
+        const uint32_t first = issued > S::kCount ? issued - S::kCount : 0;
+        for (uint32_t i = first; i < issued; ++i)
+          if (!mbar_wait_plain(full0 + 8u * (i % S::kCount), (i / S::kCount) & 1u)) atomicOr(&g_device_status, DEV_ST_TIMEOUT_DRAIN);
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA issuer (leader only)
-    if (lane == 0 && leader) {
-      const uint32_t idesc0 = make_idesc_mxf8(g.a_e5m2, g.b_e5m2, g.n_tile, 256, 0);
-      int s = 0, f = 0;
+    if (leader) {
+      const uint32_t idesc0 = make_idesc_mxf8(g.a_e5m2, g.b_e5m2, g.n_half, 256, 0);
+      const bool wide = g.n_half > 128;
+      uint32_t live = 1;         // 0 after a wait gave up: the loops run out without issuing or waiting
+      int s = 0, f = 0;          // next stage and scale slot
       uint32_t ph = 0, fph = 0;
-      int local = 0;
-      bool ok = true;
-      for (int tile = cluster; tile < num_tiles && ok; tile += nclusters, ++local) {
-        const int buf = local & 1;
-        const uint32_t tph = static_cast<uint32_t>(local >> 1) & 1u;
-        if (!mbar_wait(tempty0 + 8u * buf, tph ^ 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
+      uint32_t col = 0;          // TMEM column of the current scales
+      // scales of the next four K blocks to TMEM
+      auto scales = [&]() {
+        live = wait_live<true>(live, sffull0 + 8u * f, fph, abort_flag, peer_abort);
         tc_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * kF8MaxN);
-        uint32_t sfa = 0;
-        for (int kb = 0; kb < g.num_k_blocks; ++kb) {
-          if ((kb & 3) == 0) {   // the scales of the next four K blocks
-            if (!mbar_wait_cluster(sffull0 + 8u * f, fph, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
-            sfa = tmem_base + kF8SfCol0 + 16u * static_cast<uint32_t>(f);
-            const uint32_t src = sSf + static_cast<uint32_t>(f * kF8SfBytes);
-            tc_cp_32x128b_pair(sfa, make_sf_desc(src));
-            tc_cp_32x128b_pair(sfa + 4u, make_sf_desc(src + 512u));
-            if (g.n_tile > 128) tc_cp_32x128b_pair(sfa + 8u, make_sf_desc(src + 1024u));
-            tc_commit_pair(sfempty0 + 8u * f);
-            if (++f == kF8SfSlots) {
-              f = 0;
-              fph ^= 1u;
-            }
-          }
-          if (!mbar_wait(full0 + 8u * s, ph, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          const uint32_t a_base = st_a(s), b_base = st_b(s);
-          const uint32_t id = static_cast<uint32_t>(kb & 3);
-          const uint32_t idesc = idesc0 | id << 4 | id << 29;
+        col = tmem_base + kF8SfCol0 + static_cast<uint32_t>(4 * S::kSfGroups * f);
+        const uint32_t src = sSf + static_cast<uint32_t>(f * S::kSfGroups * 512);
+        if (elect_one() && live) {
+          tc_cp_32x128b_pair(col, make_sf_desc(src));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_mxf8_pair(d_tmem, make_sw128_desc(a_base + kk * 32, 16, 1024), make_sw128_desc(b_base + kk * 32, 16, 1024),
-                             idesc, sfa, sfa + 4u, (kb | kk) != 0 ? 1u : 0u);
-          tc_commit_pair(empty0 + 8u * s);
-          if (++s == kF8Stages) {
-            s = 0;
-            ph ^= 1u;
+          for (int half = 0; half < kHalves; ++half) {
+            tc_cp_32x128b_pair(col + 4u + 8u * half, make_sf_desc(src + 512u + 1024u * half));
+            if (wide) tc_cp_32x128b_pair(col + 8u + 8u * half, make_sf_desc(src + 1024u + 1024u * half));
           }
+          tc_commit_pair(sfempty0 + 8u * f);
         }
-        if (!ok) break;
-        tc_commit_pair(tfull0 + 8u * buf);
+        if (++f == S::kSfSlots) {
+          f = 0;
+          fph ^= 1u;
+        }
+      };
+      // four MMAs of K block kb, in block h of stage st, on accumulator buf (one lane)
+      auto block = [&](int st, int h, int half, int buf, int kb) {
+        const uint64_t ad = make_sw128_desc(st_a(st, h), 16, 1024), bd = make_sw128_desc(st_b(st, h, half), 16, 1024);
+        const uint32_t id = static_cast<uint32_t>(kb & 3);
+        const uint32_t idesc = idesc0 | id << 4 | id << 29;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)   // 32 bytes of K further inside the swizzled row: 2 in the address field
+          tc_mma_mxf8_pair(tmem_base + static_cast<uint32_t>(buf * kF8MaxN), ad + 2u * kk, bd + 2u * kk, idesc, col,
+                           col + 4u + 8u * half, (kb | kk) != 0 ? 1u : 0u);
+      };
+      auto next_stage = [&]() {
+        if (++s == S::kCount) {
+          s = 0;
+          ph ^= 1u;
+        }
+      };
+      uint32_t tph = 1;   // phase of the accumulators' buffers
+      for (int tile = cluster, local = 0; tile < num_tiles; tile += nclusters, ++local) {
+        if constexpr (kHalves == 1) {
+          const int buf = local & 1;
+          live = wait_live<false>(live, tempty0 + 8u * buf, tph, abort_flag, peer_abort);
+          tc_fence_after_sync();
+          for (int kb = 0; kb < g.num_k_blocks; kb += 2) {
+            if ((kb & 3) == 0) scales();
+            live = wait_live<false>(live, full0 + 8u * s, ph, abort_flag, peer_abort);
+            tc_fence_after_sync();
+            if (elect_one() && live) {
+              block(s, 0, 0, buf, kb);
+              if (kb + 1 < g.num_k_blocks) block(s, 1, 0, buf, kb + 1);
+              tc_commit_pair(empty0 + 8u * s);
+              if (kb + 2 >= g.num_k_blocks) tc_commit_pair(tfull0 + 8u * buf);
+            }
+            next_stage();
+          }
+          tph ^= static_cast<uint32_t>(buf);
+        } else {
+          // the first K blocks (at most a ring of them, one scale group) on half 0, then on half 1
+          const int lead = min(S::kCount, g.num_k_blocks);
+          live = wait_live<false>(live, tempty0, tph, abort_flag, peer_abort);
+          scales();
+          int st = s;
+          uint32_t sph = ph;
+          for (int kb = 0; kb < lead; ++kb) {
+            live = wait_live<false>(live, full0 + 8u * st, sph, abort_flag, peer_abort);
+            tc_fence_after_sync();
+            if (elect_one() && live) {
+              block(st, 0, 0, 0, kb);
+              if (kb == g.num_k_blocks - 1) tc_commit_pair(tfull0);
+            }
+            if (++st == S::kCount) {
+              st = 0;
+              sph ^= 1u;
+            }
+          }
+          live = wait_live<false>(live, tempty0 + 8u, tph, abort_flag, peer_abort);
+          tc_fence_after_sync();
+          for (int kb = 0; kb < lead; ++kb) {
+            if (elect_one() && live) {
+              block(s, 0, 1, 1, kb);
+              tc_commit_pair(empty0 + 8u * s);
+              if (kb == g.num_k_blocks - 1) tc_commit_pair(tfull0 + 8u);
+            }
+            next_stage();
+          }
+          for (int kb = lead; kb < g.num_k_blocks; ++kb) {
+            if ((kb & 3) == 0) scales();
+            live = wait_live<false>(live, full0 + 8u * s, ph, abort_flag, peer_abort);
+            tc_fence_after_sync();
+            if (elect_one() && live) {
+              const bool end = kb == g.num_k_blocks - 1;
+              block(s, 0, 0, 0, kb);
+              if (end) tc_commit_pair(tfull0);
+              block(s, 0, 1, 1, kb);
+              tc_commit_pair(empty0 + 8u * s);
+              if (end) tc_commit_pair(tfull0 + 8u);
+            }
+            next_stage();
+          }
+          tph ^= 1u;
+        }
       }
-      if (!ok) {
-        pair_abort(abort_flag, peer_abort);
-        atomicOr(&g_device_status, DEV_ST_TIMEOUT_MMA);
+      if (elect_one()) {
+        if (!live) atomicOr(&g_device_status, DEV_ST_TIMEOUT_MMA);
+        tc_commit_pair_local(done_bar);
+        if (!mbar_wait_plain(done_bar, 0)) atomicOr(&g_device_status, DEV_ST_TIMEOUT_DRAIN);
       }
-      tc_commit_pair_local(done_bar);
-      if (!mbar_wait_plain(done_bar, 0)) atomicOr(&g_device_status, DEV_ST_TIMEOUT_DRAIN);
     }
   } else if (warp == kF8SfWarp) {
     // ------------------------------------------------------------- scale warp (both CTAs)
@@ -288,35 +398,43 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     int f = 0;
     uint32_t fph = 0;
     bool ok = true;
-    for (int tile = cluster; tile < num_tiles && ok; tile += nclusters) {
+    uint32_t w[4 * S::kSfGroups];
+    auto load = [&](int tile, int kg) {   // rows past the operands' ends (zero codes) get scale byte 0
       int mb, nb;
       fp8_tile_coords(g, tile, mb, nb);
-      const int m0 = mb * 256 + 128 * static_cast<int>(rank), n0 = nb * g.n_tile;
-      for (int kg = 0; kg < num_k_groups; ++kg) {
-        const uint32_t* pa = g.sa + static_cast<int64_t>(kg) * g.M;
-        const uint32_t* pb = g.sb + static_cast<int64_t>(kg) * g.N;
-        uint32_t w[12];
+      const int m0 = mb * 256 + 128 * static_cast<int>(rank) + lane, n0 = nb * n_tile + lane;
+      const uint32_t* pa = g.sa + static_cast<int64_t>(kg) * g.M;
+      const uint32_t* pb = g.sb + static_cast<int64_t>(kg) * g.N;
 #pragma unroll
-        for (int c = 0; c < 12; ++c) {   // rows past the operands' ends (zero codes) get scale byte 0
-          const int r = c < 4 ? m0 + 32 * c + lane : n0 + 32 * (c - 4) + lane;
-          w[c] = 0;
-          if (c < 4 ? r < g.M : (r < g.N && 32 * (c - 4) < g.n_tile)) w[c] = __ldg(c < 4 ? pa + r : pb + r);
-        }
+      for (int c = 0; c < 4; ++c) w[c] = m0 + 32 * c < g.M ? __ldg(pa + m0 + 32 * c) : 0u;
+#pragma unroll
+      for (int c = 0; c < 8 * kHalves; ++c) {
+        const int in_half = 32 * (c & 7), n = n0 + (c >> 3) * g.n_half + in_half;
+        w[4 + c] = in_half < g.n_half && n < g.N ? __ldg(pb + n) : 0u;
+      }
+    };
+    if (cluster < num_tiles) load(cluster, 0);
+    for (int tile = cluster; tile < num_tiles && ok; tile += nclusters) {
+      for (int kg = 0; kg < num_k_groups; ++kg) {
         const bool got = mbar_wait(sfempty0 + 8u * f, fph ^ 1u, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
-        const uint32_t dst = sSf + static_cast<uint32_t>(f * kF8SfBytes + lane * 16);
+        const uint32_t dst = sSf + static_cast<uint32_t>(f * S::kSfGroups * 512 + lane * 16);
 #pragma unroll
-        for (int j = 0; j < 3; ++j)
+        for (int j = 0; j < S::kSfGroups; ++j)
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512u * j), "r"(w[4 * j]), "r"(w[4 * j + 1]),
                        "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
                        : "memory");
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(sffull_leader0 + 8u * f);
-        if (++f == kF8SfSlots) {
+        // after the fence, which would wait for them: the next group's words travel while
+        // this warp waits for a free slot
+        if (kg + 1 < num_k_groups) load(tile, kg + 1);
+        else if (tile + nclusters < num_tiles) load(tile + nclusters, 0);
+        if (++f == S::kSfSlots) {
           f = 0;
           fph ^= 1u;
         }
@@ -328,69 +446,80 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     }
   } else {
     // ------------------------------------------------------------- epilogue (8 warps, both CTAs)
-    // two warps per TMEM lane quarter, each half of the tile's 32-column pieces: TMEM ->
-    // registers -> staging (swizzled by the store's tensor map) -> TMA store
+    // two warps per TMEM lane quarter, each half of an accumulator's 32-column pieces:
+    // TMEM -> registers -> staging (swizzled by the store's tensor map) -> TMA store
     const int e = warp - 2;
     const int quad = warp & 3;
-    const int pieces = g.n_tile >> 5;
+    const int pieces = g.n_half >> 5;
     const int first = (e >> 2) ? (pieces + 1) >> 1 : 0, last = (e >> 2) ? pieces : (pieces + 1) >> 1;
-    const uint32_t stg = sOut + static_cast<uint32_t>(e * kF8StgBytes);
+    const uint32_t stg0 = sOut + static_cast<uint32_t>(e * kF8StgBytes);
     const uint32_t tempty_leader0 = map_to_rank(tempty0, 0);
     int cnt = 0;
-    int local = 0;
+    int unit = 0;   // accumulators so far: unit u is in buffer u & 1
     bool ok = true;
-    for (int tile = cluster; tile < num_tiles; tile += nclusters, ++local) {
-      const int buf = local & 1;
-      const uint32_t tph = static_cast<uint32_t>(local >> 1) & 1u;
+    for (int tile = cluster; tile < num_tiles && ok; tile += nclusters) {
       int mb, nb;
       fp8_tile_coords(g, tile, mb, nb);
-      const int row0 = mb * 256 + 128 * static_cast<int>(rank) + quad * 32, n0 = nb * g.n_tile;
-      const bool got = mbar_wait(tfull0 + 8u * buf, tph, abort_flag);
-      if (!__all_sync(0xffffffffu, got)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after_sync();
-      const uint32_t t_row = tmem_base + static_cast<uint32_t>(buf * kF8MaxN) + (static_cast<uint32_t>(quad * 32) << 16);
+      const int row0 = mb * 256 + 128 * static_cast<int>(rank) + quad * 32;
 #pragma unroll 1
-      for (int c = first; c < last; ++c, ++cnt) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(c * 32), r);
-        if (cnt >= 1) {
-          if (lane == 0) bulk_wait_group_read<0>();   // the previous store has finished reading the buffer
-          __syncwarp();
+      for (int half = 0; half < kHalves; ++half, ++unit) {
+        const int buf = unit & 1;
+        const int n0 = nb * n_tile + half * g.n_half;
+        const bool got = mbar_wait(tfull0 + 8u * buf, static_cast<uint32_t>(unit >> 1) & 1u, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
         }
+        tc_fence_after_sync();
+        // all of the warp's columns to registers at once, so that the accumulator is free
+        // again after one TMEM latency, not after the conversion and the stores
+        const uint32_t t_row = tmem_base + static_cast<uint32_t>(buf * kF8MaxN + first * 32) + (static_cast<uint32_t>(quad * 32) << 16);
+        uint32_t r[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (first + i < last) tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(i * 32), r[i]);
         tmem_ld_wait();
-        if (g.out_f32) {   // 128-byte rows, 128B swizzle: chunk j at j ^ (row & 7)
-          const uint32_t row_addr = stg + static_cast<uint32_t>(lane) * 128u;
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8u * buf);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_addr + static_cast<uint32_t>((j ^ (lane & 7)) * 16)),
-                         "r"(r[4 * j]), "r"(r[4 * j + 1]), "r"(r[4 * j + 2]), "r"(r[4 * j + 3])
-                         : "memory");
-        } else {           // 64-byte rows, 64B swizzle: chunk j at j ^ ((row >> 1) & 3)
-          const uint32_t row_addr = stg + static_cast<uint32_t>(lane) * 64u;
+        for (int i = 0; i < 4; ++i) {
+          if (first + i >= last) break;
+          const int col = n0 + (first + i) * 32;
+          if (lane == 0) {   // the buffer's previous store has finished reading it
+            if (g.out_f32) bulk_wait_group_read<0>();
+            else bulk_wait_group_read<1>();
+          }
+          __syncwarp();
+          const uint32_t stg = g.out_f32 ? stg0 : stg0 + static_cast<uint32_t>((cnt++ & 1) * 2048);
+          if (g.out_f32) {   // 128-byte rows, 128B swizzle: chunk j at j ^ (row & 7)
+            const uint32_t row_addr = stg + static_cast<uint32_t>(lane) * 128u;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t w[4];
+            for (int j = 0; j < 8; ++j)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_addr + static_cast<uint32_t>((j ^ (lane & 7)) * 16)),
+                           "r"(r[i][4 * j]), "r"(r[i][4 * j + 1]), "r"(r[i][4 * j + 2]), "r"(r[i][4 * j + 3])
+                           : "memory");
+          } else {           // 64-byte rows, 64B swizzle: chunk j at j ^ ((row >> 1) & 3)
+            const uint32_t row_addr = stg + static_cast<uint32_t>(lane) * 64u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = pack_bf16x2(__uint_as_float(r[8 * j + 2 * i]), __uint_as_float(r[8 * j + 2 * i + 1]));
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_addr + static_cast<uint32_t>((j ^ ((lane >> 1) & 3)) * 16)),
-                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                         : "memory");
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                w[q] = pack_bf16x2(__uint_as_float(r[i][8 * j + 2 * q]), __uint_as_float(r[i][8 * j + 2 * q + 1]));
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_addr + static_cast<uint32_t>((j ^ ((lane >> 1) & 3)) * 16)),
+                           "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                           : "memory");
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (col < g.N) tma_store_2d(&tmOut, stg, col, row0);
+            bulk_commit_group();
           }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(&tmOut, stg, n0 + c * 32, row0);
-          bulk_commit_group();
-        }
       }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8u * buf);
     }
     if (!ok && lane == 0) {
       pair_abort(abort_flag, peer_abort);

@@ -7,6 +7,41 @@ namespace {
 
 inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
+// Launch configuration of a kernel on clusters of two CTAs.
+void pair_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int threads, size_t smem, cudaStream_t st) {
+  cfg = cudaLaunchConfig_t{};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+}
+
+// Once per device: the kernel's shared-memory limit and how many of its CTA pairs fit.
+template <class K>
+bl_status pair_setup(PerDeviceSetup& setup, K kern, int threads, size_t smem, int* pairs) {
+  if (bl_status s = per_device_setup(setup, pairs, [&](int* r) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(head)");
+        cudaLaunchConfig_t probe;
+        cudaLaunchAttribute attr[1];
+        pair_config(probe, attr, threads, smem, nullptr);
+        probe.gridDim = dim3(2 * (device_sm_count() / 2));
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, kern, &probe);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters(head)");
+        *r = n > 0 ? n : 0;
+        return BL_OK;
+      }))
+    return s;
+  if (*pairs <= 0) return fail(BL_ERR_CUDA, "no CTA pair of this kernel fits on this device");
+  return BL_OK;
+}
+
 // ------------------------------------------------------------------ 8-bit float linear
 
 bl_status check_fp8_format(int f, const char* what) {
@@ -39,64 +74,44 @@ struct Fp8Operand {
   int e5m2;
 };
 
-// Width of the pair product's tiles: the multiple of 32 with the least modelled time. Per
-// 128 of K a tile costs the larger of its MMAs (2 cycles a column) and its operand loads
-// (128 + n / 2 rows of 128 bytes a CTA at 64 bytes a cycle), so narrow tiles pay for the
-// 256 rows of A they drag along; whole waves of tiles over the pairs decide.
-int fp8_tile_width(int64_t m, int64_t n, int64_t k_blocks, int pairs) {
+// Tiles of the pair product: one or two accumulators of a multiple of 32 columns, whichever
+// has the least modelled time. Per 128 of K a tile costs the larger of its MMAs (2 cycles
+// a column) and its operand loads (128 rows of A and half its columns of B, 128 bytes each,
+// at about 40 bytes a cycle), so narrow tiles pay for the rows of A that they drag along;
+// whole waves of tiles over the pairs decide.
+struct Fp8Tiles {
+  int halves, n_half;
+};
+Fp8Tiles fp8_tiles(int64_t m, int64_t n, int64_t k_blocks, int pairs) {
   const int64_t mb = (m + 255) / 256;
-  int best = 32;
-  double best_cost = 0;
-  for (int w = 32; w <= bl::kF8MaxN; w += 32) {
-    const int64_t tiles = mb * ((n + w - 1) / w);
-    const int64_t waves = (tiles + pairs - 1) / pairs;
-    const double cost = double(waves) * (double(k_blocks) * (256 + w) + 1500.0);
-    if (w == 32 || cost <= best_cost) {
-      best = w;
-      best_cost = cost;
+  Fp8Tiles best{1, 32};
+  double best_cost = 1e300;
+  for (int halves = 1; halves <= 2; ++halves)
+    for (int w = 32; w <= bl::kF8MaxN; w += 32) {
+      const int64_t cols = int64_t(halves) * w;
+      const int64_t waves = (mb * ((n + cols - 1) / cols) + pairs - 1) / pairs;
+      const double mma = 2.0 * cols, load = (128 + cols / 2) * 128.0 / 40.0;
+      const double cost = double(waves) * (double(k_blocks) * (mma > load ? mma : load) + 1500.0);
+      if (cost <= best_cost) {
+        best = {halves, w};
+        best_cost = cost;
+      }
     }
-  }
   return best;
 }
 
-// out[m, n] = A B^T with both operands' reduction of length k (codes [rows, k], k % 16 == 0).
-bl_status enqueue_fp8_gemm(const Fp8Operand& A, const Fp8Operand& B, int64_t k, void* out, bool f32, cudaStream_t st) {
-  constexpr size_t smem = bl::gemm_fp8_smem_bytes();
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(bl::kF8Threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  static PerDeviceSetup setup;
-  int max_clusters = 0;
-  if (bl_status s = per_device_setup(setup, &max_clusters, [&](int* r) {
-        cudaError_t e = cudaFuncSetAttribute(bl::gemm_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(fp8 gemm)");
-        cudaLaunchConfig_t probe = cfg;
-        probe.gridDim = dim3(2 * (device_sm_count() / 2));
-        int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, bl::gemm_fp8_kernel, &probe);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters(fp8 gemm)");
-        *r = n > 0 ? n : 0;
-        return BL_OK;
-      }))
-    return s;
-  if (max_clusters <= 0) return fail(BL_ERR_CUDA, "no CTA pair of the 8-bit float product fits on this device");
+template <int kHalves>
+bl_status launch_fp8_gemm(const Fp8Operand& A, const Fp8Operand& B, int64_t k, void* out, bool f32, int n_half,
+                          int max_clusters, cudaStream_t st) {
   bl::Fp8GemmArgs g{};
   g.sa = reinterpret_cast<const uint32_t*>(A.scales);
   g.sb = reinterpret_cast<const uint32_t*>(B.scales);
   g.M = static_cast<int>(A.rows);
   g.N = static_cast<int>(B.rows);
+  g.n_half = n_half;
   g.num_k_blocks = static_cast<int>((k + 127) / 128);
-  g.n_tile = fp8_tile_width(A.rows, B.rows, g.num_k_blocks, max_clusters);
   g.num_m_blocks = static_cast<int>((A.rows + 255) / 256);
-  g.num_n_blocks = static_cast<int>((B.rows + g.n_tile - 1) / g.n_tile);
+  g.num_n_blocks = static_cast<int>((B.rows + kHalves * n_half - 1) / (kHalves * n_half));
   g.a_e5m2 = A.e5m2;
   g.b_e5m2 = B.e5m2;
   g.out_f32 = f32 ? 1 : 0;
@@ -107,15 +122,29 @@ bl_status enqueue_fp8_gemm(const Fp8Operand& A, const Fp8Operand& B, int64_t k, 
   if (tiles > INT32_MAX) return fail(BL_ERR_UNSUPPORTED_SHAPE, "too much work in one call");
   CUtensorMap ta, tb, to;
   if (bl_status s = make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A.q, k, A.rows, 128, 128)) return s;
-  if (bl_status s = make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B.q, k, B.rows, 128, g.n_tile / 2)) return s;
+  if (bl_status s = make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B.q, k, B.rows, 128, n_half / 2)) return s;
   if (bl_status s = make_map_strided(&to, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                                      f32 ? 4 : 2, out, B.rows, A.rows, B.rows, 32, 32,
                                      f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
     return s;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  pair_config(cfg, attr, bl::kF8Threads, bl::gemm_fp8_smem_bytes(), st);
   cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < max_clusters ? tiles : max_clusters));
-  cudaError_t e = cudaLaunchKernelEx(&cfg, bl::gemm_fp8_kernel, ta, tb, to, g);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, bl::gemm_fp8_kernel<kHalves>, ta, tb, to, g);
   if (e != cudaSuccess) return cuda_fail(e, "fp8 gemm launch");
   return BL_OK;
+}
+
+// out[m, n] = A B^T with both operands' reduction of length k (codes [rows, k], k % 16 == 0).
+bl_status enqueue_fp8_gemm(const Fp8Operand& A, const Fp8Operand& B, int64_t k, void* out, bool f32, cudaStream_t st) {
+  static PerDeviceSetup setup[2];
+  int pairs = 0, pairs2 = 0;
+  if (bl_status s = pair_setup(setup[0], bl::gemm_fp8_kernel<1>, bl::kF8Threads, bl::gemm_fp8_smem_bytes(), &pairs)) return s;
+  if (bl_status s = pair_setup(setup[1], bl::gemm_fp8_kernel<2>, bl::kF8Threads, bl::gemm_fp8_smem_bytes(), &pairs2)) return s;
+  const Fp8Tiles tiles = fp8_tiles(A.rows, B.rows, (k + 127) / 128, pairs);
+  return tiles.halves == 2 ? launch_fp8_gemm<2>(A, B, k, out, f32, tiles.n_half, pairs2, st)
+                           : launch_fp8_gemm<1>(A, B, k, out, f32, tiles.n_half, pairs, st);
 }
 
 // Tokens up to which the streaming product runs instead of the pair product, and up to
@@ -167,32 +196,9 @@ bl_status check_ce(int64_t t, int64_t k_in, int64_t v) {
 
 bl_status launch_ce(bl::CeGroup& G, cudaStream_t st) {
   constexpr size_t smem = bl::gemm2_smem_bytes();
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(bl::kGemmThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   static PerDeviceSetup setup;
   int max_clusters = 0;
-  if (bl_status s = per_device_setup(setup, &max_clusters, [&](int* r) {
-        cudaError_t e = cudaFuncSetAttribute(bl::ce_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear ce)");
-        cudaLaunchConfig_t probe = cfg;
-        probe.gridDim = dim3(2 * (device_sm_count() / 2));
-        int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, bl::ce_gemm_kernel, &probe);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters(linear ce)");
-        *r = n > 0 ? n : 0;
-        return BL_OK;
-      }))
-    return s;
-  if (max_clusters <= 0) return fail(BL_ERR_CUDA, "no CTA pair of the linear cross entropy fits on this device");
+  if (bl_status s = pair_setup(setup, bl::ce_gemm_kernel, bl::kGemmThreads, smem, &max_clusters)) return s;
   int64_t tiles = 0;
   for (int i = 0; i < G.count; ++i) {
     G.p[i].tile_begin = static_cast<int>(tiles);
@@ -200,6 +206,9 @@ bl_status launch_ce(bl::CeGroup& G, cudaStream_t st) {
     if (tiles > INT32_MAX) return fail(BL_ERR_UNSUPPORTED_SHAPE, "too much work in one call");
   }
   G.total_tiles = static_cast<int>(tiles);
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  pair_config(cfg, attr, bl::kGemmThreads, smem, st);
   cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < max_clusters ? tiles : max_clusters));
   cudaError_t e = cudaLaunchKernelEx(&cfg, bl::ce_gemm_kernel, G);
   if (e != cudaSuccess) return cuda_fail(e, "linear ce launch");
