@@ -36,7 +36,7 @@
 // Every wait is bounded. No load uses multicast.
 #pragma once
 
-#include "gemm_tc2.cuh"
+#include "pair_issue.cuh"
 
 namespace bl {
 
@@ -95,22 +95,6 @@ struct Fp8GemmArgs {
 __device__ __forceinline__ uint32_t make_idesc_mxf8(uint32_t a_fmt, uint32_t b_fmt, uint32_t n, uint32_t m, uint32_t sf_id) {
   return (sf_id << 4) | (a_fmt << 7) | (b_fmt << 10) | ((n >> 3) << 17) | (1u << 23) | ((m >> 4) << 24) | (sf_id << 29);
 }
-// One lane of a converged warp, always the same one. The MMA and producer warps run their
-// loops with all 32 lanes and branch on this only around the instructions themselves: from
-// such a branch the compiler issues them with descriptors and addresses kept in uniform
-// registers, where they take them. Measured (8192 tokens, eight MMAs): 300 cycles to issue;
-// 570 by a lane chosen once and a predicate on each instruction, 670 from a branch on that
-// lane, which made the issuing warp slower than the tensor cores (11008 -> 2048: 171 us
-// against 145).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t on;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(on));
-  return on != 0;
-}
 __device__ __forceinline__ void tc_mma_mxf8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                  uint32_t sfa, uint32_t sfb, uint32_t acc) {
   asm volatile(
@@ -129,37 +113,6 @@ __device__ __forceinline__ uint64_t make_sf_desc(uint32_t saddr) {   // 8-row co
   return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(1) << 16 |
          static_cast<uint64_t>(128 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
 }
-// Wait of a whole warp, bounded like mbar_wait. `live` is 0 once a wait has given up, and
-// every later wait returns at once; the first to give up raises the pair's abort flags. The
-// loops around it do not branch on the outcome (their trip counts stay uniform), they only
-// stop issuing. kCluster: acquire at cluster scope, for a barrier that the other CTA's
-// threads arrive on after writing what they hand over.
-template <bool kCluster>
-__device__ __forceinline__ uint32_t wait_live(uint32_t live, uint32_t bar, uint32_t parity, volatile int* abort, uint32_t peer_flag) {
-  auto poll = [&]() {
-    uint32_t done;
-    if (kCluster)
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(done)
-          : "r"(bar), "r"(parity)
-          : "memory");
-    else done = mbar_try_wait(bar, parity) ? 1u : 0u;
-    return __all_sync(0xffffffffu, done != 0) != 0;
-  };
-  if (poll()) return live;
-  if (!live) return 0;
-  const uint64_t t0 = global_timer_ns();
-  while (!poll())
-    if (__any_sync(0xffffffffu, *abort != 0 || global_timer_ns() - t0 > kWaitTimeoutNs)) {
-      pair_abort(abort, peer_flag);
-      return 0;
-    }
-  return live;
-}
-
 __device__ __forceinline__ void fp8_tile_coords(const Fp8GemmArgs& g, int tile, int& mb, int& nb) {
   if (g.m_fastest) {
     mb = tile % g.num_m_blocks;

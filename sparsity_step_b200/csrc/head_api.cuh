@@ -171,14 +171,16 @@ size_t fp8_scale_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>(
 
 // ------------------------------------------------------------------ linear cross entropy
 
-constexpr int64_t kCePieceBytes = int64_t(64) << 20;   // dl of one piece of the vocabulary
+constexpr int64_t kCePieceBytes = int64_t(128) << 20;   // dl of one piece of the vocabulary
 
-// Vocabulary rows per piece of the backward pass: a multiple of 256.
+// Vocabulary rows per piece of the backward pass: all of them while dl fits kCePieceBytes,
+// else a multiple of 256, a quarter of the vocabulary at most, so that the two pieces held
+// at a time stay well below the logits.
 int64_t ce_piece(int64_t t, int64_t v) {
-  int64_t p = kCePieceBytes / (2 * (t > 0 ? t : 1)) / 256 * 256;
-  if (p < 1024) p = 1024;
-  const int64_t all = round_up(v, 256);
-  return p < all ? p : all;
+  const int64_t all = round_up(v, 256), fit = kCePieceBytes / (2 * (t > 0 ? t : 1)) / 256 * 256;
+  if (fit >= all) return all;
+  const int64_t quarter = round_up((v + 3) / 4, 256), p = fit < quarter ? fit : quarter;
+  return p < 1024 ? (all < 1024 ? all : 1024) : p;
 }
 
 // Shapes of the head's operators: those of every entry point, with tokens up to 2^30 (the
@@ -232,11 +234,10 @@ void ce_shape(bl::CeProblem& P, int mode, int64_t m, int64_t n, int64_t k, bool 
   P.M = static_cast<int>(m);
   P.N = static_cast<int>(n);
   P.num_k_blocks = static_cast<int>((k + 63) / 64);
+  P.part_blocks = mode == bl::CE_LSE ? bl::kCePartBlocks : (P.num_k_blocks + 1) / 2 * 2;
   P.num_m_blocks = static_cast<int>((m + 255) / 256);
   P.num_n_blocks = static_cast<int>((n + 255) / 256);
-  bl::GemmArgs order{};
-  set_raster(order, 2.0 * double(m) * double(k), 2.0 * double(n) * double(k));
-  P.m_fastest = order.m_fastest;
+  P.m_fastest = m <= n ? 1 : 0;   // the smaller operand stays in L2 while the other streams by once
 }
 
 // Layout of the workspaces (every part 256-byte aligned).
@@ -252,13 +253,16 @@ CeFwdSpace ce_fwd_space(int64_t t, int64_t v) {
   return s;
 }
 struct CeBwdSpace {
-  size_t dl, acc, total;
+  size_t grad_max, dl[2], acc, total;
 };
 CeBwdSpace ce_bwd_space(int64_t t, int64_t k_in, int64_t v, bool want_grad_x) {
   CeBwdSpace s{};
   const int64_t piece = ce_piece(t, v);
-  s.dl = 0;
-  s.acc = round256(static_cast<size_t>(t) * static_cast<size_t>(piece) * 2);
+  const size_t bytes = round256(static_cast<size_t>(t) * static_cast<size_t>(piece) * 2);
+  s.grad_max = 0;
+  s.dl[0] = 256;
+  s.dl[1] = s.dl[0] + (piece < v ? bytes : 0);   // the next piece's dl is written while this one's is read
+  s.acc = s.dl[1] + bytes;
   s.total = s.acc + (want_grad_x && piece < v ? round256(static_cast<size_t>(t) * static_cast<size_t>(k_in) * 4) : 0);
   return s;
 }
@@ -462,44 +466,56 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
   const CeBwdSpace sp = ce_bwd_space(t, k_in, v, grad_x != nullptr);
   if (!workspace || workspace_bytes < sp.total)
     return fail(BL_ERR_WORKSPACE, "workspace too small: %zu < %zu", workspace ? workspace_bytes : size_t(0), sp.total);
-  uint8_t* dl = static_cast<uint8_t*>(workspace) + sp.dl;
-  float* acc = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.acc);
+  uint8_t* space = static_cast<uint8_t*>(workspace);
+  float* grad_max = reinterpret_cast<float*>(space + sp.grad_max);
+  float* acc = reinterpret_cast<float*>(space + sp.acc);
   const int64_t piece = ce_piece(t, v);
-  const bool one = piece >= v;   // a single piece: grad_X needs no fp32 sum in memory
+  const int64_t pieces = (v + piece - 1) / piece;
+  const bool one = pieces == 1;   // a single piece: grad_X needs no fp32 sum in memory
+  bl::ce_grad_max_kernel<<<1, 1024, 0, st>>>(grad_loss, targets, t, v, grad_max);
+  cudaError_t launched = cudaGetLastError();
+  if (launched != cudaSuccess) return cuda_fail(launched, "linear ce grad max launch");
   bl::CeGroup G{};
   G.v = v;
   G.targets = targets;
   G.lse = lse;
   G.grad = grad_loss;
-  for (int64_t v0 = 0; v0 < v; v0 += piece) {
-    const int64_t n = v - v0 < piece ? v - v0 : piece;
-    const uint16_t* wp = w + v0 * k_in;
-    {   // dl of the piece [t, n], row stride `piece`
-      bl::CeProblem& P = G.p[0];
-      G.count = 1;
+  G.grad_max = grad_max;
+  // launch i: the two products of piece i - 1 and dl of piece i
+  for (int64_t i = 0; i <= pieces; ++i) {
+    G.count = 0;
+    if (i > 0) {
+      const int64_t v0 = (i - 1) * piece, n = v - v0 < piece ? v - v0 : piece;
+      const uint8_t* dl = space + sp.dl[(i - 1) & 1];
+      bl::CeProblem *px = nullptr, *pw = nullptr;
+      const bool w_first = t >= n;   // the deeper product's tiles go first
+      if (grad_w && w_first) pw = &G.p[G.count++];
+      if (grad_x) px = &G.p[G.count++];
+      if (grad_w && !w_first) pw = &G.p[G.count++];
+      if (px) {
+        ce_shape(*px, one ? bl::CE_BF16 : i == 1 ? bl::CE_PART : bl::CE_ADD_PART, t, k_in, n, false, true);
+        if (bl_status s = ce_operand(&px->tmA, dl, n, t, piece, false)) return s;
+        if (bl_status s = ce_operand(&px->tmB, w + v0 * k_in, k_in, n, k_in, true)) return s;
+        if (bl_status s = one ? ce_output(&px->tmOut, grad_x, t, k_in, k_in, false)
+                              : ce_output(&px->tmOut, acc, t, k_in, k_in, true))
+          return s;
+      }
+      if (pw) {
+        ce_shape(*pw, w32 ? bl::CE_F32 : bl::CE_BF16, n, k_in, t, true, true);
+        if (bl_status s = ce_operand(&pw->tmA, dl, n, t, piece, true)) return s;
+        if (bl_status s = ce_operand(&pw->tmB, x, k_in, t, k_in, true)) return s;
+        if (bl_status s = ce_output(&pw->tmOut, static_cast<uint8_t*>(grad_w) + v0 * k_in * (w32 ? 4 : 2), n, k_in, k_in, w32))
+          return s;
+      }
+    }
+    if (i < pieces) {   // dl of the piece [t, n], row stride `piece`
+      const int64_t v0 = i * piece, n = v - v0 < piece ? v - v0 : piece;
+      bl::CeProblem& P = G.p[G.count++];
       ce_shape(P, bl::CE_DLOGITS, t, n, k_in, false, false);
       P.v0 = static_cast<int>(v0);
       if (bl_status s = ce_operand(&P.tmA, x, k_in, t, k_in, false)) return s;
-      if (bl_status s = ce_operand(&P.tmB, wp, k_in, n, k_in, false)) return s;
-      if (bl_status s = ce_output(&P.tmOut, dl, t, n, piece, false)) return s;
-      if (bl_status s = launch_ce(G, st)) return s;
-    }
-    G.count = 0;
-    if (grad_x) {
-      bl::CeProblem& P = G.p[G.count++];
-      ce_shape(P, one ? bl::CE_BF16 : v0 == 0 ? bl::CE_F32 : bl::CE_ADD_F32, t, k_in, n, false, true);
-      if (bl_status s = ce_operand(&P.tmA, dl, n, t, piece, false)) return s;
-      if (bl_status s = ce_operand(&P.tmB, wp, k_in, n, k_in, true)) return s;
-      if (bl_status s = one ? ce_output(&P.tmOut, grad_x, t, k_in, k_in, false) : ce_output(&P.tmOut, acc, t, k_in, k_in, true))
-        return s;
-    }
-    if (grad_w) {
-      bl::CeProblem& P = G.p[G.count++];
-      ce_shape(P, w32 ? bl::CE_F32 : bl::CE_BF16, n, k_in, t, true, true);
-      if (bl_status s = ce_operand(&P.tmA, dl, n, t, piece, true)) return s;
-      if (bl_status s = ce_operand(&P.tmB, x, k_in, t, k_in, true)) return s;
-      if (bl_status s = ce_output(&P.tmOut, static_cast<uint8_t*>(grad_w) + v0 * k_in * (w32 ? 4 : 2), n, k_in, k_in, w32))
-        return s;
+      if (bl_status s = ce_operand(&P.tmB, w + v0 * k_in, k_in, n, k_in, false)) return s;
+      if (bl_status s = ce_output(&P.tmOut, space + sp.dl[i & 1], t, n, piece, false)) return s;
     }
     if (bl_status s = launch_ce(G, st)) return s;
   }
@@ -509,7 +525,7 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
     const int64_t cap = int64_t(device_sm_count()) * 16;
     if (grid > cap) grid = cap;
     bl::ce_round_kernel<<<static_cast<unsigned>(grid), 256, 0, st>>>(reinterpret_cast<const float4*>(acc), n8,
-                                                                    reinterpret_cast<uint4*>(grad_x));
+                                                                    grad_max, reinterpret_cast<uint4*>(grad_x));
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "linear ce round launch");
   }

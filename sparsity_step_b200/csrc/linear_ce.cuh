@@ -5,32 +5,41 @@
 //   dl[t, v] = (exp(l[t, v] - lse_t) - [v = y_t]) * g_t     g_t = d(total) / d(loss_t)
 //   grad_X = dl W,  grad_W = dl^T X
 //
-// Forward: one pass of the CTA-pair product of gemm_tc2.cuh whose epilogue reduces each
-// 128-column strip of logits in registers to its maximum and its sum of exponentials (fp32,
-// the logits never rounded), so a token leaves 8 bytes per 128 columns of the vocabulary
-// instead of 512; a small kernel joins the strips in a fixed order.
+// Forward: one pass of a CTA-pair product whose epilogue reduces each 128-column strip of
+// logits in registers to its maximum and its sum of exponentials (fp32, the logits never
+// rounded), so a token leaves 8 bytes per 128 columns of the vocabulary instead of 512; a
+// small kernel joins the strips in a fixed order. The tensor core's accumulator drops the
+// bits of an addend below its own last one, always towards zero: over K = 2048 the logits
+// came out 4e-6 too small. So the accumulator starts afresh every 256 of K and the parts
+// are added in registers, rounded to nearest (1e-7 to 5e-7 at any K).
 // Backward, one piece of the vocabulary after another: the logits of the piece are computed
 // again, their epilogue writes dl of the piece in bf16 (the operand type of the tensor
 // cores: one rounding of at most half a step per factor), and two products consume it,
 // grad_W of the piece's rows and the piece's addend of grad_X, summed in fp32. Four
-// products of 2 T V K operations in all against three with all logits kept (T x V).
-// Bound by the bf16 tensor pipe; W's stream (2 bytes per weight) for few tokens.
+// products of 2 T V K operations in all against three with all logits kept (T x V). g is
+// divided by its largest magnitude before that rounding and the gradients multiplied by it
+// after: with the usual constant g, dl of a target is then p - 1 itself, not a product whose
+// rounding error every token would share.
+// Bound by the bf16 tensor pipe (and the power it draws).
 //
 // The kernel takes up to three products with their own operand orders, depths and
-// epilogues in one launch (their tiles numbered consecutively), so that the products of a
-// piece fill the SMs together. Synchronisation, stages and TMEM use as in gemm_tc2.cuh.
+// epilogues in one launch (their tiles numbered consecutively, the deepest first), so that
+// the two products of one piece and the logits of the next fill the SMs together.
+// Synchronisation and TMEM use as in gemm_tc2.cuh; a stage holds two K blocks (64 KB, three
+// stages), since its waits and commit cost the issuing warp as much as one MMA.
 #pragma once
 
-#include "gemm_tc2.cuh"
+#include "pair_issue.cuh"
 
 namespace bl {
 
 enum CeMode : int {
   CE_LSE = 0,       // strip maxima and sums of exponentials, and the target's logit
   CE_DLOGITS = 1,   // dl in bf16
-  CE_BF16 = 2,      // the product, bf16
-  CE_F32 = 3,       // the product, fp32
-  CE_ADD_F32 = 4,   // the product added to fp32 memory
+  CE_BF16 = 2,      // the product times the largest |g|, bf16
+  CE_F32 = 3,       // the product times the largest |g|, fp32
+  CE_PART = 4,      // the product, fp32
+  CE_ADD_PART = 5,  // the product added to fp32 memory
 };
 
 struct CeProblem {
@@ -39,6 +48,7 @@ struct CeProblem {
   int a_mn, b_mn;                // operand order: 0 K-major, 1 MN-major
   int M, N;
   int num_k_blocks;              // ceil(K / 64)
+  int part_blocks;               // K blocks per accumulation in TMEM (even)
   int num_m_blocks, num_n_blocks;   // 256 x 256 tiles
   int m_fastest;
   int tile_begin;
@@ -52,6 +62,7 @@ struct CeGroup {
   const int64_t* targets;        // [T]
   const float* lse;              // [T]  (CE_DLOGITS)
   const float* grad;             // [T]  (CE_DLOGITS)
+  const float* grad_max;         // largest |grad| of the tokens with a loss
   float2* strips;                // [2 * n blocks, T] (max, sum)  (CE_LSE)
   float* target_logit;           // [T]  (CE_LSE)
 };
@@ -91,105 +102,129 @@ __device__ __forceinline__ void ce_tile(const CeProblem& P, int tile, int& mb, i
   }
 }
 
-// Epilogue of 32 rows x 128 columns of logits: one strip of one token per thread.
-__device__ __forceinline__ void ce_strip(const CeGroup& G, const CeProblem& P, uint32_t t_row, int row, int n0, int strip) {
-  float m = -INFINITY, s = 0.f;   // m in units of log2
-  const bool row_ok = row < P.M;
-  const int64_t rel = row_ok ? G.targets[row] - n0 : -1;
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t r[32];
-    tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(c * 32), r);
-    tmem_ld_wait();
-    const int left = P.N - n0 - c * 32;   // columns of the vocabulary in this piece
-    if (left <= 0) break;
-    if (left < 32) {
+constexpr int kCeStages = 3;
+constexpr int kCeStageBytes = 2 * kStage2Bytes;       // two K blocks
+constexpr int kCePartBlocks = 4;                      // 256 of K per accumulation of the logits
+static_assert(kCeStages * kCeStageBytes == kStages2 * kStage2Bytes, "the ring of gemm_tc2.cuh");
+
+// The accumulator's 32 rows x 128 columns of one warp: thread = row, acc[c][j] = column 32 c + j.
+using CeAcc = float[4][32];
+
+// One strip of one token per thread.
+__device__ __forceinline__ void ce_strip(const CeGroup& G, const CeProblem& P, CeAcc& acc, int row, int n0, int strip) {
+  const int left = P.N - n0;   // columns of the vocabulary in the strip
+  if (row >= P.M) return;
+  const int64_t hit = G.targets[row] - n0;
+  if (hit >= 0 && hit < 128 && hit < left) {
+    float t = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (j >= left) r[j] = 0xFF800000u;
-    }
-    const int64_t hit = rel - c * 32;
-    if (hit >= 0 && hit < 32 && hit < left) {
-      float t = 0.f;
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j == static_cast<int>(hit)) t = __uint_as_float(r[j]);
-      G.target_logit[row] = t;
-    }
-    float cm[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) cm[j] = __uint_as_float(r[j]);
-#pragma unroll
-    for (int j = 4; j < 32; ++j) cm[j & 3] = fmaxf(cm[j & 3], __uint_as_float(r[j]));
-    const float m2 = fmaxf(m, fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3])) * kLog2e);
-    float a[4] = {s * ex2(m - m2), 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < 32; ++j) a[j & 3] += ex2(fmaf(__uint_as_float(r[j]), kLog2e, -m2));
-    s = (a[0] + a[1]) + (a[2] + a[3]);
-    m = m2;
+        if (32 * c + j == static_cast<int>(hit)) t = acc[c][j];
+    G.target_logit[row] = t;
   }
-  if (row_ok) G.strips[static_cast<int64_t>(strip) * P.M + row] = make_float2(m, s);
+  if (left < 128) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (32 * c + j >= left) acc[c][j] = -INFINITY;
+  }
+  float m[4], s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    m[c] = acc[c][0];
+#pragma unroll
+    for (int j = 1; j < 32; ++j) m[c] = fmaxf(m[c], acc[c][j]);
+  }
+  const float m2 = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * kLog2e;   // in units of log2
+  if (left > 0) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(acc[c][j], kLog2e, -m2));
+  }
+  G.strips[static_cast<int64_t>(strip) * P.M + row] = make_float2(m2, (s[0] + s[1]) + (s[2] + s[3]));
 }
 
-// Epilogue of 32 rows x 128 columns through shared memory: dl, or the product itself.
-__device__ __forceinline__ void ce_store(const CeGroup& G, const CeProblem& P, uint32_t t_row, uint32_t stg, int& cnt, int row0,
-                                         int n0, int lane) {
-  const bool f32 = P.mode >= CE_F32;
-  const int cols = f32 ? 32 : 64;
-  float lse2 = 0.f, grad = 0.f;
-  int64_t rel = -1;
-  if (P.mode == CE_DLOGITS && row0 + lane < P.M) {
-    const int64_t y = G.targets[row0 + lane];
-    if (y >= 0 && y < G.v) {
-      grad = G.grad[row0 + lane];
-      lse2 = G.lse[row0 + lane] * kLog2e;
-      rel = y - P.v0 - n0;
+// 32 rows x 128 columns through shared memory: dl, or the product itself.
+__device__ __forceinline__ void ce_store(const CeGroup& G, const CeProblem& P, CeAcc& acc, uint32_t stg, int row0, int n0,
+                                         int lane) {
+  if (P.mode == CE_DLOGITS) {
+    float lse2 = 0.f, g = 0.f;
+    int64_t hit = -1;
+    if (row0 + lane < P.M) {
+      const int64_t y = G.targets[row0 + lane];
+      if (y >= 0 && y < G.v) {
+        g = G.grad[row0 + lane];
+        if (g != 0.f) g = __fdiv_rn(g, *G.grad_max);
+        lse2 = G.lse[row0 + lane] * kLog2e;
+        hit = y - P.v0 - n0;
+      }
     }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) acc[c][j] = ex2(fmaf(acc[c][j], kLog2e, -lse2));
+    if (hit >= 0 && hit < 128) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (32 * c + j == static_cast<int>(hit)) acc[c][j] -= 1.f;
+    }
+    // a token without a loss has no gradient, whatever its logits are
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) acc[c][j] = g == 0.f ? 0.f : acc[c][j] * g;
+  } else if (P.mode <= CE_F32) {
+    const float scale = *G.grad_max;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) acc[c][j] *= scale;
   }
-#pragma unroll 1
-  for (int c = 0; c < 128; c += cols, ++cnt) {
-    uint32_t w[32];   // the 128 bytes of this thread's row
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h == 1 && f32) break;
-      uint32_t r[32];
-      tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(c + 32 * h), r);
-      tmem_ld_wait();
-      if (P.mode == CE_DLOGITS) {
-        const int64_t hit = rel - c - 32 * h;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(ex2(fmaf(__uint_as_float(r[j]), kLog2e, -lse2)));
-        if (hit >= 0 && hit < 32) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j == static_cast<int>(hit)) r[j] = __float_as_uint(__uint_as_float(r[j]) - 1.f);
-        }
-        // a token without a loss has no gradient, whatever its logits are
-#pragma unroll
-        for (int j = 0; j < 32; ++j) r[j] = grad == 0.f ? 0u : __float_as_uint(__uint_as_float(r[j]) * grad);
-      }
-      if (f32) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) w[j] = r[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) w[16 * h + j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-      }
-    }
-    if (cnt >= 1) {
-      if (lane == 0) bulk_wait_group_read<0>();   // the previous store has finished reading the buffer
-      __syncwarp();
-    }
-    const uint32_t row_addr = stg + static_cast<uint32_t>(lane) * 128u;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      st_shared_v4(row_addr + static_cast<uint32_t>((j ^ (lane & 7)) * 16), w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  const uint32_t row_addr = stg + static_cast<uint32_t>(lane) * 128u;
+  auto put = [&](int j, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {   // 128B swizzle
+    st_shared_v4(row_addr + static_cast<uint32_t>((j ^ (lane & 7)) * 16), a, b, c, d);
+  };
+  auto free_buffer = [&]() {   // the previous store has finished reading the buffer
+    if (lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+  };
+  auto store = [&](int col) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      if (P.mode == CE_ADD_F32) tma_add_2d(&P.tmOut, stg, n0 + c, row0);
-      else tma_store_2d(&P.tmOut, stg, n0 + c, row0);
+      if (n0 + col < P.N) {
+        if (P.mode == CE_ADD_PART) tma_add_2d(&P.tmOut, stg, n0 + col, row0);
+        else tma_store_2d(&P.tmOut, stg, n0 + col, row0);
+      }
       bulk_commit_group();
+    }
+  };
+  if (P.mode >= CE_F32) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      free_buffer();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        put(j, __float_as_uint(acc[c][4 * j]), __float_as_uint(acc[c][4 * j + 1]), __float_as_uint(acc[c][4 * j + 2]),
+            __float_as_uint(acc[c][4 * j + 3]));
+      store(32 * c);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      free_buffer();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float* f = &acc[2 * h + (j >> 2)][8 * (j & 3)];
+        put(j, pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+      }
+      store(64 * h);
     }
   }
 }
@@ -199,21 +234,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
-  const uint32_t sA = base;
-  const uint32_t sB = base + kStages2 * kAHalfBytes;
-  const uint32_t sOut = base + kStages2 * kStage2Bytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages2 * kStage2Bytes + kOutStagingBytes);
+  // K block h of stage s: this CTA's 128 rows of A, then of B
+  auto st_a = [&](int s, int h) { return base + static_cast<uint32_t>(s * kCeStageBytes + h * kStage2Bytes); };
+  auto st_b = [&](int s, int h) { return st_a(s, h) + kAHalfBytes; };
+  const uint32_t sOut = base + kCeStages * kCeStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kCeStages * kCeStageBytes + kOutStagingBytes);
   const uint32_t bar0 = smem_u32(bars);
-  const uint32_t full0 = bar0, empty0 = bar0 + 8u * kStages2;
-  const uint32_t tfull0 = bar0 + 16u * kStages2, tempty0 = tfull0 + 16u, done_bar = tempty0 + 16u;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages2 + 5);
+  const uint32_t full0 = bar0, empty0 = bar0 + 8u * kCeStages;
+  const uint32_t tfull0 = bar0 + 16u * kCeStages, tempty0 = tfull0 + 16u, done_bar = tempty0 + 16u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kCeStages + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // warp-uniform
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages2; ++s) {
+    for (int s = 0; s < kCeStages; ++s) {
       mbar_init(full0 + 8u * s, 1);
       mbar_init(empty0 + 8u * s, 1);
     }
@@ -237,114 +273,111 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
   tc_fence_before_sync();
   cluster_sync();   // barriers of both CTAs initialised, TMEM allocated in both
   tc_fence_after_sync();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = __reduce_or_sync(0xffffffffu, *tmem_slot);   // the same in every lane: a uniform register
   const uint32_t peer_abort = map_to_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
   const int num_tiles = G.total_tiles;
   const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
 
   if (warp == 0) {
     // ------------------------------------------------------------- TMA producer (both CTAs)
-    if (lane == 0) {
-      const uint32_t full_leader0 = map_to_rank(full0, 0);
-      int s = 0;
-      uint32_t ph = 0;
-      long long issued = 0;
-      bool ok = true;
-      int local = 0;
-      for (int tile = cluster; tile < num_tiles && ok; tile += nclusters, ++local) {
-        const CeProblem& P = G.p[ce_problem(G, tile)];
-        int mb, nb;
-        ce_tile(P, tile - P.tile_begin, mb, nb);
-        const int m0 = mb * 256 + 128 * static_cast<int>(rank);
-        const int n0 = nb * 256 + 128 * static_cast<int>(rank);
-        for (int kq = 0; kq < P.num_k_blocks; ++kq) {
-          const int kb = (local & 1) ? P.num_k_blocks - 1 - kq : kq;   // serpentine K order
-          if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb = full_leader0 + 8u * s;
-          if (leader) mbar_arrive_expect_tx(full0 + 8u * s, 2 * kStage2Bytes);
-          const uint32_t a_dst = sA + s * kAHalfBytes, b_dst = sB + s * kBHalfBytes;
-          const int kc = kb * 64;
-          if (P.a_mn) {
-            tma_load_2d_pair(a_dst, &P.tmA, fb, m0, kc);
-            tma_load_2d_pair(a_dst + 8192, &P.tmA, fb, m0 + 64, kc);
-          } else {
-            tma_load_2d_pair(a_dst, &P.tmA, fb, kc, m0);
-          }
-          if (P.b_mn) {
-            tma_load_2d_pair(b_dst, &P.tmB, fb, n0, kc);
-            tma_load_2d_pair(b_dst + 8192, &P.tmB, fb, n0 + 64, kc);
-          } else {
-            tma_load_2d_pair(b_dst, &P.tmB, fb, kc, n0);
-          }
-          ++issued;
-          if (++s == kStages2) {
-            s = 0;
-            ph ^= 1u;
-          }
+    const uint32_t full_leader0 = __reduce_or_sync(0xffffffffu, map_to_rank(full0, 0));
+    uint32_t live = 1;   // 0 after a wait gave up: the loops run out without issuing or waiting
+    int s = 0;
+    uint32_t ph = 0;
+    uint32_t issued = 0;
+    for (int tile = cluster; tile < num_tiles; tile += nclusters) {
+      const CeProblem& P = G.p[ce_problem(G, tile)];
+      int mb, nb;
+      ce_tile(P, tile - P.tile_begin, mb, nb);
+      const int m0 = mb * 256 + 128 * static_cast<int>(rank);
+      const int n0 = nb * 256 + 128 * static_cast<int>(rank);
+      for (int kb = 0; kb < P.num_k_blocks; kb += 2) {
+        live = wait_live<false>(live, empty0 + 8u * s, ph ^ 1u, abort_flag, peer_abort);
+        const uint32_t fb = full_leader0 + 8u * s;
+        const bool both = kb + 1 < P.num_k_blocks;
+        if (elect_one() && live) {
+          if (leader) mbar_arrive_expect_tx(full0 + 8u * s, both ? 2 * kCeStageBytes : kCeStageBytes);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (h == 0 || both) {
+              const int kc = (kb + h) * 64;
+              if (P.a_mn) {
+                tma_load_2d_pair(st_a(s, h), &P.tmA, fb, m0, kc);
+                tma_load_2d_pair(st_a(s, h) + 8192, &P.tmA, fb, m0 + 64, kc);
+              } else {
+                tma_load_2d_pair(st_a(s, h), &P.tmA, fb, kc, m0);
+              }
+              if (P.b_mn) {
+                tma_load_2d_pair(st_b(s, h), &P.tmB, fb, n0, kc);
+                tma_load_2d_pair(st_b(s, h) + 8192, &P.tmB, fb, n0 + 64, kc);
+              } else {
+                tma_load_2d_pair(st_b(s, h), &P.tmB, fb, kc, n0);
+              }
+            }
+        }
+        issued += live;
+        if (++s == kCeStages) {
+          s = 0;
+          ph ^= 1u;
         }
       }
-      if (!ok) {
-        pair_abort(abort_flag, peer_abort);
-        atomicOr(&g_device_status, DEV_ST_TIMEOUT_PRODUCER);
-        if (leader) {   // the leader's full barriers count both CTAs' copies: drain them
-          const long long first = issued > kStages2 ? issued - kStages2 : 0;
-          for (long long i = first; i < issued; ++i)
-            if (!mbar_wait_plain(full0 + 8u * static_cast<uint32_t>(i % kStages2), static_cast<uint32_t>((i / kStages2) & 1)))
-              atomicOr(&g_device_status, DEV_ST_TIMEOUT_DRAIN);
-        }
+    }
+    if (!live && elect_one()) {
+      atomicOr(&g_device_status, DEV_ST_TIMEOUT_PRODUCER);
+      // the leader's full barriers count both CTAs' copies: drain the last ring of them
+      if (leader) {
+        const uint32_t first = issued > kCeStages ? issued - kCeStages : 0;
+        for (uint32_t i = first; i < issued; ++i)
+          if (!mbar_wait_plain(full0 + 8u * (i % kCeStages), (i / kCeStages) & 1u)) atomicOr(&g_device_status, DEV_ST_TIMEOUT_DRAIN);
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA issuer (leader only)
-    if (lane == 0 && leader) {
+    if (leader) {
+      uint32_t live = 1;
       int s = 0;
       uint32_t ph = 0;
-      int local = 0;
-      bool ok = true;
-      for (int tile = cluster; tile < num_tiles && ok; tile += nclusters, ++local) {
+      uint32_t unit = 0;   // accumulations so far: unit u is in buffer u & 1
+      for (int tile = cluster; tile < num_tiles; tile += nclusters) {
         const CeProblem& P = G.p[ce_problem(G, tile)];
         const uint32_t idesc = make_idesc(1u, 1u, 1u, P.a_mn, P.b_mn, 256, 256);
-        // K-major: a K step of 16 is 32 B inside the swizzled row; MN-major: 16 K rows = 2 KB
-        const uint32_t a_step = P.a_mn ? 2048u : 32u, b_step = P.b_mn ? 2048u : 32u;
+        // a K step of 16 in the address field (16-byte units): K-major 32 B inside the
+        // swizzled row, MN-major 16 K rows = 2 KB
+        const uint64_t a_step = P.a_mn ? 128u : 2u, b_step = P.b_mn ? 128u : 2u;
         const uint32_t a_lbo = P.a_mn ? 8192u : 16u, b_lbo = P.b_mn ? 8192u : 16u;
-        const int buf = local & 1;
-        const uint32_t tph = static_cast<uint32_t>(local >> 1) & 1u;
-        if (!mbar_wait(tempty0 + 8u * buf, tph ^ 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * kBN);
-        const int nk = P.num_k_blocks;
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!mbar_wait(full0 + 8u * s, ph, abort_flag)) {
-            ok = false;
-            break;
-          }
+        for (int k0 = 0; k0 < P.num_k_blocks; k0 += P.part_blocks, ++unit) {
+          const uint32_t buf = unit & 1u;
+          const int end = min(k0 + P.part_blocks, P.num_k_blocks);
+          live = wait_live<false>(live, tempty0 + 8u * buf, ((unit >> 1) & 1u) ^ 1u, abort_flag, peer_abort);
           tc_fence_after_sync();
-          const uint32_t a_base = sA + s * kAHalfBytes, b_base = sB + s * kBHalfBytes;
+          const uint32_t d_tmem = tmem_base + buf * kBN;
+          for (int kb = k0; kb < end; kb += 2) {
+            live = wait_live<false>(live, full0 + 8u * s, ph, abort_flag, peer_abort);
+            tc_fence_after_sync();
+            if (elect_one() && live) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_f16_pair(d_tmem, make_sw128_desc(a_base + kk * a_step, a_lbo, 1024),
-                            make_sw128_desc(b_base + kk * b_step, b_lbo, 1024), idesc, (kb | kk) != 0 ? 1u : 0u);
-          tc_commit_pair(empty0 + 8u * s);   // frees this stage in both CTAs
-          if (++s == kStages2) {
-            s = 0;
-            ph ^= 1u;
+              for (int h = 0; h < 2; ++h)
+                if (h == 0 || kb + 1 < end) {
+                  const uint64_t ad = make_sw128_desc(st_a(s, h), a_lbo, 1024), bd = make_sw128_desc(st_b(s, h), b_lbo, 1024);
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)
+                    tc_mma_f16_pair(d_tmem, ad + a_step * kk, bd + b_step * kk, idesc, kb > k0 || (h | kk) != 0 ? 1u : 0u);
+                }
+              tc_commit_pair(empty0 + 8u * s);   // frees this stage in both CTAs
+              if (kb + 2 >= end) tc_commit_pair(tfull0 + 8u * buf);   // both CTAs' accumulators complete
+            }
+            if (++s == kCeStages) {
+              s = 0;
+              ph ^= 1u;
+            }
           }
         }
-        if (!ok) break;
-        tc_commit_pair(tfull0 + 8u * buf);   // both CTAs' accumulators complete
       }
-      if (!ok) {
-        pair_abort(abort_flag, peer_abort);
-        atomicOr(&g_device_status, DEV_ST_TIMEOUT_MMA);
+      if (elect_one()) {
+        if (!live) atomicOr(&g_device_status, DEV_ST_TIMEOUT_MMA);
+        tc_commit_pair_local(done_bar);
+        if (!mbar_wait_plain(done_bar, 0)) atomicOr(&g_device_status, DEV_ST_TIMEOUT_DRAIN);
       }
-      tc_commit_pair_local(done_bar);
-      if (!mbar_wait_plain(done_bar, 0)) atomicOr(&g_device_status, DEV_ST_TIMEOUT_DRAIN);
     }
   } else {
     // ------------------------------------------------------------- epilogue (warps 2..9, both CTAs)
@@ -353,29 +386,47 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
     const int half = e >> 2;   // columns [128 half, 128 half + 128) of the tile
     const uint32_t stg = sOut + static_cast<uint32_t>(e * kStageOutBytes);
     const uint32_t tempty_leader0 = map_to_rank(tempty0, 0);
-    int cnt = 0;
-    int local = 0;
+    uint32_t unit = 0;
     bool ok = true;
-    for (int tile = cluster; tile < num_tiles; tile += nclusters, ++local) {
-      const int buf = local & 1;
-      const uint32_t tph = static_cast<uint32_t>(local >> 1) & 1u;
+    for (int tile = cluster; tile < num_tiles && ok; tile += nclusters) {
       const CeProblem& P = G.p[ce_problem(G, tile)];
       int mb, nb;
       ce_tile(P, tile - P.tile_begin, mb, nb);
       const int row0 = mb * 256 + 128 * static_cast<int>(rank) + quad * 32;
       const int n0 = nb * 256 + 128 * half;
-      const bool got = mbar_wait(tfull0 + 8u * buf, tph, abort_flag);
-      if (!__all_sync(0xffffffffu, got)) {
-        ok = false;
-        break;
+      CeAcc acc;
+#pragma unroll 1
+      for (int k0 = 0; k0 < P.num_k_blocks; k0 += P.part_blocks, ++unit) {
+        const uint32_t buf = unit & 1u;
+        const bool got = mbar_wait(tfull0 + 8u * buf, (unit >> 1) & 1u, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t t_row = tmem_base + buf * kBN + static_cast<uint32_t>(128 * half) + (static_cast<uint32_t>(quad * 32) << 16);
+        if (k0 == 0) {
+          uint32_t(&r)[4][32] = reinterpret_cast<uint32_t(&)[4][32]>(acc);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(c * 32), r[c]);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(c * 32), r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[c][j] += __uint_as_float(r[j]);
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8u * buf);   // the accumulator is free again
       }
-      tc_fence_after_sync();
-      const uint32_t t_row = tmem_base + static_cast<uint32_t>(buf * kBN + 128 * half) + (static_cast<uint32_t>(quad * 32) << 16);
-      if (P.mode == CE_LSE) ce_strip(G, P, t_row, row0 + lane, n0, nb * 2 + half);
-      else ce_store(G, P, t_row, stg, cnt, row0, n0, lane);
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8u * buf);
+      if (!ok) break;
+      if (P.mode == CE_LSE) ce_strip(G, P, acc, row0 + lane, n0, nb * 2 + half);
+      else ce_store(G, P, acc, stg, row0, n0, lane);
     }
     if (!ok && lane == 0) {
       pair_abort(abort_flag, peer_abort);
@@ -390,6 +441,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+// Largest |g| of the tokens that have a loss (0 if none): one block.
+__global__ void __launch_bounds__(1024) ce_grad_max_kernel(const float* grad, const int64_t* targets, int64_t t, int64_t v,
+                                                           float* out) {
+  __shared__ uint32_t s_max[32];
+  uint32_t m = 0;   // |g| as its bit pattern: a NaN is larger than every number and stays one
+  for (int64_t i = threadIdx.x; i < t; i += 1024) {
+    const int64_t y = targets[i];
+    if (y >= 0 && y < v) m = max(m, __float_as_uint(grad[i]) & 0x7FFFFFFFu);
+  }
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    m = __reduce_max_sync(0xFFFFFFFFu, s_max[threadIdx.x]);
+    if (threadIdx.x == 0) *out = __uint_as_float(m);
   }
 }
 
@@ -427,11 +496,13 @@ __global__ void __launch_bounds__(256) ce_join_kernel(const float2* strips, int 
   }
 }
 
-// fp32 -> bf16, 8 elements per thread and step.
-__global__ void __launch_bounds__(256) ce_round_kernel(const float4* src, int64_t n8, uint4* dst) {
+// The summed parts of grad_X times the largest |g|, bf16: 8 elements per thread and step.
+__global__ void __launch_bounds__(256) ce_round_kernel(const float4* src, int64_t n8, const float* scale, uint4* dst) {
+  const float f = *scale;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += static_cast<int64_t>(gridDim.x) * 256) {
     const float4 a = __ldg(src + 2 * i), b = __ldg(src + 2 * i + 1);
-    dst[i] = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+    dst[i] = make_uint4(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f), pack_bf16x2(b.x * f, b.y * f),
+                        pack_bf16x2(b.z * f, b.w * f));
   }
 }
 
