@@ -43,19 +43,16 @@ namespace bl {
 constexpr int kF8MaxN = 224;                              // columns of one accumulator
 constexpr int kF8ABytes = 128 * 128;                      // one K block (128 bytes) of the CTA's rows
 constexpr int kF8BBytes = kF8MaxN / 2 * 128;              // and of its columns of one accumulator
-// A stage: two K blocks of a narrow tile (3 x 60 KB), one of a wide tile (4 x 44 KB). Eight
-// MMAs each: a stage's wait and commit cost the issuing warp about 120 cycles (measured
-// with four MMAs a stage and no loads: 128 us against 109 us with eight).
+// A stage is one K block: six of 30 KB for narrow tiles, four of 44 KB for wide ones. (With
+// two K blocks a stage the refill came too late: the MMAs of two stages do not cover it.)
 template <int kHalves>
 struct F8Stage {
-  static constexpr int kCount = kHalves == 2 ? 4 : 3;
-  static constexpr int kBlocks = 3 - kHalves;             // K blocks of a stage
-  static constexpr int kBlockBytes = kF8ABytes + kHalves * kF8BBytes;
-  static constexpr int kBytes = kBlocks * kBlockBytes;
+  static constexpr int kCount = kHalves == 2 ? 4 : 6;
+    static constexpr int kBytes = kF8ABytes + kHalves * kF8BBytes;
   static constexpr int kSfGroups = 1 + 2 * kHalves;       // 128-row groups of scales: A, then B by halves
   static constexpr int kSfSlots = kHalves == 2 ? 3 : 4;
 };
-constexpr int kF8RingBytes = 3 * 2 * (kF8ABytes + kF8BBytes);   // 180 KB
+constexpr int kF8RingBytes = 6 * (kF8ABytes + kF8BBytes);   // 180 KB
 constexpr int kF8SfRingBytes = 3 * 5 * 512;
 constexpr int kF8EpiWarps = 8;
 constexpr int kF8SfWarp = 2 + kF8EpiWarps;
@@ -132,9 +129,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
-  // K block h of stage s: the CTA's rows of A, then its columns of B for each half
-  auto st_a = [&](int s, int h) { return base + static_cast<uint32_t>(s * S::kBytes + h * S::kBlockBytes); };
-  auto st_b = [&](int s, int h, int half) { return st_a(s, h) + static_cast<uint32_t>(kF8ABytes + half * kF8BBytes); };
+  // stage s: the CTA's rows of A, then its columns of B for each half
+  auto st_a = [&](int s) { return base + static_cast<uint32_t>(s * S::kBytes); };
+  auto st_b = [&](int s, int half) { return st_a(s) + static_cast<uint32_t>(kF8ABytes + half * kF8BBytes); };
   constexpr int kOutOff = kF8RingBytes;
   constexpr int kSfOff = kOutOff + kF8EpiWarps * kF8StgBytes;
   const uint32_t sOut = base + kOutOff, sSf = base + kSfOff;
@@ -188,7 +185,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     // ------------------------------------------------------------- TMA producer (both CTAs)
     const uint32_t full_leader0 = __reduce_or_sync(0xffffffffu, map_to_rank(full0, 0));
     const int my_n = g.n_half >> 1;   // columns of each half that this CTA loads
-    const uint32_t block_bytes = 2u * static_cast<uint32_t>(kF8ABytes + kHalves * my_n * 128);   // of both CTAs
+    const uint32_t stage_bytes = 2u * static_cast<uint32_t>(kF8ABytes + kHalves * my_n * 128);   // of both CTAs
     uint32_t live = 1;   // 0 after a wait gave up: the loops run out without issuing or waiting
     int s = 0;
     uint32_t ph = 0;
@@ -198,20 +195,15 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       fp8_tile_coords(g, tile, mb, nb);
       const int m0 = mb * 256 + 128 * static_cast<int>(rank);
       const int n0 = nb * n_tile + my_n * static_cast<int>(rank);
-      for (int kb = 0; kb < g.num_k_blocks; kb += S::kBlocks) {
+      for (int kb = 0; kb < g.num_k_blocks; ++kb) {
         live = wait_live<false>(live, empty0 + 8u * s, ph ^ 1u, abort_flag, peer_abort);
         const uint32_t fb = full_leader0 + 8u * s;
-        const bool both = S::kBlocks == 2 && kb + 1 < g.num_k_blocks;
         if (elect_one() && live) {
-          if (leader) mbar_arrive_expect_tx(full0 + 8u * s, both ? 2 * block_bytes : block_bytes);
+          if (leader) mbar_arrive_expect_tx(full0 + 8u * s, stage_bytes);
+          tma_load_2d_pair(st_a(s), &tmA, fb, kb * 128, m0);
 #pragma unroll
-          for (int h = 0; h < S::kBlocks; ++h)
-            if (h == 0 || both) {
-              tma_load_2d_pair(st_a(s, h), &tmA, fb, (kb + h) * 128, m0);
-#pragma unroll
-              for (int half = 0; half < kHalves; ++half)
-                tma_load_2d_pair(st_b(s, h, half), &tmB, fb, (kb + h) * 128, n0 + half * g.n_half);
-            }
+          for (int half = 0; half < kHalves; ++half)
+            tma_load_2d_pair(st_b(s, half), &tmB, fb, kb * 128, n0 + half * g.n_half);
         }
         issued += live;
         if (++s == S::kCount) {
@@ -258,9 +250,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           fph ^= 1u;
         }
       };
-      // four MMAs of K block kb, in block h of stage st, on accumulator buf (one lane)
-      auto block = [&](int st, int h, int half, int buf, int kb) {
-        const uint64_t ad = make_sw128_desc(st_a(st, h), 16, 1024), bd = make_sw128_desc(st_b(st, h, half), 16, 1024);
+      // four MMAs of K block kb, in stage st, on accumulator buf (one lane)
+      auto block = [&](int st, int half, int buf, int kb) {
+        const uint64_t ad = make_sw128_desc(st_a(st), 16, 1024), bd = make_sw128_desc(st_b(st, half), 16, 1024);
         const uint32_t id = static_cast<uint32_t>(kb & 3);
         const uint32_t idesc = idesc0 | id << 4 | id << 29;
 #pragma unroll
@@ -280,15 +272,14 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           const int buf = local & 1;
           live = wait_live<false>(live, tempty0 + 8u * buf, tph, abort_flag, peer_abort);
           tc_fence_after_sync();
-          for (int kb = 0; kb < g.num_k_blocks; kb += 2) {
+          for (int kb = 0; kb < g.num_k_blocks; ++kb) {
             if ((kb & 3) == 0) scales();
             live = wait_live<false>(live, full0 + 8u * s, ph, abort_flag, peer_abort);
             tc_fence_after_sync();
             if (elect_one() && live) {
-              block(s, 0, 0, buf, kb);
-              if (kb + 1 < g.num_k_blocks) block(s, 1, 0, buf, kb + 1);
+              block(s, 0, buf, kb);
               tc_commit_pair(empty0 + 8u * s);
-              if (kb + 2 >= g.num_k_blocks) tc_commit_pair(tfull0 + 8u * buf);
+              if (kb + 1 == g.num_k_blocks) tc_commit_pair(tfull0 + 8u * buf);
             }
             next_stage();
           }
@@ -304,7 +295,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             live = wait_live<false>(live, full0 + 8u * st, sph, abort_flag, peer_abort);
             tc_fence_after_sync();
             if (elect_one() && live) {
-              block(st, 0, 0, 0, kb);
+              block(st, 0, 0, kb);
               if (kb == g.num_k_blocks - 1) tc_commit_pair(tfull0);
             }
             if (++st == S::kCount) {
@@ -316,7 +307,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           tc_fence_after_sync();
           for (int kb = 0; kb < lead; ++kb) {
             if (elect_one() && live) {
-              block(s, 0, 1, 1, kb);
+              block(s, 1, 1, kb);
               tc_commit_pair(empty0 + 8u * s);
               if (kb == g.num_k_blocks - 1) tc_commit_pair(tfull0 + 8u);
             }
@@ -328,9 +319,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             tc_fence_after_sync();
             if (elect_one() && live) {
               const bool end = kb == g.num_k_blocks - 1;
-              block(s, 0, 0, 0, kb);
+              block(s, 0, 0, kb);
               if (end) tc_commit_pair(tfull0);
-              block(s, 0, 1, 1, kb);
+              block(s, 1, 1, kb);
               tc_commit_pair(empty0 + 8u * s);
               if (end) tc_commit_pair(tfull0 + 8u);
             }

@@ -171,16 +171,19 @@ size_t fp8_scale_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>(
 
 // ------------------------------------------------------------------ linear cross entropy
 
-constexpr int64_t kCePieceBytes = int64_t(128) << 20;   // dl of one piece of the vocabulary
+// dl of the whole vocabulary up to kCeWholeBytes, else of a piece of kCePieceBytes at most
+// (8192 x 2048 x 65536 backward: pieces of 32 MB 5.13 ms, 64 MB 5.00, 128 MB 4.55, 256 MB 4.61).
+constexpr int64_t kCeWholeBytes = int64_t(64) << 20, kCePieceBytes = int64_t(128) << 20;
 
-// Vocabulary rows per piece of the backward pass: all of them while dl fits kCePieceBytes,
-// else a multiple of 256, a quarter of the vocabulary at most, so that the two pieces held
-// at a time stay well below the logits.
+// Vocabulary rows per piece of the backward pass: all of them, or a multiple of 256 and a
+// quarter of the vocabulary at most, so that the two pieces held at a time stay well below
+// the logits.
 int64_t ce_piece(int64_t t, int64_t v) {
-  const int64_t all = round_up(v, 256), fit = kCePieceBytes / (2 * (t > 0 ? t : 1)) / 256 * 256;
-  if (fit >= all) return all;
-  const int64_t quarter = round_up((v + 3) / 4, 256), p = fit < quarter ? fit : quarter;
-  return p < 1024 ? (all < 1024 ? all : 1024) : p;
+  const int64_t all = round_up(v, 256), row = 2 * (t > 0 ? t : 1);
+  if (row * all <= kCeWholeBytes) return all;
+  const int64_t fit = kCePieceBytes / row / 256 * 256, quarter = round_up((v + 3) / 4, 256);
+  const int64_t p = fit < quarter ? fit : quarter;
+  return p >= 1024 ? p : all < 1024 ? all : 1024;
 }
 
 // Shapes of the head's operators: those of every entry point, with tokens up to 2^30 (the
@@ -234,7 +237,7 @@ void ce_shape(bl::CeProblem& P, int mode, int64_t m, int64_t n, int64_t k, bool 
   P.M = static_cast<int>(m);
   P.N = static_cast<int>(n);
   P.num_k_blocks = static_cast<int>((k + 63) / 64);
-  P.part_blocks = mode == bl::CE_LSE ? bl::kCePartBlocks : (P.num_k_blocks + 1) / 2 * 2;
+  P.part_blocks = mode == bl::CE_LSE ? bl::kCePartBlocks : P.num_k_blocks;
   P.num_m_blocks = static_cast<int>((m + 255) / 256);
   P.num_n_blocks = static_cast<int>((n + 255) / 256);
   P.m_fastest = m <= n ? 1 : 0;   // the smaller operand stays in L2 while the other streams by once

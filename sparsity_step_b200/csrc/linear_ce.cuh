@@ -10,8 +10,8 @@
 // rounded), so a token leaves 8 bytes per 128 columns of the vocabulary instead of 512; a
 // small kernel joins the strips in a fixed order. The tensor core's accumulator drops the
 // bits of an addend below its own last one, always towards zero: over K = 2048 the logits
-// came out 4e-6 too small. So the accumulator starts afresh every 256 of K and the parts
-// are added in registers, rounded to nearest (1e-7 to 5e-7 at any K).
+// came out 4e-6 too small. So the accumulator starts afresh every 512 of K and the parts
+// are added in registers, rounded to nearest, which stays below 1e-6 at any K.
 // Backward, one piece of the vocabulary after another: the logits of the piece are computed
 // again, their epilogue writes dl of the piece in bf16 (the operand type of the tensor
 // cores: one rounding of at most half a step per factor), and two products consume it,
@@ -25,8 +25,7 @@
 // The kernel takes up to three products with their own operand orders, depths and
 // epilogues in one launch (their tiles numbered consecutively, the deepest first), so that
 // the two products of one piece and the logits of the next fill the SMs together.
-// Synchronisation and TMEM use as in gemm_tc2.cuh; a stage holds two K blocks (64 KB, three
-// stages), since its waits and commit cost the issuing warp as much as one MMA.
+// Stages, synchronisation and TMEM use as in gemm_tc2.cuh.
 #pragma once
 
 #include "pair_issue.cuh"
@@ -48,7 +47,7 @@ struct CeProblem {
   int a_mn, b_mn;                // operand order: 0 K-major, 1 MN-major
   int M, N;
   int num_k_blocks;              // ceil(K / 64)
-  int part_blocks;               // K blocks per accumulation in TMEM (even)
+  int part_blocks;               // K blocks per accumulation in TMEM
   int num_m_blocks, num_n_blocks;   // 256 x 256 tiles
   int m_fastest;
   int tile_begin;
@@ -102,10 +101,7 @@ __device__ __forceinline__ void ce_tile(const CeProblem& P, int tile, int& mb, i
   }
 }
 
-constexpr int kCeStages = 3;
-constexpr int kCeStageBytes = 2 * kStage2Bytes;       // two K blocks
-constexpr int kCePartBlocks = 4;                      // 256 of K per accumulation of the logits
-static_assert(kCeStages * kCeStageBytes == kStages2 * kStage2Bytes, "the ring of gemm_tc2.cuh");
+constexpr int kCePartBlocks = 8;   // 512 of K per accumulation of the logits
 
 // The accumulator's 32 rows x 128 columns of one warp: thread = row, acc[c][j] = column 32 c + j.
 using CeAcc = float[4][32];
@@ -234,22 +230,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
-  // K block h of stage s: this CTA's 128 rows of A, then of B
-  auto st_a = [&](int s, int h) { return base + static_cast<uint32_t>(s * kCeStageBytes + h * kStage2Bytes); };
-  auto st_b = [&](int s, int h) { return st_a(s, h) + kAHalfBytes; };
-  const uint32_t sOut = base + kCeStages * kCeStageBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kCeStages * kCeStageBytes + kOutStagingBytes);
+  auto st_a = [&](int s) { return base + static_cast<uint32_t>(s * kStage2Bytes); };   // this CTA's 128 rows of A
+  auto st_b = [&](int s) { return st_a(s) + kAHalfBytes; };                           // and of B
+  const uint32_t sOut = base + kStages2 * kStage2Bytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages2 * kStage2Bytes + kOutStagingBytes);
   const uint32_t bar0 = smem_u32(bars);
-  const uint32_t full0 = bar0, empty0 = bar0 + 8u * kCeStages;
-  const uint32_t tfull0 = bar0 + 16u * kCeStages, tempty0 = tfull0 + 16u, done_bar = tempty0 + 16u;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kCeStages + 5);
+  const uint32_t full0 = bar0, empty0 = bar0 + 8u * kStages2;
+  const uint32_t tfull0 = bar0 + 16u * kStages2, tempty0 = tfull0 + 16u, done_bar = tempty0 + 16u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages2 + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // warp-uniform
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kCeStages; ++s) {
+    for (int s = 0; s < kStages2; ++s) {
       mbar_init(full0 + 8u * s, 1);
       mbar_init(empty0 + 8u * s, 1);
     }
@@ -291,32 +286,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
       ce_tile(P, tile - P.tile_begin, mb, nb);
       const int m0 = mb * 256 + 128 * static_cast<int>(rank);
       const int n0 = nb * 256 + 128 * static_cast<int>(rank);
-      for (int kb = 0; kb < P.num_k_blocks; kb += 2) {
+      for (int kb = 0; kb < P.num_k_blocks; ++kb) {
         live = wait_live<false>(live, empty0 + 8u * s, ph ^ 1u, abort_flag, peer_abort);
         const uint32_t fb = full_leader0 + 8u * s;
-        const bool both = kb + 1 < P.num_k_blocks;
+        const int kc = kb * 64;
         if (elect_one() && live) {
-          if (leader) mbar_arrive_expect_tx(full0 + 8u * s, both ? 2 * kCeStageBytes : kCeStageBytes);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (h == 0 || both) {
-              const int kc = (kb + h) * 64;
-              if (P.a_mn) {
-                tma_load_2d_pair(st_a(s, h), &P.tmA, fb, m0, kc);
-                tma_load_2d_pair(st_a(s, h) + 8192, &P.tmA, fb, m0 + 64, kc);
-              } else {
-                tma_load_2d_pair(st_a(s, h), &P.tmA, fb, kc, m0);
-              }
-              if (P.b_mn) {
-                tma_load_2d_pair(st_b(s, h), &P.tmB, fb, n0, kc);
-                tma_load_2d_pair(st_b(s, h) + 8192, &P.tmB, fb, n0 + 64, kc);
-              } else {
-                tma_load_2d_pair(st_b(s, h), &P.tmB, fb, kc, n0);
-              }
-            }
+          if (leader) mbar_arrive_expect_tx(full0 + 8u * s, 2 * kStage2Bytes);
+          if (P.a_mn) {
+            tma_load_2d_pair(st_a(s), &P.tmA, fb, m0, kc);
+            tma_load_2d_pair(st_a(s) + 8192, &P.tmA, fb, m0 + 64, kc);
+          } else {
+            tma_load_2d_pair(st_a(s), &P.tmA, fb, kc, m0);
+          }
+          if (P.b_mn) {
+            tma_load_2d_pair(st_b(s), &P.tmB, fb, n0, kc);
+            tma_load_2d_pair(st_b(s) + 8192, &P.tmB, fb, n0 + 64, kc);
+          } else {
+            tma_load_2d_pair(st_b(s), &P.tmB, fb, kc, n0);
+          }
         }
         issued += live;
-        if (++s == kCeStages) {
+        if (++s == kStages2) {
           s = 0;
           ph ^= 1u;
         }
@@ -326,9 +316,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
       atomicOr(&g_device_status, DEV_ST_TIMEOUT_PRODUCER);
       // the leader's full barriers count both CTAs' copies: drain the last ring of them
       if (leader) {
-        const uint32_t first = issued > kCeStages ? issued - kCeStages : 0;
+        const uint32_t first = issued > kStages2 ? issued - kStages2 : 0;
         for (uint32_t i = first; i < issued; ++i)
-          if (!mbar_wait_plain(full0 + 8u * (i % kCeStages), (i / kCeStages) & 1u)) atomicOr(&g_device_status, DEV_ST_TIMEOUT_DRAIN);
+          if (!mbar_wait_plain(full0 + 8u * (i % kStages2), (i / kStages2) & 1u)) atomicOr(&g_device_status, DEV_ST_TIMEOUT_DRAIN);
       }
     }
   } else if (warp == 1) {
@@ -351,22 +341,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
           live = wait_live<false>(live, tempty0 + 8u * buf, ((unit >> 1) & 1u) ^ 1u, abort_flag, peer_abort);
           tc_fence_after_sync();
           const uint32_t d_tmem = tmem_base + buf * kBN;
-          for (int kb = k0; kb < end; kb += 2) {
+          for (int kb = k0; kb < end; ++kb) {
             live = wait_live<false>(live, full0 + 8u * s, ph, abort_flag, peer_abort);
             tc_fence_after_sync();
             if (elect_one() && live) {
+              const uint64_t ad = make_sw128_desc(st_a(s), a_lbo, 1024), bd = make_sw128_desc(st_b(s), b_lbo, 1024);
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (h == 0 || kb + 1 < end) {
-                  const uint64_t ad = make_sw128_desc(st_a(s, h), a_lbo, 1024), bd = make_sw128_desc(st_b(s, h), b_lbo, 1024);
-#pragma unroll
-                  for (int kk = 0; kk < 4; ++kk)
-                    tc_mma_f16_pair(d_tmem, ad + a_step * kk, bd + b_step * kk, idesc, kb > k0 || (h | kk) != 0 ? 1u : 0u);
-                }
+              for (int kk = 0; kk < 4; ++kk)
+                tc_mma_f16_pair(d_tmem, ad + a_step * kk, bd + b_step * kk, idesc, kb > k0 || kk != 0 ? 1u : 0u);
               tc_commit_pair(empty0 + 8u * s);   // frees this stage in both CTAs
-              if (kb + 2 >= end) tc_commit_pair(tfull0 + 8u * buf);   // both CTAs' accumulators complete
+              if (kb + 1 == end) tc_commit_pair(tfull0 + 8u * buf);   // both CTAs' accumulators complete
             }
-            if (++s == kCeStages) {
+            if (++s == kStages2) {
               s = 0;
               ph ^= 1u;
             }
