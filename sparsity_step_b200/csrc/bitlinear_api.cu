@@ -14,8 +14,8 @@
 #include "codes_tc.cuh"
 #include "common.cuh"
 #include "diag_kernels.cuh"
+#include "few_tokens.cuh"
 #include "fp8_quant.cuh"
-#include "fp8_stream.cuh"
 #include "gemm_fp8.cuh"
 #include "gemm_tc.cuh"
 #include "gemm_sp2.cuh"

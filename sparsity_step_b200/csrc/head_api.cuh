@@ -147,27 +147,123 @@ bl_status enqueue_fp8_gemm(const Fp8Operand& A, const Fp8Operand& B, int64_t k, 
                            : launch_fp8_gemm<1>(A, B, k, out, f32, tiles.n_half, pairs, st);
 }
 
-// Tokens up to which the streaming product runs instead of the pair product, and up to
-// which it makes the codes of bf16 activations itself.
-constexpr int64_t kFp8StreamMaxTokens = 32;
-constexpr int64_t kFp8StreamQuantTokens = 8;
+size_t fp8_scale_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>((cols + 511) / 512) * 4 * rows; }
 
-template <int NT, bool kXBf16, bool kW5, bool kX5>
-bl_status launch_fp8_stream(const bl::Fp8StreamArgs& a, cudaStream_t st) {
-  const int blocks = (a.k + 127) / 128;
-  const int warps = blocks >= 16 ? 16 : blocks >= 8 ? 8 : 4;
-  bl::fp8_stream_kernel<NT, kXBf16, kW5, kX5><<<a.n / 16, 32 * warps, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "fp8 stream launch");
+// ------------------------------------------------------------------ few tokens
+
+constexpr int64_t kFewTokens = 32;           // rows of the tokens' operand at most
+constexpr size_t kFewSmemTwo = 113 * 1024;   // two CTAs on an SM
+constexpr size_t kFewSmemOne = 226 * 1024;
+
+struct FewPlan {
+  int split, stages, tok;
+  size_t smem;
+};
+// How a product of t <= 32 tokens is spread: K is split over a cluster while row blocks x
+// split stays within two CTAs an SM and every CTA keeps two K blocks; then as many stages
+// as fit beside the tokens' operand, two CTAs on an SM if that leaves four stages. False if
+// the operand of a CTA does not fit even when split by 8 (then the pair product runs).
+bool few_plan(bool fp8, int64_t t, int64_t num_k_blocks, int64_t row_blocks, int sms, FewPlan* p) {
+  if (t > kFewTokens || num_k_blocks > 4096) return false;
+  const int tok = t <= 16 ? 16 : 32;
+  int split = 1;
+  while (split < 8 && row_blocks * split * 2 <= 2 * int64_t(sms) && num_k_blocks >= 4 * split) split *= 2;
+  for (; split <= 8; split *= 2) {
+    const int blocks = bl::few_blocks_max(static_cast<int>(num_k_blocks), split);
+    const int parts = fp8 ? 1 : (blocks + bl::kFewPartBlocks - 1) / bl::kFewPartBlocks;
+    if (parts * tok > 256) continue;   // TMEM
+    for (const size_t room : {kFewSmemTwo, kFewSmemOne}) {
+      int stages = bl::kFewMaxStages;
+      while (stages >= 4 && bl::few_smem_bytes(fp8, tok, stages, blocks) + 1024 > room) --stages;
+      if (stages < 4) continue;
+      *p = {split, stages, tok, bl::few_smem_bytes(fp8, tok, stages, blocks) + 1024};   // + the operand's alignment
+      return true;
+    }
+  }
+  return false;
+}
+
+template <bool kFp8, int kTok>
+bl_status launch_few(const bl::FewMaps& M, bl::FewArgs& a, const FewPlan& p, cudaStream_t st) {
+  auto kern = bl::few_tokens_kernel<kFp8, kTok>;
+  static PerDeviceSetup setup;
+  int unused = 0;
+  if (bl_status s = per_device_setup(setup, &unused, [&](int* r) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmemOne);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(few tokens)");
+        *r = 1;
+        return BL_OK;
+      }))
+    return s;
+  a.split = p.split;
+  a.stages = p.stages;
+  const int blocks = bl::few_blocks_max(a.num_k_blocks, p.split);
+  a.parts = kFp8 ? 1 : (blocks + bl::kFewPartBlocks - 1) / bl::kFewPartBlocks;
+  const int cols = a.parts * kTok;
+  a.bufs = 2 * cols + (kFp8 ? 64 : 0) <= 256 ? 2 : 1;
+  a.sf_col0 = static_cast<uint32_t>(a.bufs * cols);
+  uint32_t need = a.sf_col0 + (kFp8 ? 64u : 0u);
+  a.tmem_cols = 32;
+  while (a.tmem_cols < need) a.tmem_cols *= 2;
+  int64_t grid = int64_t(a.num_row_blocks) * p.split;
+  const int64_t resident = int64_t(device_sm_count()) * (p.smem <= kFewSmemTwo ? 2 : 1);
+  if (p.split == 1 && grid > resident) grid = resident;   // several row blocks per CTA
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(bl::kFewThreads);
+  cfg.dynamicSmemBytes = p.smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, M, a);
+  if (e != cudaSuccess) return cuda_fail(e, "few tokens launch");
   return BL_OK;
 }
-template <int NT>
-bl_status enqueue_fp8_stream_codes(const bl::Fp8StreamArgs& a, bool w5, bool x5, cudaStream_t st) {
-  if (w5) return x5 ? launch_fp8_stream<NT, false, true, true>(a, st) : launch_fp8_stream<NT, false, true, false>(a, st);
-  return x5 ? launch_fp8_stream<NT, false, false, true>(a, st) : launch_fp8_stream<NT, false, false, false>(a, st);
+
+// Tokens up to which the product quantises bf16 activations itself: as many as fit whatever
+// n is (a plan for one row block has the largest split, and more row blocks may have less
+// of it, but never less than they need).
+int64_t few_quantised_tokens(int64_t k_in) {
+  FewPlan p;
+  for (const int64_t t : {kFewTokens, int64_t(16)})
+    if (few_plan(true, t, (k_in + 127) / 128, 1, 148, &p)) return t;
+  return 0;
 }
 
-size_t fp8_scale_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>((cols + 511) / 512) * 4 * rows; }
+// y of up to 32 tokens; *done is false (nothing enqueued) where the plan does not fit.
+bl_status enqueue_fp8_few(const void* x, bool x_bf16, const uint8_t* x_scales, bool x5, const uint8_t* w_q,
+                          const uint8_t* w_scales, bool w5, int64_t t, int64_t k, int64_t n, void* y, bool f32,
+                          cudaStream_t st, bool* done) {
+  *done = false;
+  FewPlan p;
+  if (!few_plan(true, t, (k + 127) / 128, (n + 127) / 128, device_sm_count(), &p)) return BL_OK;
+  bl::FewMaps M{};
+  for (int c = 0; c < 4; ++c)   // weight rows c, c + 4, ... (n % 16 == 0)
+    if (bl_status s = make_map_strided(&M.w[c], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w_q + c * k, k, n / 4, 4 * k, 128, 32,
+                                       CU_TENSOR_MAP_SWIZZLE_128B))
+      return s;
+  bl::FewArgs a{};
+  a.x = x;
+  a.xs = reinterpret_cast<const uint32_t*>(x_scales);
+  a.x_bf16 = x_bf16 ? 1 : 0;
+  a.ws = reinterpret_cast<const uint32_t*>(w_scales);
+  a.a_e5m2 = w5;
+  a.b_e5m2 = x5;
+  a.t = static_cast<int>(t);
+  a.k = static_cast<int>(k);
+  a.n = static_cast<int>(n);
+  a.num_k_blocks = static_cast<int>((k + 127) / 128);
+  a.num_row_blocks = static_cast<int>((n + 127) / 128);
+  a.y = y;
+  a.y_f32 = f32 ? 1 : 0;
+  *done = true;
+  return p.tok == 16 ? launch_few<true, 16>(M, a, p, st) : launch_few<true, 32>(M, a, p, st);
+}
 
 // ------------------------------------------------------------------ linear cross entropy
 
@@ -249,7 +345,9 @@ struct CeFwdSpace {
 };
 CeFwdSpace ce_fwd_space(int64_t t, int64_t v) {
   CeFwdSpace s{};
-  const size_t n = 2 * static_cast<size_t>((v + 255) / 256) * static_cast<size_t>(t) * sizeof(float2);
+  // 128 columns a strip; for few tokens as few as 16, an eighth of a row block
+  const size_t per_t = t <= kFewTokens ? 8 * static_cast<size_t>((v + 127) / 128) : 2 * static_cast<size_t>((v + 255) / 256);
+  const size_t n = per_t * static_cast<size_t>(t) * sizeof(float2);
   s.strips = 0;
   s.target_logit = round256(n);
   s.total = s.target_logit + round256(static_cast<size_t>(t) * sizeof(float));
@@ -306,7 +404,7 @@ bl_status bitlinear_fp8_quant_weight(const float* w, int64_t n_out, int64_t k_in
 }
 
 size_t bitlinear_fp8_fwd_workspace_size(int64_t t, int64_t k_in, int x_type) {
-  if (x_type != BL_X_BF16 || t <= kFp8StreamQuantTokens || k_in <= 0) return 0;
+  if (x_type != BL_X_BF16 || t <= 0 || k_in <= 0 || t <= few_quantised_tokens(k_in)) return 0;
   return round256(static_cast<size_t>(t) * static_cast<size_t>(k_in)) + round256(fp8_scale_bytes(t, k_in));
 }
 
@@ -331,7 +429,12 @@ bl_status bitlinear_fp8_fwd(const void* x, int x_type, const uint8_t* x_scales, 
     return fail(BL_ERR_ALIGNMENT, "every pointer must be 16-byte aligned");
   cudaStream_t st = as_stream(stream);
   const bool w5 = w_format == BL_FP8_E5M2, x5 = x_type == BL_X_E5M2, f32 = y_dtype == BL_OUT_F32;
-  if (bf16 && t > kFp8StreamQuantTokens) {   // codes of x in the workspace first
+  if (t <= kFewTokens && (!bf16 || need == 0)) {
+    bool done = false;
+    if (bl_status s = enqueue_fp8_few(x, bf16, x_scales, x5, w_q, w_scales, w5, t, k_in, n_out, y_out, f32, st, &done)) return s;
+    if (done) return BL_OK;
+  }
+  if (bf16) {   // codes of x in the workspace first
     uint8_t* xq = static_cast<uint8_t*>(workspace);
     uint8_t* xs = xq + round256(static_cast<size_t>(t) * static_cast<size_t>(k_in));
     const bl::Fp8QuantArgs a{x, t, k_in, round_up(t, 16), xq, xs, nullptr, nullptr};
@@ -339,23 +442,7 @@ bl_status bitlinear_fp8_fwd(const void* x, int x_type, const uint8_t* x_scales, 
     x = xq;
     x_scales = xs;
   }
-  if (t > kFp8StreamMaxTokens)
-    return enqueue_fp8_gemm({static_cast<const uint8_t*>(x), x_scales, t, x5}, {w_q, w_scales, n_out, w5}, k_in, y_out, f32, st);
-  bl::Fp8StreamArgs a{};
-  a.x = x;
-  a.xs = reinterpret_cast<const uint32_t*>(x_scales);
-  a.wq = w_q;
-  a.ws = reinterpret_cast<const uint32_t*>(w_scales);
-  a.y = y_out;
-  a.t = static_cast<int>(t);
-  a.k = static_cast<int>(k_in);
-  a.n = static_cast<int>(n_out);
-  a.y_f32 = f32 ? 1 : 0;
-  if (bf16 && t <= kFp8StreamQuantTokens)
-    return w5 ? launch_fp8_stream<1, true, true, false>(a, st) : launch_fp8_stream<1, true, false, false>(a, st);
-  if (t <= 8) return enqueue_fp8_stream_codes<1>(a, w5, x5, st);
-  if (t <= 16) return enqueue_fp8_stream_codes<2>(a, w5, x5, st);
-  return enqueue_fp8_stream_codes<4>(a, w5, x5, st);
+  return enqueue_fp8_gemm({static_cast<const uint8_t*>(x), x_scales, t, x5}, {w_q, w_scales, n_out, w5}, k_in, y_out, f32, st);
 }
 
 bl_status bitlinear_fp8_bwd(const uint8_t* dy_q, const uint8_t* dy_scales, const uint8_t* dy_qt, const uint8_t* dy_scales_t,
@@ -420,19 +507,41 @@ bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const in
   if (!aligned16(x) || !aligned16(targets) || !aligned16(loss_out) || !aligned16(lse_out) || !aligned16(workspace))
     return fail(BL_ERR_ALIGNMENT, "every pointer must be 16-byte aligned");
   cudaStream_t st = as_stream(stream);
-  bl::CeGroup G{};
-  G.count = 1;
-  G.v = v;
-  G.targets = targets;
-  G.strips = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + sp.strips);
-  G.target_logit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.target_logit);
-  bl::CeProblem& P = G.p[0];
-  ce_shape(P, bl::CE_LSE, t, v, k_in, false, false);
-  if (bl_status s = ce_operand(&P.tmA, x, k_in, t, k_in, false)) return s;
-  if (bl_status s = ce_operand(&P.tmB, w, k_in, v, k_in, false)) return s;
-  if (bl_status s = launch_ce(G, st)) return s;
-  bl::ce_join_kernel<<<static_cast<unsigned>((t + 31) / 32), 256, 0, st>>>(G.strips, 2 * P.num_n_blocks, t, v, targets,
-                                                                          G.target_logit, loss_out, lse_out);
+  float2* strips = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + sp.strips);
+  float* target_logit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.target_logit);
+  int num_strips = 0;
+  FewPlan plan;
+  if (few_plan(false, t, k_in / 64, (v + 127) / 128, device_sm_count(), &plan)) {
+    bl::FewMaps M{};
+    if (bl_status s = ce_operand(&M.w[0], w, k_in, v, k_in, false)) return s;
+    bl::FewArgs a{};
+    a.x = x;
+    a.t = static_cast<int>(t);
+    a.k = static_cast<int>(k_in);
+    a.n = static_cast<int>(v);
+    a.num_k_blocks = static_cast<int>(k_in / 64);
+    a.num_row_blocks = static_cast<int>((v + 127) / 128);
+    a.targets = targets;
+    a.strips = strips;
+    a.target_logit = target_logit;
+    num_strips = a.num_row_blocks * (plan.split > 1 ? plan.split : 4);
+    if (bl_status s = plan.tok == 16 ? launch_few<false, 16>(M, a, plan, st) : launch_few<false, 32>(M, a, plan, st)) return s;
+  } else {
+    bl::CeGroup G{};
+    G.count = 1;
+    G.v = v;
+    G.targets = targets;
+    G.strips = strips;
+    G.target_logit = target_logit;
+    bl::CeProblem& P = G.p[0];
+    ce_shape(P, bl::CE_LSE, t, v, k_in, false, false);
+    if (bl_status s = ce_operand(&P.tmA, x, k_in, t, k_in, false)) return s;
+    if (bl_status s = ce_operand(&P.tmB, w, k_in, v, k_in, false)) return s;
+    num_strips = 2 * P.num_n_blocks;
+    if (bl_status s = launch_ce(G, st)) return s;
+  }
+  bl::ce_join_kernel<<<static_cast<unsigned>((t + 31) / 32), bl::kCeJoinThreads, 0, st>>>(strips, num_strips, t, v, targets,
+                                                                                         target_logit, loss_out, lse_out);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "linear ce join launch");
   return BL_OK;

@@ -448,32 +448,35 @@ __global__ void __launch_bounds__(1024) ce_grad_max_kernel(const float* grad, co
   }
 }
 
-// Joins the strips of each token: 32 tokens x 8 slices of the strips per block, the
+// Joins the strips of each token: 32 tokens x 32 slices of the strips per block, the
 // slices' (max, sum) pairs joined in order.
-__global__ void __launch_bounds__(256) ce_join_kernel(const float2* strips, int num_strips, int64_t t, int64_t v,
-                                                      const int64_t* targets, const float* target_logit, float* loss,
-                                                      float* lse) {
-  __shared__ float2 s_part[8][32];
+constexpr int kCeJoinThreads = 1024;
+__global__ void __launch_bounds__(kCeJoinThreads) ce_join_kernel(const float2* strips, int num_strips, int64_t t, int64_t v,
+                                                                 const int64_t* targets, const float* target_logit,
+                                                                 float* loss, float* lse) {
+  __shared__ float2 s_part[32][32];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float m = -INFINITY, s = 0.f;
-  if (row < t)
-    for (int i = slice; i < num_strips; i += 8) {
+  if (row < t) {
+#pragma unroll 4
+    for (int i = slice; i < num_strips; i += 32) {
       const float2 p = strips[static_cast<int64_t>(i) * t + row];
-      if (p.y == 0.f) continue;   // a strip past the vocabulary's end
-      const float m2 = fmaxf(m, p.x);
-      s = s * ex2(m - m2) + p.y * ex2(p.x - m2);
+      const bool some = p.y != 0.f;   // else a strip past the vocabulary's end
+      const float m2 = some ? fmaxf(m, p.x) : m;
+      s = some ? s * ex2(m - m2) + p.y * ex2(p.x - m2) : s;
       m = m2;
     }
+  }
   s_part[slice][lane] = make_float2(m, s);
   __syncthreads();
   if (slice == 0 && row < t) {
-    float mm = s_part[0][lane].x;
+    float mm = -INFINITY;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) mm = fmaxf(mm, s_part[i][lane].x);
+    for (int i = 0; i < 32; ++i) mm = fmaxf(mm, s_part[i][lane].x);
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 32; ++i)
       if (s_part[i][lane].y != 0.f) ss += s_part[i][lane].y * ex2(s_part[i][lane].x - mm);
     const float l = mm * 0.6931471805599453f + logf(ss);
     const int64_t y = targets[row];

@@ -130,6 +130,28 @@ def test_fwd(t, k, n):
     assert B.bitlinear_device_status()[0] == 0
 
 
+# few tokens: row blocks that one CTA walks over, K split by 2, 4 and 8, a ragged last row
+# block, the widest K that still fits beside the weights and ones that do not
+FEW_SHAPES = [(1, 192, 40016), (3, 64, 19008), (16, 2048, 11008), (32, 2048, 4112), (17, 1088, 2064), (8, 11008, 2064),
+              (1, 320, 16), (20, 24640, 48), (20, 39936, 32), (8, 131072, 16)]
+
+
+@pytest.mark.parametrize("t,k,n", FEW_SHAPES)
+def test_fwd_few_tokens(t, k, n):
+    rng = np.random.default_rng(t + k + n)
+    x, w = bf16(rng, t, k), (rng.normal(size=(n, k)) * 0.02).astype(np.float32)
+    w[n // 3:] *= 5.0
+    xd, wq = dev(x, torch.bfloat16), B.bitlinear_fp8_quant_weight(dev(w))
+    xo = H.fp8_quant(x, "e4m3")[2]
+    wo = H.decode(u8(wq["q"]), "e4m3") * np.exp2(u8(wq["scales"]).transpose(1, 0, 2).reshape(n, -1).astype(np.float64) - 127.0
+                                                 ).repeat(128, 1)[:, :k]
+    y = B.bitlinear_fp8_fwd(xd, wq["q"], wq["scales"], y_dtype=torch.float32)
+    product_close(y, xo, wo, k)
+    xq = B.bitlinear_fp8_quant(xd)
+    assert torch.equal(B.bitlinear_fp8_fwd(xq["q"], wq["q"], wq["scales"], x_scales=xq["scales"], y_dtype=torch.float32), y)
+    assert B.bitlinear_device_status()[0] == 0
+
+
 @pytest.mark.parametrize("xf,wf", [("e5m2", "e4m3"), ("e4m3", "e5m2"), ("e5m2", "e5m2")])
 @pytest.mark.parametrize("t", [3, 12, 20, 150])
 def test_fwd_formats(t, xf, wf):
@@ -222,7 +244,8 @@ def check_loss(loss, lse, o, d):
 
 
 CE_SHAPES = [(1, 64, 1), (1, 2048, 1000), (2, 128, 2), (3, 64, 255), (8, 192, 256), (9, 64, 257), (32, 576, 31), (33, 64, 33),
-             (100, 128, 5003), (255, 320, 640), (257, 1088, 1031), (300, 64, 12289)]
+             (100, 128, 5003), (255, 320, 640), (257, 1088, 1031), (300, 64, 12289),
+             (1, 2048, 40001), (32, 64, 50001), (17, 1088, 5003), (5, 11008, 300), (32, 8192, 1000), (20, 2112, 19)]
 
 
 @pytest.mark.parametrize("t,k,v", CE_SHAPES)
