@@ -10,9 +10,11 @@
 // 128 bytes) as far ahead as shared memory allows, and nothing between HBM and the tensor
 // core touches them: converting 8-bit codes in registers for warp MMAs (three times the
 // instructions) bounded an earlier version at 10.6 us for 22.5 MB against 3.5 of HBM time.
-// The tokens' operand is made once per CTA, while the first weights are on their way, and
-// stays in shared memory: 16 or 32 rows, 128-byte swizzled, quantised here from bf16 (kFp8)
-// so that a single token needs one launch.
+// The tokens' operand has 16 or 32 rows, 128-byte swizzled. kFp8: made once per CTA, while
+// the first weights are on their way, and kept in shared memory; from bf16 it is quantised
+// here, so that a single token needs one launch. Logits: a K block of it comes with every K
+// block of weights (from L2; kept, it would take the room of the CTA's second ring).
+// Two CTAs fit on an SM, so that the next call's are set up while this one's run.
 // Where there are fewer row blocks than SMs, a cluster of up to 8 CTAs splits K and adds its
 // partial sums through distributed shared memory in the order of the ranks; else a CTA
 // walks over several row blocks with its ring running on.
@@ -21,7 +23,6 @@
 // order, which tcgen05.cp puts at (lane r / 4, column r % 4), while the MMA looks for row i's
 // at (lane i % 32, column i / 32). So the rows are permuted instead: four copies of 32 rows
 // each, four apart, and MMA row 32 c + l is weight row 4 l + c.
-// The accumulator of the logits starts afresh every 512 of K (linear_ce.cuh).
 // Every wait is bounded. No load uses multicast.
 #pragma once
 
@@ -36,14 +37,21 @@ constexpr int kFewThreads = 192;      // producer, MMA, four epilogue warps
 constexpr int kFewMaxStages = 8;
 constexpr int kFewStageBytes = 128 * 128;
 constexpr int kFewSfBytes = 512;
-constexpr int kFewPartBlocks = kCePartBlocks;   // K blocks (64 of K) per accumulation of logits
+// Each of a K block's four MMAs has an accumulator of its own: with so few columns an MMA is
+// short against its latency, and four that add to the same columns wait for one another. The
+// logits' start afresh after 32 K blocks, that is 512 of K each.
+constexpr int kFewPartBlocks = 32;
+__host__ __device__ constexpr int few_parts(bool fp8, int blocks) {
+  return fp8 ? 4 : 4 * ((blocks + kFewPartBlocks - 1) / kFewPartBlocks);
+}
 constexpr int kFewBarBytes = 256;
 
 struct FewMaps {
   CUtensorMap w[4];   // kFp8: rows c, c + 4, c + 8, ...; else w[0]: all rows
+  CUtensorMap x;      // bf16 or codes (not x_bf16)
 };
 struct FewArgs {
-  const void* x;              // [t, k]: bf16, or codes (kFp8)
+  const void* x;              // [t, k] bf16 (x_bf16)
   const uint32_t* xs;         // scale words of codes, [ceil(k / 512), t]
   int x_bf16;                 // kFp8: quantise x here (e4m3)
   const uint32_t* ws;         // kFp8: [ceil(k / 512), n]
@@ -61,11 +69,13 @@ struct FewArgs {
   float* target_logit;
 };
 
-// Shared memory: ring | scale ring (kFp8) | tokens' operand | its scales (kFp8) | barriers.
+// Shared memory: ring of weights | ring of their scales (kFp8) or of the tokens' operand |
+// tokens' operand and its scales (kFp8) | barriers.
 __host__ __device__ constexpr int few_blocks_max(int num_k_blocks, int split) { return (num_k_blocks + split - 1) / split; }
+__host__ __device__ constexpr int few_ring2_bytes(bool fp8, int tok) { return fp8 ? kFewSfBytes : tok * 128; }
 __host__ __device__ constexpr size_t few_smem_bytes(bool fp8, int tok, int stages, int blocks) {
-  return 1024 + static_cast<size_t>(stages) * (kFewStageBytes + (fp8 ? kFewSfBytes : 0)) + static_cast<size_t>(blocks) * tok * 128 +
-         (fp8 ? static_cast<size_t>(blocks / 4 + 2) * kFewSfBytes : 0) + kFewBarBytes;
+  return 2048 + static_cast<size_t>(stages) * (kFewStageBytes + few_ring2_bytes(fp8, tok)) +
+         (fp8 ? static_cast<size_t>(blocks) * tok * 128 + static_cast<size_t>(blocks / 4 + 2) * kFewSfBytes : 0) + kFewBarBytes;
 }
 
 __device__ __forceinline__ void tc_mma_mxf8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
@@ -90,60 +100,64 @@ __device__ __forceinline__ void tmem_ld_tokens(uint32_t taddr, uint32_t (&r)[kTo
   if constexpr (kTok == 16) tmem_ld_32x32b_x16(taddr, r);
   else tmem_ld_32x32b_x32(taddr, r);
 }
+__device__ __forceinline__ int lane_id() { return static_cast<int>(threadIdx.x & 31); }
 __device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// The tokens' operand of K blocks [kb0, kb1) and its scales, by all threads of the CTA.
-template <bool kFp8, int kTok>
-__device__ __forceinline__ void few_tokens_operand(const FewArgs& a, uint32_t sB, uint32_t sSfb, int kb0, int kb1) {
-  const int blocks = kb1 - kb0;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  if (kFp8) {   // scale words not written below must still be finite numbers
-    const int words = ((kb1 - 1) / 4 - kb0 / 4 + 1) * (kFewSfBytes / 16);
-    for (int i = threadIdx.x; i < words; i += kFewThreads) st_shared_v4(sSfb + 16u * i, 0, 0, 0, 0);
-    __syncthreads();
+// Scales of the tokens' operand of K blocks [kb0, kb1) and, from bf16, its codes, by all
+// threads of the CTA.
+template <int kTok>
+__device__ __forceinline__ void few_fp8_operand(const FewArgs& a, uint32_t sB, uint32_t sSfb, int kb0, int kb1) {
+  const int blocks = kb1 - kb0, groups = (kb1 - 1) / 4 - kb0 / 4 + 1;
+  // scale word of token i of K group g at 512 g + 16 i; tokens past the last and the other
+  // columns are zeros
+  for (int i = threadIdx.x; i < groups * 32; i += kFewThreads) {
+    const int tok = i & 31;
+    uint32_t w = 0;
+    if (!a.x_bf16 && tok < a.t) w = __ldg(a.xs + static_cast<int64_t>(kb0 / 4 + (i >> 5)) * a.t + tok);
+    st_shared_v4(sSfb + 16u * static_cast<uint32_t>(i), w, 0, 0, 0);
   }
-  // item: 16 bytes (chunk j) of token tok in block b; 8 lanes make a row of 128 bytes
-  const int items = blocks * kTok * 8;
-  for (int i0 = 0; i0 < items; i0 += kFewThreads) {
-    const int i = i0 + static_cast<int>(threadIdx.x);   // items % 32 == 0: a warp is all in or all out
-    if (i >= items) break;
-    const int j = i & 7, tok = (i >> 3) % kTok, b = (i >> 3) / kTok;
-    const int kb = kb0 + b;
-    uint4 v = zero;
-    if constexpr (!kFp8) {
-      if (tok < a.t)
-        v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(tok) * a.k + kb * 64 + j * 8));
-    } else {
-      const bool in = tok < a.t && kb * 128 + j * 16 < a.k;
-      const int64_t at = static_cast<int64_t>(tok) * a.k + kb * 128 + j * 16;
-      const uint32_t sf = sSfb + static_cast<uint32_t>((kb / 4 - kb0 / 4) * kFewSfBytes + tok * 16 + (kb & 3));
-      if (a.x_bf16) {
-        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + at);
-        const uint4 lo = in ? __ldg(p) : zero, hi = in ? __ldg(p + 1) : zero;
-        uint32_t m = __vmaxu2(__vmaxu2(__vmaxu2(lo.x & 0x7FFF7FFFu, lo.y & 0x7FFF7FFFu), __vmaxu2(lo.z & 0x7FFF7FFFu, lo.w & 0x7FFF7FFFu)),
-                              __vmaxu2(__vmaxu2(hi.x & 0x7FFF7FFFu, hi.y & 0x7FFF7FFFu), __vmaxu2(hi.z & 0x7FFF7FFFu, hi.w & 0x7FFF7FFFu)));
-        m = max(m & 0xFFFFu, m >> 16);
+  if (!a.x_bf16) return;
+  auto at = [&](int b, int tok, int j) { return sB + static_cast<uint32_t>((b * kTok + tok) * 128 + ((j ^ (tok & 7)) * 16)); };
+  for (int i = threadIdx.x; i < blocks * (kTok - a.t) * 8; i += kFewThreads) {   // rows without a token
+    const int r = i >> 3;
+    st_shared_v4(at(r / (kTok - a.t), a.t + r % (kTok - a.t), i & 7), 0, 0, 0, 0);
+  }
+  __syncthreads();   // the scale words are zeros before their bytes are filled in
+  // item: 16 codes (chunk j) of token tok in block b, 8 lanes to a block of 128; four items
+  // a thread at a time, so that their loads overlap
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int items = blocks * a.t * 8;
+  for (int i0 = static_cast<int>(threadIdx.x); i0 - lane_id() < items; i0 += 4 * kFewThreads) {
+    uint4 lo[4], hi[4];
 #pragma unroll
-        for (int off = 1; off < 8; off <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
-        const uint32_t byte = fp8_scale_byte(m << 16, fp8_top_exponent(FP8_E4M3));
-        const float inv = fp8_inv_scale(byte);
-        auto codes = [&](uint32_t p0, uint32_t p1) {
-          return fp8_pack4<false>(__uint_as_float(p0 << 16) * inv, __uint_as_float(p0 & 0xFFFF0000u) * inv,
-                                  __uint_as_float(p1 << 16) * inv, __uint_as_float(p1 & 0xFFFF0000u) * inv);
-        };
-        if (tok < a.t) {
-          v = make_uint4(codes(lo.x, lo.y), codes(lo.z, lo.w), codes(hi.x, hi.y), codes(hi.z, hi.w));
-          if (j == 0) st_shared_u8(sf, byte);
-        }
-      } else {
-        if (in) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.x) + at));
-        if (tok < a.t && j == 0)
-          st_shared_u8(sf, (__ldg(a.xs + static_cast<int64_t>(kb >> 2) * a.t + tok) >> (8 * (kb & 3))) & 255u);
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * kFewThreads, j = i & 7, tok = (i >> 3) % a.t, kb = kb0 + (i >> 3) / a.t;
+      const bool in = i < items && kb * 128 + j * 16 < a.k;
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(tok) * a.k + kb * 128 + j * 16);
+      lo[u] = in ? __ldg(p) : zero;
+      hi[u] = in ? __ldg(p + 1) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * kFewThreads, j = i & 7, tok = (i >> 3) % a.t, b = (i >> 3) / a.t, kb = kb0 + b;
+      uint32_t m = __vmaxu2(__vmaxu2(__vmaxu2(lo[u].x & 0x7FFF7FFFu, lo[u].y & 0x7FFF7FFFu), __vmaxu2(lo[u].z & 0x7FFF7FFFu, lo[u].w & 0x7FFF7FFFu)),
+                            __vmaxu2(__vmaxu2(hi[u].x & 0x7FFF7FFFu, hi[u].y & 0x7FFF7FFFu), __vmaxu2(hi[u].z & 0x7FFF7FFFu, hi[u].w & 0x7FFF7FFFu)));
+      m = max(m & 0xFFFFu, m >> 16);
+#pragma unroll
+      for (int off = 1; off < 8; off <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+      const uint32_t byte = fp8_scale_byte(m << 16, fp8_top_exponent(FP8_E4M3));
+      const float inv = fp8_inv_scale(byte);
+      auto codes = [&](uint32_t p0, uint32_t p1) {
+        return fp8_pack4<false>(__uint_as_float(p0 << 16) * inv, __uint_as_float(p0 & 0xFFFF0000u) * inv,
+                                __uint_as_float(p1 << 16) * inv, __uint_as_float(p1 & 0xFFFF0000u) * inv);
+      };
+      if (i < items) {
+        st_shared_v4(at(b, tok, j), codes(lo[u].x, lo[u].y), codes(lo[u].z, lo[u].w), codes(hi[u].x, hi[u].y), codes(hi[u].z, hi[u].w));
+        if (j == 0) st_shared_u8(sSfb + static_cast<uint32_t>((kb / 4 - kb0 / 4) * kFewSfBytes + tok * 16 + (kb & 3)), byte);
       }
     }
-    st_shared_v4(sB + static_cast<uint32_t>((b * kTok + tok) * 128 + ((j ^ (tok & 7)) * 16)), v.x, v.y, v.z, v.w);
   }
 }
 
@@ -153,13 +167,12 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   const int max_blocks = few_blocks_max(a.num_k_blocks, a.split);
-  const uint32_t sRing = base, sSfa = sRing + static_cast<uint32_t>(a.stages * kFewStageBytes);
-  const uint32_t sB0 = sSfa + (kFp8 ? static_cast<uint32_t>(a.stages * kFewSfBytes) : 0u);
-  const uint32_t sB = (sB0 + 1023u) & ~1023u;
-  const uint32_t sSfb = sB + static_cast<uint32_t>(max_blocks * kTok * 128);
+  const uint32_t sRing = base, sRing2 = sRing + static_cast<uint32_t>(a.stages * kFewStageBytes);
+  const uint32_t sB = (sRing2 + static_cast<uint32_t>(a.stages * few_ring2_bytes(kFp8, kTok)) + 1023u) & ~1023u;
+  const uint32_t sSfb = sB + (kFp8 ? static_cast<uint32_t>(max_blocks * kTok * 128) : 0u);
   const uint32_t bar0 = sSfb + (kFp8 ? static_cast<uint32_t>((max_blocks / 4 + 2) * kFewSfBytes) : 0u);
   const uint32_t full0 = bar0, empty0 = bar0 + 8u * kFewMaxStages, tfull0 = empty0 + 8u * kFewMaxStages, tempty0 = tfull0 + 16u;
-  const uint32_t slot = tempty0 + 16u;
+  const uint32_t xfull = tempty0 + 16u, slot = xfull + 8u;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem_raw + (slot - raw));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + (slot - raw) + 4);
 
@@ -177,8 +190,10 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
       mbar_init(tfull0 + 8u * b, 1);
       mbar_init(tempty0 + 8u * b, 4);   // epilogue warps
     }
+    mbar_init(xfull, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    if (!kFp8 || !a.x_bf16) tma_prefetch_desc(&M.x);
     for (int c = 0; c < (kFp8 ? 4 : 1); ++c) tma_prefetch_desc(&M.w[c]);
   }
   if (warp == 1) {
@@ -189,6 +204,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = __reduce_or_sync(0xffffffffu, *tmem_slot);
+  follow_stream();
 
   uint32_t live = 1;   // producer and MMA warps: 0 after a wait gave up
   int s = 0;
@@ -196,17 +212,19 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
   const uint32_t own_abort = map_to_rank(slot + 4u, static_cast<uint32_t>(rank));
   auto issue = [&](int blk, int kb) {   // K block kb of row block blk into stage s
     const int row0 = blk * 128;
-    const uint32_t sf_bytes = kFp8 ? 4u * static_cast<uint32_t>(min(128, a.n - row0)) : 0u;
+    const uint32_t more = kFp8 ? 4u * static_cast<uint32_t>(min(128, a.n - row0)) : static_cast<uint32_t>(kTok * 128);
+    const uint32_t dst2 = sRing2 + static_cast<uint32_t>(s * few_ring2_bytes(kFp8, kTok));
     live = wait_live<false>(live, empty0 + 8u * s, ph ^ 1u, abort_flag, own_abort);
     if (elect_one() && live) {
       const uint32_t fb = full0 + 8u * s, dst = sRing + static_cast<uint32_t>(s * kFewStageBytes);
-      mbar_arrive_expect_tx(fb, kFewStageBytes + sf_bytes);
+      mbar_arrive_expect_tx(fb, kFewStageBytes + more);
       if constexpr (kFp8) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) tma_load_2d(dst + 4096u * c, &M.w[c], fb, kb * 128, row0 / 4);
-        bulk_load_1d(sSfa + static_cast<uint32_t>(s * kFewSfBytes), a.ws + static_cast<int64_t>(kb >> 2) * a.n + row0, sf_bytes, fb);
+        bulk_load_1d(dst2, a.ws + static_cast<int64_t>(kb >> 2) * a.n + row0, more, fb);
       } else {
         tma_load_2d(dst, &M.w[0], fb, kb * 64, row0);
+        tma_load_2d(dst2, &M.x, fb, kb * 64, 0);
       }
     }
     issued += live;
@@ -216,17 +234,26 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
     }
   };
   // the first ring of weights is on its way while all warps make the tokens' operand
-  const int ahead = min(a.stages, kb1 - kb0);
-  if (warp == 0)
-    for (int i = 0; i < ahead; ++i) issue(blk0, kb0 + i);
-  few_tokens_operand<kFp8, kTok>(a, sB, sSfb, kb0, kb1);
-  fence_proxy_async_smem();
-  __syncthreads();
+  const int ahead = kFp8 ? min(a.stages, kb1 - kb0) : 0;
+  if constexpr (kFp8) {
+    if (warp == 0) {
+      if (!a.x_bf16 && elect_one()) {   // codes as they are: rows past the last token are zeros
+        mbar_arrive_expect_tx(xfull, static_cast<uint32_t>((kb1 - kb0) * kTok * 128));
+        for (int b = 0; b < kb1 - kb0; ++b) tma_load_2d(sB + static_cast<uint32_t>(b * kTok * 128), &M.x, xfull, (kb0 + b) * 128, 0);
+      }
+      __syncwarp();
+      for (int i = 0; i < ahead; ++i) issue(blk0, kb0 + i);
+    }
+    few_fp8_operand<kTok>(a, sB, sSfb, kb0, kb1);
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
 
   if (warp == 0) {
     // ------------------------------------------------------------- TMA producer
     for (int blk = blk0; blk < a.num_row_blocks; blk += blk_step)
       for (int kb = blk == blk0 ? kb0 + ahead : kb0; kb < kb1; ++kb) issue(blk, kb);
+    if (kFp8 && !a.x_bf16 && elect_one() && !mbar_wait_plain(xfull, 0)) atomicOr(&g_device_status, DEV_ST_TIMEOUT_DRAIN);
     if (!live && elect_one()) {
       atomicOr(&g_device_status, DEV_ST_TIMEOUT_PRODUCER);
       const uint32_t st = static_cast<uint32_t>(a.stages), first = issued > st ? issued - st : 0;
@@ -237,6 +264,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
     // ------------------------------------------------------------- MMA issuer
     const uint32_t idesc0 = kFp8 ? make_idesc_mxf8(a.a_e5m2, a.b_e5m2, kTok, 128, 0) : make_idesc(1u, 1u, 1u, 0u, 0u, kTok, 128);
     uint32_t unit = 0, count = 0;
+    if (kFp8 && !a.x_bf16) live = wait_live<false>(live, xfull, 0, abort_flag, own_abort);
     for (int blk = blk0; blk < a.num_row_blocks; blk += blk_step, ++unit) {
       const uint32_t buf = a.bufs == 2 ? unit & 1u : 0u, uph = a.bufs == 2 ? unit >> 1 : unit;
       live = wait_live<false>(live, tempty0 + 8u * buf, (uph & 1u) ^ 1u, abort_flag, own_abort);
@@ -246,23 +274,25 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
         tc_fence_after_sync();
         if (elect_one() && live) {
           const int b = kb - kb0;
-          const int part = kFp8 ? 0 : b / kFewPartBlocks;
-          const uint32_t first = kFp8 ? (b == 0) : (b % kFewPartBlocks == 0);
+          const int part = kFp8 ? 0 : 4 * (b / kFewPartBlocks);
+          const uint32_t add = (kFp8 ? b == 0 : b % kFewPartBlocks == 0) ? 0u : 1u;
           const uint32_t d = tmem_base + (buf * a.parts + part) * kTok;
           const uint64_t ad = make_sw128_desc(sRing + static_cast<uint32_t>(s * kFewStageBytes), 16, 1024);
-          const uint64_t bd = make_sw128_desc(sB + static_cast<uint32_t>(b * kTok * 128), 16, 1024);
+          const uint64_t bd = make_sw128_desc(kFp8 ? sB + static_cast<uint32_t>(b * kTok * 128)
+                                                   : sRing2 + static_cast<uint32_t>(s * kTok * 128), 16, 1024);
           if constexpr (kFp8) {
             // eight slots of scale columns: a slot's last user was at least a ring of stages ago
             const uint32_t col = tmem_base + a.sf_col0 + 8u * (count % kFewMaxStages);
-            tc_cp_32x128b(col, make_sf_desc(sSfa + static_cast<uint32_t>(s * kFewSfBytes)));
+            tc_cp_32x128b(col, make_sf_desc(sRing2 + static_cast<uint32_t>(s * kFewSfBytes)));
             tc_cp_32x128b(col + 4u, make_sf_desc(sSfb + static_cast<uint32_t>((kb / 4 - kb0 / 4) * kFewSfBytes)));
             const uint32_t id = static_cast<uint32_t>(kb & 3), idesc = idesc0 | id << 4 | id << 29;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc_mma_mxf8(d, ad + 2u * kk, bd + 2u * kk, idesc, col, col + 4u, kk != 0 || !first ? 1u : 0u);
+              tc_mma_mxf8(d + static_cast<uint32_t>(kk * kTok), ad + 2u * kk, bd + 2u * kk, idesc, col, col + 4u, add);
           } else {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) tc_mma_f16(d, ad + 2u * kk, bd + 2u * kk, idesc0, kk != 0 || !first ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_f16(d + static_cast<uint32_t>(kk * kTok), ad + 2u * kk, bd + 2u * kk, idesc0, add);
           }
           tc_commit(empty0 + 8u * s);
           if (kb + 1 == kb1) tc_commit(tfull0 + 8u * buf);
@@ -294,7 +324,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
       tmem_ld_wait();
 #pragma unroll
       for (int i = 0; i < kTok; ++i) v[i] = __uint_as_float(r[i]);
-      const int parts = kFp8 ? 1 : (kb1 - kb0 + kFewPartBlocks - 1) / kFewPartBlocks;
+      const int parts = few_parts(kFp8, kb1 - kb0);
       for (int p = 1; p < parts; ++p) {
         tmem_ld_tokens<kTok>(t_row + static_cast<uint32_t>(p * kTok), r);
         tmem_ld_wait();

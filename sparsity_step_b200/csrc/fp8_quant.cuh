@@ -19,7 +19,7 @@
 // Bound by HBM: 2 (4 for weights) bytes read, 1 + 1 written per element.
 #pragma once
 
-#include "common.cuh"
+#include "pair_issue.cuh"
 
 namespace bl {
 
@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kFp8QuantThreads) fp8_quant_kernel(const Fp8Qu
   const int64_t col_blocks = (a.cols + 127) / 128, row_blocks = (a.rows + 127) / 128;
   const int64_t cb = blockIdx.x % col_blocks, rb = blockIdx.x / col_blocks;   // a row of tiles is read in order
   const int64_t col0 = cb * 128 + cv * 8, row0 = rb * 128 + rg * 8;
+  follow_stream();
   const bool col_ok = col0 < a.cols;   // cols % 8 == 0: a thread's 8 columns are all in or all out
 
   if constexpr (!kWeight) {

@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   tc_fence_before_sync();
   cluster_sync();   // barriers of both CTAs initialised, TMEM allocated in both
   tc_fence_after_sync();
+  follow_stream();
   const uint32_t tmem_base = __reduce_or_sync(0xffffffffu, *tmem_slot);   // the same in every lane: a uniform register
   const uint32_t peer_abort = map_to_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
   const int num_tiles = g.num_m_blocks * g.num_n_blocks;

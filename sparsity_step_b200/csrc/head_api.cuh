@@ -7,18 +7,34 @@ namespace {
 
 inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-// Launch configuration of a kernel on clusters of two CTAs.
-void pair_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int threads, size_t smem, cudaStream_t st) {
+// Launch configuration of the head's kernels: clusters of `cluster` CTAs, set up while the
+// kernel before them on the stream still runs (follow_stream() in the kernel).
+void head_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int64_t grid, int threads, size_t smem, int cluster,
+                 cudaStream_t st) {
   cfg = cudaLaunchConfig_t{};
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(threads);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+}
+
+// A kernel without clusters or dynamic shared memory.
+template <class... P, class... A>
+bl_status launch_head(const char* what, void (*kern)(P...), int64_t grid, int threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  head_config(cfg, attr, grid, threads, 0, 0, st);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  return BL_OK;
 }
 
 // Once per device: the kernel's shared-memory limit and how many of its CTA pairs fit.
@@ -28,9 +44,8 @@ bl_status pair_setup(PerDeviceSetup& setup, K kern, int threads, size_t smem, in
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(head)");
         cudaLaunchConfig_t probe;
-        cudaLaunchAttribute attr[1];
-        pair_config(probe, attr, threads, smem, nullptr);
-        probe.gridDim = dim3(2 * (device_sm_count() / 2));
+        cudaLaunchAttribute attr[2];
+        head_config(probe, attr, 2 * (device_sm_count() / 2), threads, smem, 2, nullptr);
         int n = 0;
         e = cudaOccupancyMaxActiveClusters(&n, kern, &probe);
         if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters(head)");
@@ -53,17 +68,9 @@ template <bool kWeight>
 bl_status enqueue_fp8_quant(const bl::Fp8QuantArgs& a, bool e5m2, cudaStream_t st) {
   const int64_t tiles = ((a.rows + 127) / 128) * ((a.cols + 127) / 128);
   if (tiles > INT32_MAX) return fail(BL_ERR_UNSUPPORTED_SHAPE, "too much work in one call");
-  const unsigned grid = static_cast<unsigned>(tiles);
-  if (a.qt) {
-    if (e5m2) bl::fp8_quant_kernel<kWeight, true, true><<<grid, bl::kFp8QuantThreads, 0, st>>>(a);
-    else bl::fp8_quant_kernel<kWeight, false, true><<<grid, bl::kFp8QuantThreads, 0, st>>>(a);
-  } else {
-    if (e5m2) bl::fp8_quant_kernel<kWeight, true, false><<<grid, bl::kFp8QuantThreads, 0, st>>>(a);
-    else bl::fp8_quant_kernel<kWeight, false, false><<<grid, bl::kFp8QuantThreads, 0, st>>>(a);
-  }
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "fp8 quant launch");
-  return BL_OK;
+  auto kern = a.qt ? (e5m2 ? bl::fp8_quant_kernel<kWeight, true, true> : bl::fp8_quant_kernel<kWeight, false, true>)
+                   : (e5m2 ? bl::fp8_quant_kernel<kWeight, true, false> : bl::fp8_quant_kernel<kWeight, false, false>);
+  return launch_head("fp8 quant launch", kern, tiles, bl::kFp8QuantThreads, st, a);
 }
 
 // One operand of the pair product: K-major codes [rows, k] (row stride k) and their scales.
@@ -127,10 +134,9 @@ bl_status launch_fp8_gemm(const Fp8Operand& A, const Fp8Operand& B, int64_t k, v
                                      f32 ? 4 : 2, out, B.rows, A.rows, B.rows, 32, 32,
                                      f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
     return s;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
-  pair_config(cfg, attr, bl::kF8Threads, bl::gemm_fp8_smem_bytes(), st);
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < max_clusters ? tiles : max_clusters));
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  head_config(cfg, attr, 2 * (tiles < max_clusters ? tiles : max_clusters), bl::kF8Threads, bl::gemm_fp8_smem_bytes(), 2, st);
   cudaError_t e = cudaLaunchKernelEx(&cfg, bl::gemm_fp8_kernel<kHalves>, ta, tb, to, g);
   if (e != cudaSuccess) return cuda_fail(e, "fp8 gemm launch");
   return BL_OK;
@@ -170,13 +176,12 @@ bool few_plan(bool fp8, int64_t t, int64_t num_k_blocks, int64_t row_blocks, int
   while (split < 8 && row_blocks * split * 2 <= 2 * int64_t(sms) && num_k_blocks >= 4 * split) split *= 2;
   for (; split <= 8; split *= 2) {
     const int blocks = bl::few_blocks_max(static_cast<int>(num_k_blocks), split);
-    const int parts = fp8 ? 1 : (blocks + bl::kFewPartBlocks - 1) / bl::kFewPartBlocks;
-    if (parts * tok > 256) continue;   // TMEM
+    if (bl::few_parts(fp8, blocks) * tok > 256) continue;   // TMEM
     for (const size_t room : {kFewSmemTwo, kFewSmemOne}) {
       int stages = bl::kFewMaxStages;
-      while (stages >= 4 && bl::few_smem_bytes(fp8, tok, stages, blocks) + 1024 > room) --stages;
+      while (stages >= 4 && bl::few_smem_bytes(fp8, tok, stages, blocks) > room) --stages;
       if (stages < 4) continue;
-      *p = {split, stages, tok, bl::few_smem_bytes(fp8, tok, stages, blocks) + 1024};   // + the operand's alignment
+      *p = {split, stages, tok, bl::few_smem_bytes(fp8, tok, stages, blocks)};
       return true;
     }
   }
@@ -198,7 +203,7 @@ bl_status launch_few(const bl::FewMaps& M, bl::FewArgs& a, const FewPlan& p, cud
   a.split = p.split;
   a.stages = p.stages;
   const int blocks = bl::few_blocks_max(a.num_k_blocks, p.split);
-  a.parts = kFp8 ? 1 : (blocks + bl::kFewPartBlocks - 1) / bl::kFewPartBlocks;
+  a.parts = bl::few_parts(kFp8, blocks);
   const int cols = a.parts * kTok;
   a.bufs = 2 * cols + (kFp8 ? 64 : 0) <= 256 ? 2 : 1;
   a.sf_col0 = static_cast<uint32_t>(a.bufs * cols);
@@ -208,31 +213,23 @@ bl_status launch_few(const bl::FewMaps& M, bl::FewArgs& a, const FewPlan& p, cud
   int64_t grid = int64_t(a.num_row_blocks) * p.split;
   const int64_t resident = int64_t(device_sm_count()) * (p.smem <= kFewSmemTwo ? 2 : 1);
   if (p.split == 1 && grid > resident) grid = resident;   // several row blocks per CTA
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(bl::kFewThreads);
-  cfg.dynamicSmemBytes = p.smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  head_config(cfg, attr, grid, bl::kFewThreads, p.smem, p.split, st);
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, M, a);
   if (e != cudaSuccess) return cuda_fail(e, "few tokens launch");
   return BL_OK;
 }
 
-// Tokens up to which the product quantises bf16 activations itself: as many as fit whatever
-// n is (a plan for one row block has the largest split, and more row blocks may have less
-// of it, but never less than they need).
-int64_t few_quantised_tokens(int64_t k_in) {
+// Tokens up to which the product quantises bf16 activations itself, where their codes fit
+// whatever n is (a plan for one row block has the largest split, and more row blocks may
+// have less of it, but never less than they need). More tokens go through the quantiser:
+// every CTA would repeat their work (11008 -> 2048: 16 tokens 11 us either way, 32 tokens
+// 25.6 us in the product, 20 through the quantiser).
+constexpr int64_t kFewQuantised = 16;
+bool few_quantises(int64_t t, int64_t k_in) {
   FewPlan p;
-  for (const int64_t t : {kFewTokens, int64_t(16)})
-    if (few_plan(true, t, (k_in + 127) / 128, 1, 148, &p)) return t;
-  return 0;
+  return t <= kFewQuantised && few_plan(true, t, (k_in + 127) / 128, 1, 148, &p);
 }
 
 // y of up to 32 tokens; *done is false (nothing enqueued) where the plan does not fit.
@@ -247,6 +244,8 @@ bl_status enqueue_fp8_few(const void* x, bool x_bf16, const uint8_t* x_scales, b
     if (bl_status s = make_map_strided(&M.w[c], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w_q + c * k, k, n / 4, 4 * k, 128, 32,
                                        CU_TENSOR_MAP_SWIZZLE_128B))
       return s;
+  if (!x_bf16)
+    if (bl_status s = make_map(&M.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, k, t, 128, p.tok)) return s;
   bl::FewArgs a{};
   a.x = x;
   a.xs = reinterpret_cast<const uint32_t*>(x_scales);
@@ -308,9 +307,8 @@ bl_status launch_ce(bl::CeGroup& G, cudaStream_t st) {
   }
   G.total_tiles = static_cast<int>(tiles);
   cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute attr[1];
-  pair_config(cfg, attr, bl::kGemmThreads, smem, st);
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < max_clusters ? tiles : max_clusters));
+  cudaLaunchAttribute attr[2];
+  head_config(cfg, attr, 2 * (tiles < max_clusters ? tiles : max_clusters), bl::kGemmThreads, smem, 2, st);
   cudaError_t e = cudaLaunchKernelEx(&cfg, bl::ce_gemm_kernel, G);
   if (e != cudaSuccess) return cuda_fail(e, "linear ce launch");
   return BL_OK;
@@ -404,7 +402,7 @@ bl_status bitlinear_fp8_quant_weight(const float* w, int64_t n_out, int64_t k_in
 }
 
 size_t bitlinear_fp8_fwd_workspace_size(int64_t t, int64_t k_in, int x_type) {
-  if (x_type != BL_X_BF16 || t <= 0 || k_in <= 0 || t <= few_quantised_tokens(k_in)) return 0;
+  if (x_type != BL_X_BF16 || t <= 0 || k_in <= 0 || few_quantises(t, k_in)) return 0;
   return round256(static_cast<size_t>(t) * static_cast<size_t>(k_in)) + round256(fp8_scale_bytes(t, k_in));
 }
 
@@ -429,12 +427,7 @@ bl_status bitlinear_fp8_fwd(const void* x, int x_type, const uint8_t* x_scales, 
     return fail(BL_ERR_ALIGNMENT, "every pointer must be 16-byte aligned");
   cudaStream_t st = as_stream(stream);
   const bool w5 = w_format == BL_FP8_E5M2, x5 = x_type == BL_X_E5M2, f32 = y_dtype == BL_OUT_F32;
-  if (t <= kFewTokens && (!bf16 || need == 0)) {
-    bool done = false;
-    if (bl_status s = enqueue_fp8_few(x, bf16, x_scales, x5, w_q, w_scales, w5, t, k_in, n_out, y_out, f32, st, &done)) return s;
-    if (done) return BL_OK;
-  }
-  if (bf16) {   // codes of x in the workspace first
+  if (need) {   // codes of bf16 x in the workspace first
     uint8_t* xq = static_cast<uint8_t*>(workspace);
     uint8_t* xs = xq + round256(static_cast<size_t>(t) * static_cast<size_t>(k_in));
     const bl::Fp8QuantArgs a{x, t, k_in, round_up(t, 16), xq, xs, nullptr, nullptr};
@@ -442,6 +435,10 @@ bl_status bitlinear_fp8_fwd(const void* x, int x_type, const uint8_t* x_scales, 
     x = xq;
     x_scales = xs;
   }
+  bool done = false;
+  if (bl_status s = enqueue_fp8_few(x, bf16 && !need, x_scales, x5, w_q, w_scales, w5, t, k_in, n_out, y_out, f32, st, &done))
+    return s;
+  if (done) return BL_OK;
   return enqueue_fp8_gemm({static_cast<const uint8_t*>(x), x_scales, t, x5}, {w_q, w_scales, n_out, w5}, k_in, y_out, f32, st);
 }
 
@@ -514,8 +511,8 @@ bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const in
   if (few_plan(false, t, k_in / 64, (v + 127) / 128, device_sm_count(), &plan)) {
     bl::FewMaps M{};
     if (bl_status s = ce_operand(&M.w[0], w, k_in, v, k_in, false)) return s;
+    if (bl_status s = make_map(&M.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, k_in, t, 64, plan.tok)) return s;
     bl::FewArgs a{};
-    a.x = x;
     a.t = static_cast<int>(t);
     a.k = static_cast<int>(k_in);
     a.n = static_cast<int>(v);
@@ -540,11 +537,9 @@ bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const in
     num_strips = 2 * P.num_n_blocks;
     if (bl_status s = launch_ce(G, st)) return s;
   }
-  bl::ce_join_kernel<<<static_cast<unsigned>((t + 31) / 32), bl::kCeJoinThreads, 0, st>>>(strips, num_strips, t, v, targets,
-                                                                                         target_logit, loss_out, lse_out);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "linear ce join launch");
-  return BL_OK;
+  return launch_head("linear ce join launch", bl::ce_join_kernel, (t + 31) / 32, bl::kCeJoinThreads, st,
+                     static_cast<const float2*>(strips), num_strips, t, v, targets, static_cast<const float*>(target_logit),
+                     loss_out, lse_out);
 }
 
 size_t bitlinear_linear_ce_bwd_workspace_size(int64_t t, int64_t k_in, int64_t v, int want_grad_x) {
@@ -584,9 +579,9 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
   const int64_t piece = ce_piece(t, v);
   const int64_t pieces = (v + piece - 1) / piece;
   const bool one = pieces == 1;   // a single piece: grad_X needs no fp32 sum in memory
-  bl::ce_grad_max_kernel<<<1, 1024, 0, st>>>(grad_loss, targets, t, v, grad_max);
-  cudaError_t launched = cudaGetLastError();
-  if (launched != cudaSuccess) return cuda_fail(launched, "linear ce grad max launch");
+  if (bl_status s = launch_head("linear ce grad max launch", bl::ce_grad_max_kernel, 1, 1024, st, grad_loss, targets, t, v,
+                                grad_max))
+    return s;
   bl::CeGroup G{};
   G.v = v;
   G.targets = targets;
@@ -636,10 +631,9 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
     int64_t grid = (n8 + 255) / 256;
     const int64_t cap = int64_t(device_sm_count()) * 16;
     if (grid > cap) grid = cap;
-    bl::ce_round_kernel<<<static_cast<unsigned>(grid), 256, 0, st>>>(reinterpret_cast<const float4*>(acc), n8,
-                                                                    grad_max, reinterpret_cast<uint4*>(grad_x));
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e, "linear ce round launch");
+    if (bl_status s = launch_head("linear ce round launch", bl::ce_round_kernel, grid, 256, st, reinterpret_cast<const float4*>(acc),
+                                  n8, static_cast<const float*>(grad_max), reinterpret_cast<uint4*>(grad_x)))
+      return s;
   }
   return BL_OK;
 }

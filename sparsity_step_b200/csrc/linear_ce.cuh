@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
   tc_fence_before_sync();
   cluster_sync();   // barriers of both CTAs initialised, TMEM allocated in both
   tc_fence_after_sync();
+  follow_stream();
   const uint32_t tmem_base = __reduce_or_sync(0xffffffffu, *tmem_slot);   // the same in every lane: a uniform register
   const uint32_t peer_abort = map_to_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
   const int num_tiles = G.total_tiles;
@@ -434,6 +435,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
 __global__ void __launch_bounds__(1024) ce_grad_max_kernel(const float* grad, const int64_t* targets, int64_t t, int64_t v,
                                                            float* out) {
   __shared__ uint32_t s_max[32];
+  follow_stream();
   uint32_t m = 0;   // |g| as its bit pattern: a NaN is larger than every number and stays one
   for (int64_t i = threadIdx.x; i < t; i += 1024) {
     const int64_t y = targets[i];
@@ -457,6 +459,7 @@ __global__ void __launch_bounds__(kCeJoinThreads) ce_join_kernel(const float2* s
   __shared__ float2 s_part[32][32];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  follow_stream();
   float m = -INFINITY, s = 0.f;
   if (row < t) {
 #pragma unroll 4
@@ -487,6 +490,7 @@ __global__ void __launch_bounds__(kCeJoinThreads) ce_join_kernel(const float2* s
 
 // The summed parts of grad_X times the largest |g|, bf16: 8 elements per thread and step.
 __global__ void __launch_bounds__(256) ce_round_kernel(const float4* src, int64_t n8, const float* scale, uint4* dst) {
+  follow_stream();
   const float f = *scale;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += static_cast<int64_t>(gridDim.x) * 256) {
     const float4 a = __ldg(src + 2 * i), b = __ldg(src + 2 * i + 1);

@@ -1,10 +1,19 @@
-// How the producer and MMA warps of the head's CTA-pair kernels wait and issue
-// (gemm_fp8.cuh, linear_ce.cuh).
+// How the head's kernels follow one another on a stream, and how the producer and MMA warps
+// of its tensor-core kernels wait and issue (gemm_fp8.cuh, linear_ce.cuh, few_tokens.cuh).
 #pragma once
 
 #include "gemm_tc2.cuh"
 
 namespace bl {
+
+// The head's kernels are launched with programmatic stream serialisation: a kernel may be
+// set up (blocks placed, barriers and TMEM prepared) while the one before it on the stream
+// still runs, and waits here, before its first access to global memory, until that one has
+// completed and its writes are visible. Every thread calls it.
+__device__ __forceinline__ void follow_stream() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 // One lane of a converged warp, always the same one. The MMA and producer warps run their
 // loops with all 32 lanes and branch on this only around the instructions themselves: from

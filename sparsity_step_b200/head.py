@@ -3,10 +3,12 @@ float linear and the linear cross entropy. Argument checks and marshalling only,
 ``bitlinear.py``."""
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from ._lib import BL_OUT_BF16, BL_OUT_F32, check, lib
-from .bitlinear import _call, _need, _need_bytes, _need_vec, _ptr
+from .bitlinear import _call, _need, _need_bytes, _ptr
 
 BL_FP8_E4M3 = 0
 BL_FP8_E5M2 = 1
@@ -20,12 +22,36 @@ def _fmt(dtype, name: str) -> int:
     return _FP8[dtype]
 
 
+def _check(t, dtype, shape, name: str, dev) -> None:
+    """``_need`` with its passing case first: a single-token call is short enough for its
+    checks to count."""
+    if (getattr(t, "dtype", None) == dtype and t.shape == shape and t.device == dev and dev.type == "cuda"
+            and t.is_contiguous()):
+        return
+    _need(t, dtype, shape, name, dev)
+
+
+def _launch(fn, dev: torch.device, stream, *args) -> int:
+    """``_call``, without the stream object where the tensors' device is current and the
+    call goes to its current stream."""
+    if stream is None and torch.cuda.current_device() == dev.index:
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    return _call(fn, dev, stream, *args)
+
+
 def _matrix(t, name: str) -> tuple[int, int]:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected two dimensions, got shape {tuple(t.shape)}")
-    return int(t.shape[0]), int(t.shape[1])
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected two dimensions, got shape {tuple(shape)}")
+    return shape[0], shape[1]
+
+
+@functools.lru_cache(maxsize=4096)
+def _size(fn: str, *args) -> int:
+    """A workspace size (a function of the arguments alone)."""
+    return int(getattr(lib(), fn)(*args))
 
 
 def fp8_scales_shape(rows: int, cols: int) -> tuple[int, int, int]:
@@ -39,18 +65,19 @@ def _rows16(rows: int) -> int:
 
 def _quant(fn, name: str, src, dtype, want_t: bool, fmt, out: dict | None, stream) -> dict:
     rows, cols = _matrix(src, name)
-    _need(src, dtype, None, name)
     code, dev = _fmt(fmt, "fmt"), src.device
+    _check(src, dtype, (rows, cols), name, dev)
     o = dict(out or {})
     shapes = {"q": ((rows, cols), fmt), "scales": (fp8_scales_shape(rows, cols), torch.uint8)}
     if want_t:
         shapes["qt"] = ((cols, _rows16(rows)), fmt)
         shapes["scales_t"] = (fp8_scales_shape(cols, rows), torch.uint8)
     for key, (shape, dt) in shapes.items():
-        if key not in o:
+        if key in o:
+            _check(o[key], dt, shape, key, dev)
+        else:
             o[key] = torch.empty(shape, dtype=dt, device=dev)
-        _need(o[key], dt, shape, key, dev)
-    st = _call(getattr(lib(), fn), dev, stream, _ptr(src), rows, cols, code, _ptr(o["q"]), _ptr(o["scales"]),
+    st = _launch(getattr(lib(), fn), dev, stream, _ptr(src), rows, cols, code, _ptr(o["q"]), _ptr(o["scales"]),
                _ptr(o["qt"]) if want_t else None, _ptr(o["scales_t"]) if want_t else None)
     check(st, fn)
     return o
@@ -77,7 +104,7 @@ def bitlinear_fp8_quant_weight(w: torch.Tensor, *, want_t: bool = False, fmt=tor
 
 def bitlinear_fp8_fwd_workspace_size(t: int, k_in: int, x_dtype=torch.bfloat16) -> int:
     x_type = BL_X_BF16 if x_dtype == torch.bfloat16 else _fmt(x_dtype, "x_dtype")
-    return int(lib().bitlinear_fp8_fwd_workspace_size(t, k_in, x_type))
+    return _size("bitlinear_fp8_fwd_workspace_size", t, k_in, x_type)
 
 
 def bitlinear_fp8_fwd(x: torch.Tensor, w_q: torch.Tensor, w_scales: torch.Tensor, *,
@@ -97,22 +124,23 @@ def bitlinear_fp8_fwd(x: torch.Tensor, w_q: torch.Tensor, w_scales: torch.Tensor
         x_type = _fmt(x.dtype, "x")
         if x_scales is None:
             raise ValueError("8-bit x needs x_scales")
-        _need(x_scales, torch.uint8, fp8_scales_shape(t, k_in), "x_scales", dev)
-    _need(x, x.dtype, None, "x")
+        _check(x_scales, torch.uint8, fp8_scales_shape(t, k_in), "x_scales", dev)
+    _check(x, x.dtype, (t, k_in), "x", dev)
     w_fmt = _fmt(w_q.dtype, "w_q")
-    _need(w_q, w_q.dtype, (n_out, k_in), "w_q", dev)
-    _need(w_scales, torch.uint8, fp8_scales_shape(n_out, k_in), "w_scales", dev)
+    _check(w_q, w_q.dtype, (n_out, k_in), "w_q", dev)
+    _check(w_scales, torch.uint8, fp8_scales_shape(n_out, k_in), "w_scales", dev)
     if y is None:
-        y = torch.empty((t, n_out), dtype=y_dtype, device=dev)
-    if y.dtype not in (torch.bfloat16, torch.float32):
+        y = x.new_empty((t, n_out), dtype=y_dtype)
+    else:
+        _check(y, y.dtype, (t, n_out), "y", dev)
+    if y.dtype != torch.bfloat16 and y.dtype != torch.float32:
         raise TypeError(f"y: expected bfloat16 or float32, got {y.dtype}")
-    _need(y, y.dtype, (t, n_out), "y", dev)
-    need = int(lib().bitlinear_fp8_fwd_workspace_size(t, k_in, x_type))
+    need = _size("bitlinear_fp8_fwd_workspace_size", t, k_in, x_type) if x_type == BL_X_BF16 else 0
     if need and workspace is None:
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     if workspace is not None:
         _need_bytes(workspace, need, "workspace", dev)
-    st = _call(lib().bitlinear_fp8_fwd, dev, stream, _ptr(x), x_type, _ptr(x_scales), _ptr(w_q), w_fmt, _ptr(w_scales),
+    st = _launch(lib().bitlinear_fp8_fwd, dev, stream, _ptr(x), x_type, _ptr(x_scales), _ptr(w_q), w_fmt, _ptr(w_scales),
                t, k_in, n_out, _ptr(y), BL_OUT_F32 if y.dtype == torch.float32 else BL_OUT_BF16, _ptr(workspace),
                0 if workspace is None else workspace.numel())
     check(st, "bitlinear_fp8_fwd")
@@ -144,29 +172,29 @@ def bitlinear_fp8_bwd(dy: dict, x: dict | None, w: dict | None, *, want_grad_x: 
     dy_fmt = _fmt(dy["q"].dtype, "dy")
     x_fmt = w_fmt = BL_FP8_E4M3
     if want_grad_x:
-        _need(dy["q"], dy["q"].dtype, (t, n_out), "dy q", dev)
-        _need(dy["scales"], torch.uint8, fp8_scales_shape(t, n_out), "dy scales", dev)
+        _check(dy["q"], dy["q"].dtype, (t, n_out), "dy q", dev)
+        _check(dy["scales"], torch.uint8, fp8_scales_shape(t, n_out), "dy scales", dev)
         w_fmt = _fmt(w["qt"].dtype, "w")
-        _need(w["qt"], w["qt"].dtype, (k_in, n_out), "w qt", dev)
-        _need(w["scales_t"], torch.uint8, fp8_scales_shape(k_in, n_out), "w scales_t", dev)
+        _check(w["qt"], w["qt"].dtype, (k_in, n_out), "w qt", dev)
+        _check(w["scales_t"], torch.uint8, fp8_scales_shape(k_in, n_out), "w scales_t", dev)
         if grad_x is None:
             grad_x = torch.empty((t, k_in), dtype=torch.bfloat16, device=dev)
-        _need(grad_x, torch.bfloat16, (t, k_in), "grad_x", dev)
+        _check(grad_x, torch.bfloat16, (t, k_in), "grad_x", dev)
     if want_grad_w:
-        _need(dy["qt"], dy["q"].dtype, (n_out, t16), "dy qt", dev)
-        _need(dy["scales_t"], torch.uint8, fp8_scales_shape(n_out, t), "dy scales_t", dev)
+        _check(dy["qt"], dy["q"].dtype, (n_out, t16), "dy qt", dev)
+        _check(dy["scales_t"], torch.uint8, fp8_scales_shape(n_out, t), "dy scales_t", dev)
         x_fmt = _fmt(x["qt"].dtype, "x")
-        _need(x["qt"], x["qt"].dtype, (k_in, t16), "x qt", dev)
-        _need(x["scales_t"], torch.uint8, fp8_scales_shape(k_in, t), "x scales_t", dev)
+        _check(x["qt"], x["qt"].dtype, (k_in, t16), "x qt", dev)
+        _check(x["scales_t"], torch.uint8, fp8_scales_shape(k_in, t), "x scales_t", dev)
         if grad_w is None:
             grad_w = torch.empty((n_out, k_in), dtype=grad_w_dtype, device=dev)
         if grad_w.dtype not in (torch.bfloat16, torch.float32):
             raise TypeError(f"grad_w: expected bfloat16 or float32, got {grad_w.dtype}")
-        _need(grad_w, grad_w.dtype, (n_out, k_in), "grad_w", dev)
+        _check(grad_w, grad_w.dtype, (n_out, k_in), "grad_w", dev)
     gwdt = BL_OUT_F32 if grad_w is not None and grad_w.dtype == torch.float32 else BL_OUT_BF16
     xp, wp = x if want_grad_w else {}, w if want_grad_x else {}
     dyt = dy if want_grad_w else {}
-    st = _call(lib().bitlinear_fp8_bwd, dev, stream, _ptr(dy["q"]), _ptr(dy.get("scales")), _ptr(dyt.get("qt")),
+    st = _launch(lib().bitlinear_fp8_bwd, dev, stream, _ptr(dy["q"]), _ptr(dy.get("scales")), _ptr(dyt.get("qt")),
                _ptr(dyt.get("scales_t")), dy_fmt, _ptr(xp.get("qt")), _ptr(xp.get("scales_t")), x_fmt, _ptr(wp.get("qt")),
                _ptr(wp.get("scales_t")), w_fmt, t, k_in, n_out, _ptr(grad_x), _ptr(grad_w), gwdt)
     check(st, "bitlinear_fp8_bwd")
@@ -176,14 +204,14 @@ def bitlinear_fp8_bwd(dy: dict, x: dict | None, w: dict | None, *, want_grad_x: 
 def _check_ce(x, w, targets) -> tuple[int, int, int]:
     t, k_in = _matrix(x, "x")
     v = _matrix(w, "w")[0]
-    _need(x, torch.bfloat16, None, "x")
-    _need(w, torch.bfloat16, (v, k_in), "w", x.device)
-    _need(targets, torch.int64, (t,), "targets", x.device)
+    _check(x, torch.bfloat16, (t, k_in), "x", x.device)
+    _check(w, torch.bfloat16, (v, k_in), "w", x.device)
+    _check(targets, torch.int64, (t,), "targets", x.device)
     return t, k_in, v
 
 
 def bitlinear_linear_ce_fwd_workspace_size(t: int, v: int) -> int:
-    return int(lib().bitlinear_linear_ce_fwd_workspace_size(t, v))
+    return _size("bitlinear_linear_ce_fwd_workspace_size", t, v)
 
 
 def bitlinear_linear_ce_fwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, *,
@@ -195,24 +223,26 @@ def bitlinear_linear_ce_fwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Ten
     t, k_in, v = _check_ce(x, w, targets)
     dev = x.device
     if loss is None:
-        loss = torch.empty((t,), dtype=torch.float32, device=dev)
+        loss = x.new_empty((t,), dtype=torch.float32)
+    else:
+        _check(loss, torch.float32, (t,), "loss", dev)
     if lse is None:
-        lse = torch.empty((t,), dtype=torch.float32, device=dev)
-    _need(loss, torch.float32, (t,), "loss", dev)
-    _need(lse, torch.float32, (t,), "lse", dev)
+        lse = x.new_empty((t,), dtype=torch.float32)
+    else:
+        _check(lse, torch.float32, (t,), "lse", dev)
     need = bitlinear_linear_ce_fwd_workspace_size(t, v)
     if need and workspace is None:
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     if workspace is not None:
         _need_bytes(workspace, need, "workspace", dev)
-    st = _call(lib().bitlinear_linear_ce_fwd, dev, stream, _ptr(x), _ptr(w), _ptr(targets), t, k_in, v, _ptr(loss),
+    st = _launch(lib().bitlinear_linear_ce_fwd, dev, stream, _ptr(x), _ptr(w), _ptr(targets), t, k_in, v, _ptr(loss),
                _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel())
     check(st, "bitlinear_linear_ce_fwd")
     return loss, lse
 
 
 def bitlinear_linear_ce_bwd_workspace_size(t: int, k_in: int, v: int, want_grad_x: bool = True) -> int:
-    return int(lib().bitlinear_linear_ce_bwd_workspace_size(t, k_in, v, int(want_grad_x)))
+    return _size("bitlinear_linear_ce_bwd_workspace_size", t, k_in, v, int(want_grad_x))
 
 
 def bitlinear_linear_ce_bwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
@@ -225,25 +255,25 @@ def bitlinear_linear_ce_bwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Ten
     the total with respect to each token's loss; returns (grad_x or None, grad_w or None)."""
     t, k_in, v = _check_ce(x, w, targets)
     dev = x.device
-    _need_vec(lse, torch.float32, t, "lse", dev)
-    _need_vec(grad_loss, torch.float32, t, "grad_loss", dev)
+    _check(lse, torch.float32, (t,), "lse", dev)
+    _check(grad_loss, torch.float32, (t,), "grad_loss", dev)
     if want_grad_x and grad_x is None:
         grad_x = torch.empty((t, k_in), dtype=torch.bfloat16, device=dev)
     if want_grad_w and grad_w is None:
         grad_w = torch.empty((v, k_in), dtype=grad_w_dtype, device=dev)
     if grad_x is not None:
-        _need(grad_x, torch.bfloat16, (t, k_in), "grad_x", dev)
+        _check(grad_x, torch.bfloat16, (t, k_in), "grad_x", dev)
     if grad_w is not None:
         if grad_w.dtype not in (torch.bfloat16, torch.float32):
             raise TypeError(f"grad_w: expected bfloat16 or float32, got {grad_w.dtype}")
-        _need(grad_w, grad_w.dtype, (v, k_in), "grad_w", dev)
+        _check(grad_w, grad_w.dtype, (v, k_in), "grad_w", dev)
     gwdt = BL_OUT_F32 if grad_w is not None and grad_w.dtype == torch.float32 else BL_OUT_BF16
     need = bitlinear_linear_ce_bwd_workspace_size(t, k_in, v, grad_x is not None)
     if need and workspace is None:
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     if workspace is not None:
         _need_bytes(workspace, need, "workspace", dev)
-    st = _call(lib().bitlinear_linear_ce_bwd, dev, stream, _ptr(x), _ptr(w), _ptr(targets), _ptr(lse), _ptr(grad_loss), t,
+    st = _launch(lib().bitlinear_linear_ce_bwd, dev, stream, _ptr(x), _ptr(w), _ptr(targets), _ptr(lse), _ptr(grad_loss), t,
                k_in, v, _ptr(grad_x), _ptr(grad_w), gwdt, _ptr(workspace), 0 if workspace is None else workspace.numel())
     check(st, "bitlinear_linear_ce_bwd")
     return grad_x, grad_w
