@@ -38,6 +38,23 @@ __device__ __forceinline__ uint32_t fp8_scale_byte(uint32_t bits, int top) {
 __device__ __forceinline__ float fp8_inv_scale(uint32_t byte) {
   return __uint_as_float(byte == 255u ? 0x7FFFFFFFu : (254u - byte) << 23);
 }
+// The same as bf16, in both halves.
+__device__ __forceinline__ uint32_t fp8_inv_scale_bf16x2(uint32_t byte) {
+  const uint32_t h = byte == 255u ? 0x7FFFu : (254u - byte) << 7;
+  return h | h << 16;
+}
+// Two bf16 times two powers of two: exact down to bf16's subnormals, which are far below
+// half of either format's smallest code.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Larger magnitudes of two bf16 pairs; a NaN stays one (its pattern is above every number's).
+__device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&a)),
+                                       __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 // 2^e of a scale byte; byte 0 is 2^-127, a subnormal.
 __device__ __forceinline__ float fp8_scale(uint32_t byte) {
   return __uint_as_float(byte == 255u ? 0x7FFFFFFFu : byte == 0u ? 0x00400000u : byte << 23);
@@ -56,6 +73,13 @@ __device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d
   return fp8_pack2<kE5M2>(a, b) | fp8_pack2<kE5M2>(c, d) << 16;
 }
 
+// Codes of two scaled bf16 pairs.
+template <bool kE5M2>
+__device__ __forceinline__ uint32_t fp8_codes4(uint32_t a, uint32_t b) {
+  return fp8_pack4<kE5M2>(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u), __uint_as_float(b << 16),
+                          __uint_as_float(b & 0xFFFF0000u));
+}
+
 struct Fp8QuantArgs {
   const void* src;        // bf16 (activations) or fp32 (weights) [rows, cols]
   int64_t rows, cols;     // cols % 16 == 0
@@ -68,12 +92,11 @@ struct Fp8QuantArgs {
 
 // One scale byte of block b of row r, in a [ceil(blocks / 4), rows, 4] array; the last
 // block also clears the bytes behind it, so the whole array is always written.
-__device__ __forceinline__ void fp8_put_scale(uint8_t* scales, int64_t rows, int64_t r, int64_t b, int64_t blocks,
-                                              uint32_t byte) {
+__device__ __forceinline__ void fp8_put_scale(uint8_t* scales, int64_t rows, int64_t r, int b, int blocks, uint32_t byte) {
   uint8_t* p = scales + ((b >> 2) * rows + r) * 4;
   p[b & 3] = static_cast<uint8_t>(byte);
   if (b == blocks - 1)
-    for (int64_t j = (b & 3) + 1; j < 4; ++j) p[j] = 0;
+    for (int j = (b & 3) + 1; j < 4; ++j) p[j] = 0;
 }
 
 constexpr int kFp8QuantThreads = 256;
@@ -82,13 +105,18 @@ template <bool kWeight, bool kE5M2, bool kT>
 __global__ void __launch_bounds__(kFp8QuantThreads) fp8_quant_kernel(const Fp8QuantArgs a) {
   constexpr int kTop = fp8_top_exponent(kE5M2 ? FP8_E5M2 : FP8_E4M3);
   __shared__ uint32_t s_max[8][64];                          // per warp: column maxima (bf16 pairs) or one block maximum
+  __shared__ __align__(16) uint32_t s_inv[64];               // column pairs' 2^-e
   __shared__ __align__(16) uint8_t s_t[kT ? 128 * 128 : 16];   // transposed codes
   __shared__ uint8_t s_row[128];                             // row scale bytes
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cv = lane & 15, rg = warp * 2 + (lane >> 4);
-  const int64_t col_blocks = (a.cols + 127) / 128, row_blocks = (a.rows + 127) / 128;
-  const int64_t cb = blockIdx.x % col_blocks, rb = blockIdx.x / col_blocks;   // a row of tiles is read in order
-  const int64_t col0 = cb * 128 + cv * 8, row0 = rb * 128 + rg * 8;
+  const int col_blocks = static_cast<int>((a.cols + 127) / 128), row_blocks = static_cast<int>((a.rows + 127) / 128);
+  // a row of tiles is read in order (32-bit division: tiles are counted in 31 bits)
+  const int rb = static_cast<int>(blockIdx.x / static_cast<unsigned>(col_blocks));
+  const int cb = static_cast<int>(blockIdx.x - static_cast<unsigned>(rb) * static_cast<unsigned>(col_blocks));
+  const int64_t col0 = static_cast<int64_t>(cb) * 128 + cv * 8, row0 = static_cast<int64_t>(rb) * 128 + rg * 8;
+  const int64_t at0 = row0 * a.cols + col0;   // this thread's first element
+  const int rows_in = row0 < a.rows ? static_cast<int>(a.rows - row0 < 8 ? a.rows - row0 : 8) : 0;
   follow_stream();
   const bool col_ok = col0 < a.cols;   // cols % 8 == 0: a thread's 8 columns are all in or all out
 
@@ -98,21 +126,19 @@ __global__ void __launch_bounds__(kFp8QuantThreads) fp8_quant_kernel(const Fp8Qu
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       v[i] = make_uint4(0, 0, 0, 0);
-      if (col_ok && row0 + i < a.rows)
-        v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.src) + (row0 + i) * a.cols + col0));
+      if (col_ok && i < rows_in) v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.src) + at0 + i * a.cols));
     }
     uint32_t rm[4] = {0, 0, 0, 0};   // maxima of row pairs (i, i + 4) as 16-bit |bf16| patterns
     uint32_t cm[4] = {0, 0, 0, 0};   // column pairs
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t w0 = v[i].x & 0x7FFF7FFFu, w1 = v[i].y & 0x7FFF7FFFu, w2 = v[i].z & 0x7FFF7FFFu, w3 = v[i].w & 0x7FFF7FFFu;
       if (kT) {
-        cm[0] = __vmaxu2(cm[0], w0);
-        cm[1] = __vmaxu2(cm[1], w1);
-        cm[2] = __vmaxu2(cm[2], w2);
-        cm[3] = __vmaxu2(cm[3], w3);
+        cm[0] = absmax_bf16x2(cm[0], v[i].x);
+        cm[1] = absmax_bf16x2(cm[1], v[i].y);
+        cm[2] = absmax_bf16x2(cm[2], v[i].z);
+        cm[3] = absmax_bf16x2(cm[3], v[i].w);
       }
-      const uint32_t m2 = __vmaxu2(__vmaxu2(w0, w1), __vmaxu2(w2, w3));
+      const uint32_t m2 = absmax_bf16x2(absmax_bf16x2(v[i].x, v[i].y), absmax_bf16x2(v[i].z, v[i].w));
       const uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
       rm[i & 3] |= i < 4 ? m : m << 16;
     }
@@ -124,17 +150,12 @@ __global__ void __launch_bounds__(kFp8QuantThreads) fp8_quant_kernel(const Fp8Qu
     for (int i = 0; i < 8; ++i) {
       const uint32_t pat = i < 4 ? rm[i & 3] & 0xFFFFu : rm[i & 3] >> 16;
       const uint32_t byte = fp8_scale_byte(pat << 16, kTop);
-      const float inv = fp8_inv_scale(byte);
+      const uint32_t inv2 = fp8_inv_scale_bf16x2(byte);
       if (cv == i) s_row[rg * 8 + i] = static_cast<uint8_t>(byte);
-      if (col_ok && row0 + i < a.rows) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t c[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          c[j] = fp8_pack4<kE5M2>(__uint_as_float(w[2 * j] << 16) * inv, __uint_as_float(w[2 * j] & 0xFFFF0000u) * inv,
-                                  __uint_as_float(w[2 * j + 1] << 16) * inv, __uint_as_float(w[2 * j + 1] & 0xFFFF0000u) * inv);
-        *reinterpret_cast<uint2*>(a.q + (row0 + i) * a.cols + col0) = make_uint2(c[0], c[1]);
-      }
+      if (col_ok && i < rows_in)
+        *reinterpret_cast<uint2*>(a.q + at0 + i * a.cols) =
+            make_uint2(fp8_codes4<kE5M2>(mul_bf16x2(v[i].x, inv2), mul_bf16x2(v[i].y, inv2)),
+                       fp8_codes4<kE5M2>(mul_bf16x2(v[i].z, inv2), mul_bf16x2(v[i].w, inv2)));
     }
     if (kT) {
 #pragma unroll
@@ -142,31 +163,39 @@ __global__ void __launch_bounds__(kFp8QuantThreads) fp8_quant_kernel(const Fp8Qu
       if (lane < 16) *reinterpret_cast<uint4*>(&s_max[warp][cv * 4]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
     }
     __syncthreads();
-    if (threadIdx.x < 128 && rb * 128 + threadIdx.x < a.rows)
-      fp8_put_scale(a.scales, a.rows, rb * 128 + threadIdx.x, cb, col_blocks, s_row[threadIdx.x]);
+    if (threadIdx.x < 128 && static_cast<int64_t>(rb) * 128 + threadIdx.x < a.rows)
+      fp8_put_scale(a.scales, a.rows, static_cast<int64_t>(rb) * 128 + threadIdx.x, cb, col_blocks, s_row[threadIdx.x]);
     if constexpr (kT) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      if (threadIdx.x < 64) {   // scales of a pair of columns
         uint32_t m = 0;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) m = __vmaxu2(m, s_max[w][cv * 4 + j]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c = cv * 8 + 2 * j + h;
-          const uint32_t byte = fp8_scale_byte((h ? m >> 16 : m & 0xFFFFu) << 16, kTop);
-          const float inv = fp8_inv_scale(byte);
-          float f[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t w = j == 0 ? v[i].x : j == 1 ? v[i].y : j == 2 ? v[i].z : v[i].w;
-            f[i] = __uint_as_float(h ? w & 0xFFFF0000u : w << 16) * inv;
-          }
-          // 8-byte word rg of column c, its place rotated by the column group: a half-warp's
-          // 16 words fall into 16 different bank pairs
-          *reinterpret_cast<uint2*>(s_t + c * 128 + ((rg ^ cv) * 8)) =
-              make_uint2(fp8_pack4<kE5M2>(f[0], f[1], f[2], f[3]), fp8_pack4<kE5M2>(f[4], f[5], f[6], f[7]));
-          if (rg == 0 && col_ok) fp8_put_scale(a.scales_t, a.cols, cb * 128 + c, rb, row_blocks, byte);
+        for (int w = 0; w < 8; ++w) m = __vmaxu2(m, s_max[w][threadIdx.x]);
+        const uint32_t b0 = fp8_scale_byte(m << 16, kTop), b1 = fp8_scale_byte(m & 0xFFFF0000u, kTop);
+        s_inv[threadIdx.x] = (fp8_inv_scale_bf16x2(b0) & 0xFFFFu) | (fp8_inv_scale_bf16x2(b1) & 0xFFFF0000u);
+        const int64_t col = static_cast<int64_t>(cb) * 128 + 2 * threadIdx.x;
+        if (col < a.cols) {   // an even number of columns: both or none
+          fp8_put_scale(a.scales_t, a.cols, col, rb, row_blocks, b0);
+          fp8_put_scale(a.scales_t, a.cols, col + 1, rb, row_blocks, b1);
         }
+      }
+      __syncthreads();
+      const uint4 inv4 = *reinterpret_cast<const uint4*>(&s_inv[cv * 4]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // columns 2 j and 2 j + 1 side by side: one multiplication per row for both
+        const uint32_t inv2 = j == 0 ? inv4.x : j == 1 ? inv4.y : j == 2 ? inv4.z : inv4.w;
+        uint32_t p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = mul_bf16x2(j == 0 ? v[i].x : j == 1 ? v[i].y : j == 2 ? v[i].z : v[i].w, inv2);
+        // 8-byte word rg of a column, its place rotated by the column group: a half-warp's
+        // 16 words fall into 16 different bank pairs
+        uint8_t* dst = s_t + (cv * 8 + 2 * j) * 128 + ((rg ^ cv) * 8);
+        auto even = [&](int i) { return __uint_as_float(p[i] << 16); };
+        auto odd = [&](int i) { return __uint_as_float(p[i] & 0xFFFF0000u); };
+        *reinterpret_cast<uint2*>(dst) = make_uint2(fp8_pack4<kE5M2>(even(0), even(1), even(2), even(3)),
+                                                    fp8_pack4<kE5M2>(even(4), even(5), even(6), even(7)));
+        *reinterpret_cast<uint2*>(dst + 128) = make_uint2(fp8_pack4<kE5M2>(odd(0), odd(1), odd(2), odd(3)),
+                                                          fp8_pack4<kE5M2>(odd(4), odd(5), odd(6), odd(7)));
       }
     }
   } else {
@@ -176,8 +205,8 @@ __global__ void __launch_bounds__(kFp8QuantThreads) fp8_quant_kernel(const Fp8Qu
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       v[i][0] = v[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (col_ok && row0 + i < a.rows) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.src) + (row0 + i) * a.cols + col0);
+      if (col_ok && i < rows_in) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.src) + at0 + i * a.cols);
         v[i][0] = __ldg(p);
         v[i][1] = __ldg(p + 1);
       }
@@ -201,13 +230,13 @@ __global__ void __launch_bounds__(kFp8QuantThreads) fp8_quant_kernel(const Fp8Qu
     for (int i = 0; i < 8; ++i) {
       c[i] = make_uint2(fp8_pack4<kE5M2>(v[i][0].x * inv, v[i][0].y * inv, v[i][0].z * inv, v[i][0].w * inv),
                         fp8_pack4<kE5M2>(v[i][1].x * inv, v[i][1].y * inv, v[i][1].z * inv, v[i][1].w * inv));
-      if (col_ok && row0 + i < a.rows) *reinterpret_cast<uint2*>(a.q + (row0 + i) * a.cols + col0) = c[i];
+      if (col_ok && i < rows_in) *reinterpret_cast<uint2*>(a.q + at0 + i * a.cols) = c[i];
     }
-    if (threadIdx.x < 128 && rb * 128 + threadIdx.x < a.rows)
-      fp8_put_scale(a.scales, a.rows, rb * 128 + threadIdx.x, cb, col_blocks, byte);
+    if (threadIdx.x < 128 && static_cast<int64_t>(rb) * 128 + threadIdx.x < a.rows)
+      fp8_put_scale(a.scales, a.rows, static_cast<int64_t>(rb) * 128 + threadIdx.x, cb, col_blocks, byte);
     if constexpr (kT) {
-      if (threadIdx.x >= 128 && cb * 128 + threadIdx.x - 128 < a.cols)
-        fp8_put_scale(a.scales_t, a.cols, cb * 128 + threadIdx.x - 128, rb, row_blocks, byte);
+      const int64_t col = static_cast<int64_t>(cb) * 128 + (threadIdx.x & 127);
+      if (threadIdx.x >= 128 && col < a.cols) fp8_put_scale(a.scales_t, a.cols, col, rb, row_blocks, byte);
       // the same codes transposed: an 8 x 8 byte block per thread by byte permutes
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -233,7 +262,7 @@ __global__ void __launch_bounds__(kFp8QuantThreads) fp8_quant_kernel(const Fp8Qu
     for (int it = 0; it < 4; ++it) {
       const int idx = it * kFp8QuantThreads + threadIdx.x;
       const int c = idx >> 3, piece = idx & 7;
-      const int64_t col = cb * 128 + c, row = rb * 128 + piece * 16;
+      const int64_t col = static_cast<int64_t>(cb) * 128 + c, row = static_cast<int64_t>(rb) * 128 + piece * 16;
       if (col < a.cols && row < a.rows_pad) {
         const int g = (c >> 3) & 15;
         const uint2 lo = *reinterpret_cast<const uint2*>(s_t + c * 128 + (((2 * piece) ^ g) * 8));
