@@ -23,11 +23,14 @@
 // Bound by the bf16 tensor pipe (and the power it draws).
 //
 // The kernel takes up to three products with their own operand orders, depths and
-// epilogues in one launch (their tiles numbered consecutively, the deepest first), so that
-// the two products of one piece and the logits of the next fill the SMs together.
+// epilogues in one launch, so that the two products of one piece and the logits of the next
+// fill the SMs together; each pair gets as many tiles of each as make its K blocks add up to
+// its share (tiles of different depth dealt out in turn left some pairs with twice the work
+// at 2047 x 1536 x 32003: 0.53 -> 0.42 ms).
 // Stages, synchronisation and TMEM use as in gemm_tc2.cuh.
 #pragma once
 
+#include "gemm_sp2.cuh"
 #include "pair_issue.cuh"
 
 namespace bl {
@@ -50,13 +53,25 @@ struct CeProblem {
   int part_blocks;               // K blocks per accumulation in TMEM
   int num_m_blocks, num_n_blocks;   // 256 x 256 tiles
   int m_fastest;
-  int tile_begin;
   int v0;                        // first vocabulary row of the piece (CE_DLOGITS)
 };
 constexpr int kMaxCeGroup = 3;
+constexpr int kMaxCePairs = 80;
+constexpr int kMaxCeExtra = 48;
+// Which tiles of a product a CTA pair computes: `count` of them, one a round; the pairs stand
+// in the order of their counts (`pos`), so that a round's tiles are consecutive and its pairs
+// the first ones. Every pair takes part in the first `common` rounds; round common + i
+// begins at tile start[i].
+struct CeShares {
+  int16_t pos[kMaxCePairs];
+  int count[kMaxCePairs];
+  int common;
+  int start[kMaxCeExtra];
+};
 struct CeGroup {
   CeProblem p[kMaxCeGroup];
-  int count, total_tiles;
+  CeShares share[kMaxCeGroup];
+  int count;
   int64_t v;                     // vocabulary size
   const int64_t* targets;        // [T]
   const float* lse;              // [T]  (CE_DLOGITS)
@@ -85,11 +100,9 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-__device__ __forceinline__ int ce_problem(const CeGroup& G, int tile) {
-  int i = 0;
-#pragma unroll
-  for (int j = 1; j < kMaxCeGroup; ++j) i += (j < G.count && tile >= G.p[j].tile_begin) ? 1 : 0;
-  return i;
+// Tile of round r for the pair at position pos.
+__device__ __forceinline__ int ce_round_tile(const CeShares& S, int pairs, int pos, int r) {
+  return (r < S.common ? r * pairs : S.start[r - S.common]) + pos;
 }
 __device__ __forceinline__ void ce_tile(const CeProblem& P, int tile, int& mb, int& nb) {
   if (P.m_fastest) {
@@ -271,7 +284,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
   follow_stream();
   const uint32_t tmem_base = __reduce_or_sync(0xffffffffu, *tmem_slot);   // the same in every lane: a uniform register
   const uint32_t peer_abort = map_to_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
-  const int num_tiles = G.total_tiles;
   const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
 
   if (warp == 0) {
@@ -281,35 +293,38 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
     int s = 0;
     uint32_t ph = 0;
     uint32_t issued = 0;
-    for (int tile = cluster; tile < num_tiles; tile += nclusters) {
-      const CeProblem& P = G.p[ce_problem(G, tile)];
-      int mb, nb;
-      ce_tile(P, tile - P.tile_begin, mb, nb);
-      const int m0 = mb * 256 + 128 * static_cast<int>(rank);
-      const int n0 = nb * 256 + 128 * static_cast<int>(rank);
-      for (int kb = 0; kb < P.num_k_blocks; ++kb) {
-        live = wait_live<false>(live, empty0 + 8u * s, ph ^ 1u, abort_flag, peer_abort);
-        const uint32_t fb = full_leader0 + 8u * s;
-        const int kc = kb * 64;
-        if (elect_one() && live) {
-          if (leader) mbar_arrive_expect_tx(full0 + 8u * s, 2 * kStage2Bytes);
-          if (P.a_mn) {
-            tma_load_2d_pair(st_a(s), &P.tmA, fb, m0, kc);
-            tma_load_2d_pair(st_a(s) + 8192, &P.tmA, fb, m0 + 64, kc);
-          } else {
-            tma_load_2d_pair(st_a(s), &P.tmA, fb, kc, m0);
+    for (int j = 0; j < G.count; ++j) {
+      const CeProblem& P = G.p[j];
+      const int rounds = G.share[j].count[cluster], pos = G.share[j].pos[cluster];
+      for (int r = 0; r < rounds; ++r) {
+        int mb, nb;
+        ce_tile(P, ce_round_tile(G.share[j], nclusters, pos, r), mb, nb);
+        const int m0 = mb * 256 + 128 * static_cast<int>(rank);
+        const int n0 = nb * 256 + 128 * static_cast<int>(rank);
+        for (int kb = 0; kb < P.num_k_blocks; ++kb) {
+          live = wait_live<false>(live, empty0 + 8u * s, ph ^ 1u, abort_flag, peer_abort);
+          const uint32_t fb = full_leader0 + 8u * s;
+          const int kc = kb * 64;
+          if (elect_one() && live) {
+            if (leader) mbar_arrive_expect_tx(full0 + 8u * s, 2 * kStage2Bytes);
+            if (P.a_mn) {
+              tma_load_2d_pair(st_a(s), &P.tmA, fb, m0, kc);
+              tma_load_2d_pair(st_a(s) + 8192, &P.tmA, fb, m0 + 64, kc);
+            } else {
+              tma_load_2d_pair(st_a(s), &P.tmA, fb, kc, m0);
+            }
+            if (P.b_mn) {
+              tma_load_2d_pair(st_b(s), &P.tmB, fb, n0, kc);
+              tma_load_2d_pair(st_b(s) + 8192, &P.tmB, fb, n0 + 64, kc);
+            } else {
+              tma_load_2d_pair(st_b(s), &P.tmB, fb, kc, n0);
+            }
           }
-          if (P.b_mn) {
-            tma_load_2d_pair(st_b(s), &P.tmB, fb, n0, kc);
-            tma_load_2d_pair(st_b(s) + 8192, &P.tmB, fb, n0 + 64, kc);
-          } else {
-            tma_load_2d_pair(st_b(s), &P.tmB, fb, kc, n0);
+          issued += live;
+          if (++s == kStages2) {
+            s = 0;
+            ph ^= 1u;
           }
-        }
-        issued += live;
-        if (++s == kStages2) {
-          s = 0;
-          ph ^= 1u;
         }
       }
     }
@@ -329,33 +344,36 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
       int s = 0;
       uint32_t ph = 0;
       uint32_t unit = 0;   // accumulations so far: unit u is in buffer u & 1
-      for (int tile = cluster; tile < num_tiles; tile += nclusters) {
-        const CeProblem& P = G.p[ce_problem(G, tile)];
+      for (int j = 0; j < G.count; ++j) {
+        const CeProblem& P = G.p[j];
+        const int rounds = G.share[j].count[cluster];
         const uint32_t idesc = make_idesc(1u, 1u, 1u, P.a_mn, P.b_mn, 256, 256);
         // a K step of 16 in the address field (16-byte units): K-major 32 B inside the
         // swizzled row, MN-major 16 K rows = 2 KB
         const uint64_t a_step = P.a_mn ? 128u : 2u, b_step = P.b_mn ? 128u : 2u;
         const uint32_t a_lbo = P.a_mn ? 8192u : 16u, b_lbo = P.b_mn ? 8192u : 16u;
-        for (int k0 = 0; k0 < P.num_k_blocks; k0 += P.part_blocks, ++unit) {
-          const uint32_t buf = unit & 1u;
-          const int end = min(k0 + P.part_blocks, P.num_k_blocks);
-          live = wait_live<false>(live, tempty0 + 8u * buf, ((unit >> 1) & 1u) ^ 1u, abort_flag, peer_abort);
-          tc_fence_after_sync();
-          const uint32_t d_tmem = tmem_base + buf * kBN;
-          for (int kb = k0; kb < end; ++kb) {
-            live = wait_live<false>(live, full0 + 8u * s, ph, abort_flag, peer_abort);
+        for (int r = 0; r < rounds; ++r) {
+          for (int k0 = 0; k0 < P.num_k_blocks; k0 += P.part_blocks, ++unit) {
+            const uint32_t buf = unit & 1u;
+            const int end = min(k0 + P.part_blocks, P.num_k_blocks);
+            live = wait_live<false>(live, tempty0 + 8u * buf, ((unit >> 1) & 1u) ^ 1u, abort_flag, peer_abort);
             tc_fence_after_sync();
-            if (elect_one() && live) {
-              const uint64_t ad = make_sw128_desc(st_a(s), a_lbo, 1024), bd = make_sw128_desc(st_b(s), b_lbo, 1024);
+            const uint32_t d_tmem = tmem_base + buf * kBN;
+            for (int kb = k0; kb < end; ++kb) {
+              live = wait_live<false>(live, full0 + 8u * s, ph, abort_flag, peer_abort);
+              tc_fence_after_sync();
+              if (elect_one() && live) {
+                const uint64_t ad = make_sw128_desc(st_a(s), a_lbo, 1024), bd = make_sw128_desc(st_b(s), b_lbo, 1024);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc_mma_f16_pair(d_tmem, ad + a_step * kk, bd + b_step * kk, idesc, kb > k0 || kk != 0 ? 1u : 0u);
-              tc_commit_pair(empty0 + 8u * s);   // frees this stage in both CTAs
-              if (kb + 1 == end) tc_commit_pair(tfull0 + 8u * buf);   // both CTAs' accumulators complete
-            }
-            if (++s == kStages2) {
-              s = 0;
-              ph ^= 1u;
+                for (int kk = 0; kk < 4; ++kk)
+                  tc_mma_f16_pair(d_tmem, ad + a_step * kk, bd + b_step * kk, idesc, kb > k0 || kk != 0 ? 1u : 0u);
+                tc_commit_pair(empty0 + 8u * s);   // frees this stage in both CTAs
+                if (kb + 1 == end) tc_commit_pair(tfull0 + 8u * buf);   // both CTAs' accumulators complete
+              }
+              if (++s == kStages2) {
+                s = 0;
+                ph ^= 1u;
+              }
             }
           }
         }
@@ -375,45 +393,48 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
     const uint32_t tempty_leader0 = map_to_rank(tempty0, 0);
     uint32_t unit = 0;
     bool ok = true;
-    for (int tile = cluster; tile < num_tiles && ok; tile += nclusters) {
-      const CeProblem& P = G.p[ce_problem(G, tile)];
-      int mb, nb;
-      ce_tile(P, tile - P.tile_begin, mb, nb);
-      const int row0 = mb * 256 + 128 * static_cast<int>(rank) + quad * 32;
-      const int n0 = nb * 256 + 128 * half;
-      CeAcc acc;
+    for (int j = 0; j < G.count && ok; ++j) {
+      const CeProblem& P = G.p[j];
+      const int rounds = G.share[j].count[cluster], pos = G.share[j].pos[cluster];
+      for (int r = 0; r < rounds && ok; ++r) {
+        int mb, nb;
+        ce_tile(P, ce_round_tile(G.share[j], nclusters, pos, r), mb, nb);
+        const int row0 = mb * 256 + 128 * static_cast<int>(rank) + quad * 32;
+        const int n0 = nb * 256 + 128 * half;
+        CeAcc acc;
 #pragma unroll 1
-      for (int k0 = 0; k0 < P.num_k_blocks; k0 += P.part_blocks, ++unit) {
-        const uint32_t buf = unit & 1u;
-        const bool got = mbar_wait(tfull0 + 8u * buf, (unit >> 1) & 1u, abort_flag);
-        if (!__all_sync(0xffffffffu, got)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        const uint32_t t_row = tmem_base + buf * kBN + static_cast<uint32_t>(128 * half) + (static_cast<uint32_t>(quad * 32) << 16);
-        if (k0 == 0) {
-          uint32_t(&r)[4][32] = reinterpret_cast<uint32_t(&)[4][32]>(acc);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(c * 32), r[c]);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(c * 32), r);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) acc[c][j] += __uint_as_float(r[j]);
+        for (int k0 = 0; k0 < P.num_k_blocks; k0 += P.part_blocks, ++unit) {
+          const uint32_t buf = unit & 1u;
+          const bool got = mbar_wait(tfull0 + 8u * buf, (unit >> 1) & 1u, abort_flag);
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
           }
+          tc_fence_after_sync();
+          const uint32_t t_row = tmem_base + buf * kBN + static_cast<uint32_t>(128 * half) + (static_cast<uint32_t>(quad * 32) << 16);
+          if (k0 == 0) {
+            uint32_t(&r)[4][32] = reinterpret_cast<uint32_t(&)[4][32]>(acc);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(c * 32), r[c]);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {   // 16 columns at a time: with 32 the registers do not last
+              uint32_t r[16];
+              tmem_ld_32x32b_x16(t_row + static_cast<uint32_t>(c * 16), r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) acc[c >> 1][16 * (c & 1) + j] += __uint_as_float(r[j]);
+            }
+          }
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8u * buf);   // the accumulator is free again
         }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8u * buf);   // the accumulator is free again
+        if (!ok) break;
+        if (P.mode == CE_LSE) ce_strip(G, P, acc, row0 + lane, n0, nb * 2 + half);
+        else ce_store(G, P, acc, stg, row0, n0, lane);
       }
-      if (!ok) break;
-      if (P.mode == CE_LSE) ce_strip(G, P, acc, row0 + lane, n0, nb * 2 + half);
-      else ce_store(G, P, acc, stg, row0, n0, lane);
     }
     if (!ok && lane == 0) {
       pair_abort(abort_flag, peer_abort);
