@@ -1,5 +1,5 @@
-// Products of up to 32 tokens with a large weight matrix, on the tensor cores with the
-// weights as the M operand:
+// Products of few tokens (blocks of up to 128, the logits up to 32) with a large weight matrix, on the
+// tensor cores with the weights as the M operand:
 //
 //   kFp8:  y[t, n]  = sum_k xq[t, k] 2^ex * wq[n, k] 2^ew   (kind::mxf8f6f4, block-scaled)
 //   else:  l[t, v]  = sum_k X[t, k] W[v, k]                  (kind::f16), reduced to strips of
@@ -10,10 +10,10 @@
 // 128 bytes) as far ahead as shared memory allows, and nothing between HBM and the tensor
 // core touches them: converting 8-bit codes in registers for warp MMAs (three times the
 // instructions) bounded an earlier version at 10.6 us for 22.5 MB against 3.5 of HBM time.
-// The tokens' operand has 16 or 32 rows, 128-byte swizzled. kFp8: made once per CTA, while
-// the first weights are on their way, and kept in shared memory; from bf16 it is quantised
-// here, so that a single token needs one launch. Logits: a K block of it comes with every K
-// block of weights (from L2; kept, it would take the room of the CTA's second ring).
+// The tokens' operand has 16 to 128 rows, 128-byte swizzled, and a K block of it comes with
+// every K block of weights (from L2), except for bf16 activations of up to 16 tokens (kFp8):
+// these are quantised here, once per CTA while the first weights are on their way, and kept
+// in shared memory, so that a single token needs one launch.
 // Two CTAs fit on an SM, so that the next call's are set up while this one's run.
 // Where there are fewer row blocks than SMs, a cluster of up to 8 CTAs splits K and adds its
 // partial sums through distributed shared memory in the order of the ranks; else a CTA
@@ -37,12 +37,9 @@ constexpr int kFewThreads = 192;      // producer, MMA, four epilogue warps
 constexpr int kFewMaxStages = 8;
 constexpr int kFewStageBytes = 128 * 128;
 constexpr int kFewSfBytes = 512;
-// Each of a K block's four MMAs has an accumulator of its own: with so few columns an MMA is
-// short against its latency, and four that add to the same columns wait for one another. The
-// logits' start afresh after 32 K blocks, that is 512 of K each.
-constexpr int kFewPartBlocks = 32;
+constexpr int kFewPartBlocks = kCePartBlocks;   // K blocks (64 of K) per accumulation of logits
 __host__ __device__ constexpr int few_parts(bool fp8, int blocks) {
-  return fp8 ? 4 : 4 * ((blocks + kFewPartBlocks - 1) / kFewPartBlocks);
+  return fp8 ? 1 : (blocks + kFewPartBlocks - 1) / kFewPartBlocks;
 }
 constexpr int kFewBarBytes = 256;
 
@@ -56,7 +53,7 @@ struct FewArgs {
   int x_bf16;                 // kFp8: quantise x here (e4m3)
   const uint32_t* ws;         // kFp8: [ceil(k / 512), n]
   int a_e5m2, b_e5m2;
-  int t, k, n;
+  int t, k, n;                // t: all tokens; blockIdx.y is the block of kTok (kFp8 codes only, else one)
   int num_k_blocks, num_row_blocks;
   int split;                  // CTAs of the cluster that share a row block
   int stages;
@@ -69,13 +66,18 @@ struct FewArgs {
   float* target_logit;
 };
 
-// Shared memory: ring of weights | ring of their scales (kFp8) or of the tokens' operand |
-// tokens' operand and its scales (kFp8) | barriers.
+// The partial sums of a split K (kTok x 128 fp32) go over the rings once their MMAs are done.
+constexpr size_t few_ring_bytes(bool fp8, int tok, int stages) {
+  return static_cast<size_t>(stages) * (kFewStageBytes + (fp8 ? kFewSfBytes : 0) + tok * 128);
+}
+static_assert(few_ring_bytes(true, 128, 3) >= 128 * 128 * 4 && 3 * kFewStageBytes >= 64 * 128 * 4, "exchange over the rings");
+// Shared memory: ring of weights | ring of their scales (kFp8) | tokens' operand, a ring too
+// or (quantised here) all K blocks of the CTA | its scales (kFp8) | barriers.
 __host__ __device__ constexpr int few_blocks_max(int num_k_blocks, int split) { return (num_k_blocks + split - 1) / split; }
-__host__ __device__ constexpr int few_ring2_bytes(bool fp8, int tok) { return fp8 ? kFewSfBytes : tok * 128; }
-__host__ __device__ constexpr size_t few_smem_bytes(bool fp8, int tok, int stages, int blocks) {
-  return 2048 + static_cast<size_t>(stages) * (kFewStageBytes + few_ring2_bytes(fp8, tok)) +
-         (fp8 ? static_cast<size_t>(blocks) * tok * 128 + static_cast<size_t>(blocks / 4 + 2) * kFewSfBytes : 0) + kFewBarBytes;
+__host__ __device__ constexpr size_t few_smem_bytes(bool fp8, bool kept, int tok, int stages, int blocks) {
+  return 2048 + static_cast<size_t>(stages) * (kFewStageBytes + (fp8 ? kFewSfBytes : 0)) +
+         static_cast<size_t>(kept ? blocks : stages) * tok * 128 + (fp8 ? static_cast<size_t>(blocks / 4 + 2) * kFewSfBytes : 0) +
+         kFewBarBytes;
 }
 
 __device__ __forceinline__ void tc_mma_mxf8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
@@ -95,9 +97,17 @@ __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
   return v;
 }
-template <int kTok>
-__device__ __forceinline__ void tmem_ld_tokens(uint32_t taddr, uint32_t (&r)[kTok]) {
-  if constexpr (kTok == 16) tmem_ld_32x32b_x16(taddr, r);
+__device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+template <int kCols>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[kCols]) {
+  if constexpr (kCols == 16) tmem_ld_32x32b_x16(taddr, r);
   else tmem_ld_32x32b_x32(taddr, r);
 }
 __device__ __forceinline__ int lane_id() { return static_cast<int>(threadIdx.x & 31); }
@@ -108,15 +118,17 @@ __device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
 // Scales of the tokens' operand of K blocks [kb0, kb1) and, from bf16, its codes, by all
 // threads of the CTA.
 template <int kTok>
-__device__ __forceinline__ void few_fp8_operand(const FewArgs& a, uint32_t sB, uint32_t sSfb, int kb0, int kb1) {
+__device__ __forceinline__ void few_fp8_operand(const FewArgs& a, uint32_t sB, uint32_t sSfb, int kb0, int kb1, int tok0) {
   const int blocks = kb1 - kb0, groups = (kb1 - 1) / 4 - kb0 / 4 + 1;
-  // scale word of token i of K group g at 512 g + 16 i; tokens past the last and the other
-  // columns are zeros
+  // scale word of token i of K group g at 512 g + 16 (i % 32) + 4 (i / 32), zero past the last
   for (int i = threadIdx.x; i < groups * 32; i += kFewThreads) {
-    const int tok = i & 31;
-    uint32_t w = 0;
-    if (!a.x_bf16 && tok < a.t) w = __ldg(a.xs + static_cast<int64_t>(kb0 / 4 + (i >> 5)) * a.t + tok);
-    st_shared_v4(sSfb + 16u * static_cast<uint32_t>(i), w, 0, 0, 0);
+    uint32_t w[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int tok = tok0 + 32 * c + (i & 31);
+      w[c] = !a.x_bf16 && tok < a.t ? __ldg(a.xs + static_cast<int64_t>(kb0 / 4 + (i >> 5)) * a.t + tok) : 0u;
+    }
+    st_shared_v4(sSfb + 16u * static_cast<uint32_t>(i), w[0], w[1], w[2], w[3]);
   }
   if (!a.x_bf16) return;
   auto at = [&](int b, int tok, int j) { return sB + static_cast<uint32_t>((b * kTok + tok) * 128 + ((j ^ (tok & 7)) * 16)); };
@@ -167,12 +179,13 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   const int max_blocks = few_blocks_max(a.num_k_blocks, a.split);
-  const uint32_t sRing = base, sRing2 = sRing + static_cast<uint32_t>(a.stages * kFewStageBytes);
-  const uint32_t sB = (sRing2 + static_cast<uint32_t>(a.stages * few_ring2_bytes(kFp8, kTok)) + 1023u) & ~1023u;
-  const uint32_t sSfb = sB + (kFp8 ? static_cast<uint32_t>(max_blocks * kTok * 128) : 0u);
+  const bool kept = kFp8 && a.x_bf16;
+  const uint32_t sRing = base, sSfa = sRing + static_cast<uint32_t>(a.stages * kFewStageBytes);
+  const uint32_t sB = (sSfa + (kFp8 ? static_cast<uint32_t>(a.stages * kFewSfBytes) : 0u) + 1023u) & ~1023u;
+  const uint32_t sSfb = sB + static_cast<uint32_t>((kept ? max_blocks : a.stages) * kTok * 128);
   const uint32_t bar0 = sSfb + (kFp8 ? static_cast<uint32_t>((max_blocks / 4 + 2) * kFewSfBytes) : 0u);
   const uint32_t full0 = bar0, empty0 = bar0 + 8u * kFewMaxStages, tfull0 = empty0 + 8u * kFewMaxStages, tempty0 = tfull0 + 16u;
-  const uint32_t xfull = tempty0 + 16u, slot = xfull + 8u;
+  const uint32_t slot = tempty0 + 16u;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem_raw + (slot - raw));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + (slot - raw) + 4);
 
@@ -181,6 +194,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
   const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * a.num_k_blocks / a.split);
   const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * a.num_k_blocks / a.split);
   const int blk0 = blockIdx.x / a.split, blk_step = gridDim.x / a.split;
+  const int tok0 = blockIdx.y * kTok, toks = min(kTok, a.t - tok0);   // this CTA's tokens
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(full0 + 8u * s, 1);
@@ -190,10 +204,9 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
       mbar_init(tfull0 + 8u * b, 1);
       mbar_init(tempty0 + 8u * b, 4);   // epilogue warps
     }
-    mbar_init(xfull, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    if (!kFp8 || !a.x_bf16) tma_prefetch_desc(&M.x);
+    if (!kept) tma_prefetch_desc(&M.x);
     for (int c = 0; c < (kFp8 ? 4 : 1); ++c) tma_prefetch_desc(&M.w[c]);
   }
   if (warp == 1) {
@@ -212,20 +225,19 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
   const uint32_t own_abort = map_to_rank(slot + 4u, static_cast<uint32_t>(rank));
   auto issue = [&](int blk, int kb) {   // K block kb of row block blk into stage s
     const int row0 = blk * 128;
-    const uint32_t more = kFp8 ? 4u * static_cast<uint32_t>(min(128, a.n - row0)) : static_cast<uint32_t>(kTok * 128);
-    const uint32_t dst2 = sRing2 + static_cast<uint32_t>(s * few_ring2_bytes(kFp8, kTok));
+    const uint32_t sf_bytes = kFp8 ? 4u * static_cast<uint32_t>(min(128, a.n - row0)) : 0u;
     live = wait_live<false>(live, empty0 + 8u * s, ph ^ 1u, abort_flag, own_abort);
     if (elect_one() && live) {
       const uint32_t fb = full0 + 8u * s, dst = sRing + static_cast<uint32_t>(s * kFewStageBytes);
-      mbar_arrive_expect_tx(fb, kFewStageBytes + more);
+      mbar_arrive_expect_tx(fb, kFewStageBytes + sf_bytes + (kept ? 0u : static_cast<uint32_t>(kTok * 128)));
       if constexpr (kFp8) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) tma_load_2d(dst + 4096u * c, &M.w[c], fb, kb * 128, row0 / 4);
-        bulk_load_1d(dst2, a.ws + static_cast<int64_t>(kb >> 2) * a.n + row0, more, fb);
+        bulk_load_1d(sSfa + static_cast<uint32_t>(s * kFewSfBytes), a.ws + static_cast<int64_t>(kb >> 2) * a.n + row0, sf_bytes, fb);
       } else {
         tma_load_2d(dst, &M.w[0], fb, kb * 64, row0);
-        tma_load_2d(dst2, &M.x, fb, kb * 64, 0);
       }
+      if (!kept) tma_load_2d(sB + static_cast<uint32_t>(s * kTok * 128), &M.x, fb, kb * (kFp8 ? 128 : 64), tok0);
     }
     issued += live;
     if (++s == a.stages) {
@@ -236,15 +248,9 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
   // the first ring of weights is on its way while all warps make the tokens' operand
   const int ahead = kFp8 ? min(a.stages, kb1 - kb0) : 0;
   if constexpr (kFp8) {
-    if (warp == 0) {
-      if (!a.x_bf16 && elect_one()) {   // codes as they are: rows past the last token are zeros
-        mbar_arrive_expect_tx(xfull, static_cast<uint32_t>((kb1 - kb0) * kTok * 128));
-        for (int b = 0; b < kb1 - kb0; ++b) tma_load_2d(sB + static_cast<uint32_t>(b * kTok * 128), &M.x, xfull, (kb0 + b) * 128, 0);
-      }
-      __syncwarp();
+    if (warp == 0)
       for (int i = 0; i < ahead; ++i) issue(blk0, kb0 + i);
-    }
-    few_fp8_operand<kTok>(a, sB, sSfb, kb0, kb1);
+    few_fp8_operand<kTok>(a, sB, sSfb, kb0, kb1, tok0);
     fence_proxy_async_smem();
     __syncthreads();
   }
@@ -253,7 +259,6 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
     // ------------------------------------------------------------- TMA producer
     for (int blk = blk0; blk < a.num_row_blocks; blk += blk_step)
       for (int kb = blk == blk0 ? kb0 + ahead : kb0; kb < kb1; ++kb) issue(blk, kb);
-    if (kFp8 && !a.x_bf16 && elect_one() && !mbar_wait_plain(xfull, 0)) atomicOr(&g_device_status, DEV_ST_TIMEOUT_DRAIN);
     if (!live && elect_one()) {
       atomicOr(&g_device_status, DEV_ST_TIMEOUT_PRODUCER);
       const uint32_t st = static_cast<uint32_t>(a.stages), first = issued > st ? issued - st : 0;
@@ -264,7 +269,6 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
     // ------------------------------------------------------------- MMA issuer
     const uint32_t idesc0 = kFp8 ? make_idesc_mxf8(a.a_e5m2, a.b_e5m2, kTok, 128, 0) : make_idesc(1u, 1u, 1u, 0u, 0u, kTok, 128);
     uint32_t unit = 0, count = 0;
-    if (kFp8 && !a.x_bf16) live = wait_live<false>(live, xfull, 0, abort_flag, own_abort);
     for (int blk = blk0; blk < a.num_row_blocks; blk += blk_step, ++unit) {
       const uint32_t buf = a.bufs == 2 ? unit & 1u : 0u, uph = a.bufs == 2 ? unit >> 1 : unit;
       live = wait_live<false>(live, tempty0 + 8u * buf, (uph & 1u) ^ 1u, abort_flag, own_abort);
@@ -274,25 +278,23 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
         tc_fence_after_sync();
         if (elect_one() && live) {
           const int b = kb - kb0;
-          const int part = kFp8 ? 0 : 4 * (b / kFewPartBlocks);
-          const uint32_t add = (kFp8 ? b == 0 : b % kFewPartBlocks == 0) ? 0u : 1u;
+          const int part = kFp8 ? 0 : b / kFewPartBlocks;
+          const uint32_t add = (kFp8 ? b == 0 : b % kFewPartBlocks == 0) ? 0u : 1u;   // first MMA of an accumulation
           const uint32_t d = tmem_base + (buf * a.parts + part) * kTok;
           const uint64_t ad = make_sw128_desc(sRing + static_cast<uint32_t>(s * kFewStageBytes), 16, 1024);
-          const uint64_t bd = make_sw128_desc(kFp8 ? sB + static_cast<uint32_t>(b * kTok * 128)
-                                                   : sRing2 + static_cast<uint32_t>(s * kTok * 128), 16, 1024);
+          const uint64_t bd = make_sw128_desc(sB + static_cast<uint32_t>((kept ? b : s) * kTok * 128), 16, 1024);
           if constexpr (kFp8) {
             // eight slots of scale columns: a slot's last user was at least a ring of stages ago
             const uint32_t col = tmem_base + a.sf_col0 + 8u * (count % kFewMaxStages);
-            tc_cp_32x128b(col, make_sf_desc(sRing2 + static_cast<uint32_t>(s * kFewSfBytes)));
+            tc_cp_32x128b(col, make_sf_desc(sSfa + static_cast<uint32_t>(s * kFewSfBytes)));
             tc_cp_32x128b(col + 4u, make_sf_desc(sSfb + static_cast<uint32_t>((kb / 4 - kb0 / 4) * kFewSfBytes)));
             const uint32_t id = static_cast<uint32_t>(kb & 3), idesc = idesc0 | id << 4 | id << 29;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc_mma_mxf8(d + static_cast<uint32_t>(kk * kTok), ad + 2u * kk, bd + 2u * kk, idesc, col, col + 4u, add);
+              tc_mma_mxf8(d, ad + 2u * kk, bd + 2u * kk, idesc, col, col + 4u, kk != 0 ? 1u : add);
           } else {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_f16(d + static_cast<uint32_t>(kk * kTok), ad + 2u * kk, bd + 2u * kk, idesc0, add);
+            for (int kk = 0; kk < 4; ++kk) tc_mma_f16(d, ad + 2u * kk, bd + 2u * kk, idesc0, kk != 0 ? 1u : add);
           }
           tc_commit(empty0 + 8u * s);
           if (kb + 1 == kb1) tc_commit(tfull0 + 8u * buf);
@@ -318,50 +320,56 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
       }
       tc_fence_after_sync();
       const uint32_t t_row = tmem_base + buf * a.parts * kTok + (static_cast<uint32_t>(quad * 32) << 16);
-      uint32_t r[kTok];
-      float v[kTok];
-      tmem_ld_tokens<kTok>(t_row, r);
-      tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < kTok; ++i) v[i] = __uint_as_float(r[i]);
-      const int parts = few_parts(kFp8, kb1 - kb0);
-      for (int p = 1; p < parts; ++p) {
-        tmem_ld_tokens<kTok>(t_row + static_cast<uint32_t>(p * kTok), r);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) v[i] += __uint_as_float(r[i]);
-      }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tempty0 + 8u * buf);
       const int local = kFp8 ? 4 * lane + quad : quad * 32 + lane;   // the weight row of this thread
       const int row = blk * 128 + local;
-      if (a.split > 1) {   // the cluster's only row block: partial sums for the exchange below, in the ring
+      const int parts = few_parts(kFp8, kb1 - kb0);
+      constexpr int kCols = kTok < 32 ? kTok : 32;
+#pragma unroll 1
+      for (int c0 = 0; c0 < kTok; c0 += kCols) {   // tokens, 16 or 32 at a time
+        uint32_t r[kCols];
+        float v[kCols];
+        tmem_ld_cols<kCols>(t_row + static_cast<uint32_t>(c0), r);
+        tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < kTok; ++i)
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sRing + static_cast<uint32_t>((i * 128 + local) * 4)), "f"(v[i]) : "memory");
-      } else if constexpr (kFp8) {
+        for (int i = 0; i < kCols; ++i) v[i] = __uint_as_float(r[i]);
+        for (int p = 1; p < parts; ++p) {
+          tmem_ld_cols<kCols>(t_row + static_cast<uint32_t>(p * kTok + c0), r);
+          tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < kTok; ++i)
-          if (i < a.t && row < a.n) {
-            const int64_t off = static_cast<int64_t>(i) * a.n + row;
-            if (a.y_f32) static_cast<float*>(a.y)[off] = v[i];
-            else static_cast<__nv_bfloat16*>(a.y)[off] = __float2bfloat16_rn(v[i]);
-          }
-      } else {   // one strip of 32 rows per warp
+          for (int i = 0; i < kCols; ++i) v[i] += __uint_as_float(r[i]);
+        }
+        if (c0 + kCols == kTok) {   // the accumulators are free again
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tempty0 + 8u * buf);
+        }
+        if (a.split > 1) {   // the cluster's only row block: partial sums for the exchange below, in the rings
 #pragma unroll
-        for (int i = 0; i < kTok; ++i)
-          if (i < a.t) {
-            if (row < a.n && a.targets[i] == row) a.target_logit[i] = v[i];
-            const float l2 = row < a.n ? v[i] * kLog2e : -INFINITY;
-            float m = l2;
+          for (int i = 0; i < kCols; ++i)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sRing + static_cast<uint32_t>(((c0 + i) * 128 + local) * 4)), "f"(v[i]) : "memory");
+        } else if constexpr (kFp8) {
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-            float e = row < a.n ? ex2(fmaf(v[i], kLog2e, -m)) : 0.f;
+          for (int i = 0; i < kCols; ++i)
+            if (c0 + i < toks && row < a.n) {
+              const int64_t off = static_cast<int64_t>(tok0 + c0 + i) * a.n + row;
+              if (a.y_f32) static_cast<float*>(a.y)[off] = v[i];
+              else static_cast<__nv_bfloat16*>(a.y)[off] = __float2bfloat16_rn(v[i]);
+            }
+        } else {   // one strip of 32 rows per warp
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) e += __shfl_xor_sync(0xffffffffu, e, off);
-            if (lane == 0) a.strips[static_cast<int64_t>(blk * 4 + quad) * a.t + i] = make_float2(m, e);
-          }
+          for (int i = 0; i < kCols; ++i)
+            if (i < a.t) {
+              if (row < a.n && a.targets[i] == row) a.target_logit[i] = v[i];
+              const float l2 = row < a.n ? v[i] * kLog2e : -INFINITY;
+              float m = l2;
+#pragma unroll
+              for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+              float e = row < a.n ? ex2(fmaf(v[i], kLog2e, -m)) : 0.f;
+#pragma unroll
+              for (int off = 16; off > 0; off >>= 1) e += __shfl_xor_sync(0xffffffffu, e, off);
+              if (lane == 0) a.strips[static_cast<int64_t>(blk * 4 + quad) * a.t + i] = make_float2(m, e);
+            }
+        }
       }
     }
     if (!ok && lane == 0) {
@@ -374,20 +382,30 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
   if (a.split > 1) {
     cluster_sync();   // every CTA's partial sums are in its shared memory
     const int per = 128 / a.split, blk = blk0;   // rows of the block that this CTA finishes
+    auto at = [&](int i, int local, int c) {   // rank c's partial sum
+      return map_to_rank(sRing + static_cast<uint32_t>((i * 128 + local) * 4), static_cast<uint32_t>(c));
+    };
     auto total = [&](int i, int local) {   // ranks in order
       float v = 0.f;
-      for (int c = 0; c < a.split; ++c)
-        v += ld_shared_cluster_f32(map_to_rank(sRing + static_cast<uint32_t>((i * 128 + local) * 4), static_cast<uint32_t>(c)));
+      for (int c = 0; c < a.split; ++c) v += ld_shared_cluster_f32(at(i, local, c));
       return v;
     };
     if constexpr (kFp8) {
-      for (int e = threadIdx.x; e < a.t * per; e += kFewThreads) {
-        const int i = e / per, local = rank * per + e % per, row = blk * 128 + local;
+      const int quads = per / 4;   // four rows at a time (n % 16 == 0)
+      for (int e = threadIdx.x; e < toks * quads; e += kFewThreads) {
+        const int i = e / quads, local = rank * per + 4 * (e % quads), row = blk * 128 + local;
         if (row < a.n) {
-          const float v = total(i, local);
-          const int64_t off = static_cast<int64_t>(i) * a.n + row;
-          if (a.y_f32) static_cast<float*>(a.y)[off] = v;
-          else static_cast<__nv_bfloat16*>(a.y)[off] = __float2bfloat16_rn(v);
+          float4 p[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c < a.split) p[c] = ld_shared_cluster_v4(at(i, local, c));
+          float4 v = p[0];
+#pragma unroll
+          for (int c = 1; c < 8; ++c)
+            if (c < a.split) v = make_float4(v.x + p[c].x, v.y + p[c].y, v.z + p[c].z, v.w + p[c].w);
+          const int64_t off = static_cast<int64_t>(tok0 + i) * a.n + row;
+          if (a.y_f32) *reinterpret_cast<float4*>(static_cast<float*>(a.y) + off) = v;
+          else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.y) + off) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
         }
       }
     } else {

@@ -157,7 +157,7 @@ size_t fp8_scale_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>(
 
 // ------------------------------------------------------------------ few tokens
 
-constexpr int64_t kFewTokens = 32;           // rows of the tokens' operand at most
+constexpr int64_t kFewFp8Tokens = 512, kFewCeTokens = 32, kFewQuantised = 16;
 constexpr size_t kFewSmemTwo = 113 * 1024;   // two CTAs on an SM
 constexpr size_t kFewSmemOne = 226 * 1024;
 
@@ -165,23 +165,27 @@ struct FewPlan {
   int split, stages, tok;
   size_t smem;
 };
-// How a product of t <= 32 tokens is spread: K is split over a cluster while row blocks x
-// split stays within two CTAs an SM and every CTA keeps two K blocks; then as many stages
-// as fit beside the tokens' operand, two CTAs on an SM if that leaves four stages. False if
-// the operand of a CTA does not fit even when split by 8 (then the pair product runs).
-bool few_plan(bool fp8, int64_t t, int64_t num_k_blocks, int64_t row_blocks, int sms, FewPlan* p) {
-  if (t > kFewTokens || num_k_blocks > 4096) return false;
-  const int tok = t <= 16 ? 16 : 32;
+// How a product of few tokens is spread: K is split over a cluster while row blocks x split
+// stays within two CTAs an SM and every CTA keeps two K blocks; then as many stages as fit
+// beside the tokens' operand (`kept`: all of its K blocks, quantised in the kernel), two
+// CTAs on an SM if that leaves three stages. Beyond 128 tokens only where the 128 x 128 tiles
+// are fewer than half the SMs (129 tokens 11008 -> 2048: the pair product, whose few tiles
+// walk over all of K, takes 36.5 us). False if it does not fit even when split by 8.
+bool few_plan(bool fp8, bool kept, int64_t t, int64_t num_k_blocks, int64_t row_blocks, int sms, FewPlan* p) {
+  if (t > (kept ? kFewQuantised : fp8 ? kFewFp8Tokens : kFewCeTokens) || num_k_blocks > 4096) return false;
+  const int tok = t <= 16 ? 16 : t <= 32 ? 32 : t <= 64 ? 64 : 128;
+  const int64_t blocks_mn = row_blocks * ((t + tok - 1) / tok);
+  if (t > 128 && 2 * blocks_mn > sms) return false;   // the pair product fills the SMs
   int split = 1;
-  while (split < 8 && row_blocks * split * 2 <= 2 * int64_t(sms) && num_k_blocks >= 4 * split) split *= 2;
+  while (split < 8 && blocks_mn * split * 2 <= 2 * int64_t(sms) && num_k_blocks >= 4 * split) split *= 2;
   for (; split <= 8; split *= 2) {
     const int blocks = bl::few_blocks_max(static_cast<int>(num_k_blocks), split);
     if (bl::few_parts(fp8, blocks) * tok > 256) continue;   // TMEM
     for (const size_t room : {kFewSmemTwo, kFewSmemOne}) {
       int stages = bl::kFewMaxStages;
-      while (stages >= 4 && bl::few_smem_bytes(fp8, tok, stages, blocks) > room) --stages;
-      if (stages < 4) continue;
-      *p = {split, stages, tok, bl::few_smem_bytes(fp8, tok, stages, blocks)};
+      while (stages >= 3 && bl::few_smem_bytes(fp8, kept, tok, stages, blocks) > room) --stages;
+      if (stages < 3) continue;
+      *p = {split, stages, tok, bl::few_smem_bytes(fp8, kept, tok, stages, blocks)};
       return true;
     }
   }
@@ -216,29 +220,29 @@ bl_status launch_few(const bl::FewMaps& M, bl::FewArgs& a, const FewPlan& p, cud
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   head_config(cfg, attr, grid, bl::kFewThreads, p.smem, p.split, st);
+  cfg.gridDim.y = static_cast<unsigned>((a.t + kTok - 1) / kTok);
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, M, a);
   if (e != cudaSuccess) return cuda_fail(e, "few tokens launch");
   return BL_OK;
 }
 
-// Tokens up to which the product quantises bf16 activations itself, where their codes fit
-// whatever n is (a plan for one row block has the largest split, and more row blocks may
+// Whether the product quantises bf16 activations itself: up to 16 tokens, where their codes
+// fit whatever n is (a plan for one row block has the largest split, and more row blocks may
 // have less of it, but never less than they need). More tokens go through the quantiser:
 // every CTA would repeat their work (11008 -> 2048: 16 tokens 11 us either way, 32 tokens
 // 25.6 us in the product, 20 through the quantiser).
-constexpr int64_t kFewQuantised = 16;
 bool few_quantises(int64_t t, int64_t k_in) {
   FewPlan p;
-  return t <= kFewQuantised && few_plan(true, t, (k_in + 127) / 128, 1, 148, &p);
+  return few_plan(true, true, t, (k_in + 127) / 128, 1, 148, &p);
 }
 
-// y of up to 32 tokens; *done is false (nothing enqueued) where the plan does not fit.
+// y of few tokens; *done is false (nothing enqueued) where the plan does not fit.
 bl_status enqueue_fp8_few(const void* x, bool x_bf16, const uint8_t* x_scales, bool x5, const uint8_t* w_q,
                           const uint8_t* w_scales, bool w5, int64_t t, int64_t k, int64_t n, void* y, bool f32,
                           cudaStream_t st, bool* done) {
   *done = false;
   FewPlan p;
-  if (!few_plan(true, t, (k + 127) / 128, (n + 127) / 128, device_sm_count(), &p)) return BL_OK;
+  if (!few_plan(true, x_bf16, t, (k + 127) / 128, (n + 127) / 128, device_sm_count(), &p)) return BL_OK;
   bl::FewMaps M{};
   for (int c = 0; c < 4; ++c)   // weight rows c, c + 4, ... (n % 16 == 0)
     if (bl_status s = make_map_strided(&M.w[c], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w_q + c * k, k, n / 4, 4 * k, 128, 32,
@@ -261,7 +265,12 @@ bl_status enqueue_fp8_few(const void* x, bool x_bf16, const uint8_t* x_scales, b
   a.y = y;
   a.y_f32 = f32 ? 1 : 0;
   *done = true;
-  return p.tok == 16 ? launch_few<true, 16>(M, a, p, st) : launch_few<true, 32>(M, a, p, st);
+  switch (p.tok) {
+    case 16: return launch_few<true, 16>(M, a, p, st);
+    case 32: return launch_few<true, 32>(M, a, p, st);
+    case 64: return launch_few<true, 64>(M, a, p, st);
+    default: return launch_few<true, 128>(M, a, p, st);
+  }
 }
 
 // ------------------------------------------------------------------ linear cross entropy
@@ -397,7 +406,7 @@ struct CeFwdSpace {
 CeFwdSpace ce_fwd_space(int64_t t, int64_t v) {
   CeFwdSpace s{};
   // 128 columns a strip; for few tokens as few as 16, an eighth of a row block
-  const size_t per_t = t <= kFewTokens ? 8 * static_cast<size_t>((v + 127) / 128) : 2 * static_cast<size_t>((v + 255) / 256);
+  const size_t per_t = t <= kFewCeTokens ? 8 * static_cast<size_t>((v + 127) / 128) : 2 * static_cast<size_t>((v + 255) / 256);
   const size_t n = per_t * static_cast<size_t>(t) * sizeof(float2);
   s.strips = 0;
   s.target_logit = round256(n);
@@ -561,7 +570,7 @@ bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const in
   float* target_logit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.target_logit);
   int num_strips = 0;
   FewPlan plan;
-  if (few_plan(false, t, k_in / 64, (v + 127) / 128, device_sm_count(), &plan)) {
+  if (few_plan(false, false, t, k_in / 64, (v + 127) / 128, device_sm_count(), &plan)) {
     bl::FewMaps M{};
     if (bl_status s = ce_operand(&M.w[0], w, k_in, v, k_in, false)) return s;
     if (bl_status s = make_map(&M.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, k_in, t, 64, plan.tok)) return s;

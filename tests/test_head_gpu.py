@@ -133,7 +133,7 @@ def test_fwd(t, k, n):
 # few tokens: row blocks that one CTA walks over, K split by 2, 4 and 8, a ragged last row
 # block, the widest K that still fits beside the weights and ones that do not
 FEW_SHAPES = [(1, 192, 40016), (3, 64, 19008), (16, 2048, 11008), (32, 2048, 4112), (17, 1088, 2064), (8, 11008, 2064),
-              (1, 320, 16), (20, 24640, 48), (20, 39936, 32), (8, 131072, 16)]
+              (1, 320, 16), (20, 24640, 48), (20, 39936, 32), (8, 131072, 16), (129, 1088, 48), (300, 4096, 144), (512, 576, 272)]
 
 
 @pytest.mark.parametrize("t,k,n", FEW_SHAPES)
