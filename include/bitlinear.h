@@ -423,13 +423,15 @@ bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const in
 /*
  * Its gradients, given lse of the forward call and grad_loss [t] fp32, the derivative of
  * the total with respect to each loss[t]; either output may be NULL:
- *   dl[t, v] = (exp(l[t, v] - lse[t]) - [v == targets[t]]) * grad_loss[t], rounded to bf16
+ *   dl[t, v] = (exp(l[t, v] - lse[t]) - [v == targets[t]]) * grad_loss[t]
  *   grad_x [t, k_in] bf16 = dl . w,   grad_w [v, k_in] (grad_w_dtype) = dl^T . x.
- * The logits are computed again, one piece of the vocabulary after another, so the
- * workspace holds one piece of dl (and an fp32 sum of grad_x), never [t, v]. Sums are
- * fp32 and in a fixed order. An x row without a loss must still be finite.
+ * dl is rounded to bf16 for these products, relative to the largest |grad_loss|. A token
+ * without a loss contributes nothing, whatever its x, lse and grad_loss hold.
+ * The logits are computed again, one piece of the vocabulary after another; the workspace
+ * holds two pieces of dl, an fp32 sum of grad_x and a copy of x, and all of dl [t, v] only
+ * where that is below 64 MB. Sums are fp32 and in a fixed order.
  */
-size_t bitlinear_linear_ce_bwd_workspace_size(int64_t t, int64_t k_in, int64_t v, int want_grad_x);
+size_t bitlinear_linear_ce_bwd_workspace_size(int64_t t, int64_t k_in, int64_t v, int want_grad_x, int want_grad_w);
 bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const int64_t* targets, const float* lse,
                                   const float* grad_loss, int64_t t, int64_t k_in, int64_t v, uint16_t* grad_x,
                                   void* grad_w, int grad_w_dtype, void* workspace, size_t workspace_bytes, void* stream);

@@ -14,14 +14,18 @@
 //
 // A cluster of two CTAs computes one tile of 256 rows x kHalves * n_half columns (n_half a
 // multiple of 32, at most 224). Why 224 and not the 256 of the other pair kernels: the
-// scales live in TMEM beside the accumulators, 2 x 224 + 64 = 512 columns. What bounds the
-// product is the operands' way from L2 to the SMs (about 40 bytes a cycle and SM), so
+// scales live in TMEM beside the accumulators, 2 x 224 + 64 = 512 columns.
 //   kHalves = 2 (the wide tile): both accumulators belong to one tile, whose two column
 //     halves share every load of A: 44 KB per 128 of K for 896 MMA cycles. With no
 //     accumulator to spare, the next tile's first four K blocks run on half 0 alone while
 //     the epilogue still drains half 1, then on half 1, so the tensor cores do not wait.
 //   kHalves = 1: one accumulator per tile, the other one drained meanwhile; 30 KB per 448
-//     MMA cycles. For products with too few wide tiles to fill the SMs evenly.
+//     MMA cycles. For products with too few wide tiles to fill the SMs evenly, or short K.
+// What bounds it: 8192 tokens, 2048 -> 11008 take 133-145 us (2.5-2.8 PFLOP/s), the loads
+// alone 84, the MMAs alone 110, and with all-zero operands the whole kernel 126 at full
+// clock, while with real ones the card runs into its 1000 W (1432 MHz in a long loop, 168
+// us); cuBLAS's 8-bit product of that shape with one scale per tensor: 177 us, 166 in the
+// long loop. The int8 pair product, one MMA kind without scales, takes 121.
 //
 // Scales. A 32-bit word holds a row's bytes of four consecutive K blocks ([K / 512, rows, 4]
 // in memory), so one copy serves 16 MMAs per half, which select their byte by the
@@ -48,7 +52,7 @@ constexpr int kF8BBytes = kF8MaxN / 2 * 128;              // and of its columns 
 template <int kHalves>
 struct F8Stage {
   static constexpr int kCount = kHalves == 2 ? 4 : 6;
-    static constexpr int kBytes = kF8ABytes + kHalves * kF8BBytes;
+  static constexpr int kBytes = kF8ABytes + kHalves * kF8BBytes;
   static constexpr int kSfGroups = 1 + 2 * kHalves;       // 128-row groups of scales: A, then B by halves
   static constexpr int kSfSlots = kHalves == 2 ? 3 : 4;
 };

@@ -82,10 +82,12 @@ struct Fp8Operand {
 };
 
 // Tiles of the pair product: one or two accumulators of a multiple of 32 columns, whichever
-// has the least modelled time. Per 128 of K a tile costs the larger of its MMAs (2 cycles
+// has the least modelled time in cycles. Per 128 of K a tile costs the larger of its MMAs (2
 // a column) and its operand loads (128 rows of A and half its columns of B, 128 bytes each,
-// at about 40 bytes a cycle), so narrow tiles pay for the rows of A that they drag along;
-// whole waves of tiles over the pairs decide.
+// at about 40 bytes a cycle); besides, a narrow tile costs about 1500 and a wide one, whose
+// two accumulators are drained one after the other, 5000; whole waves of tiles over the
+// pairs decide. Over 16 shapes (300 to 16384 rows, K 896 to 11008) the choice was within 3%
+// of the best of all 14 tiles; the widest tile alone would be up to 1.5 times slower.
 struct Fp8Tiles {
   int halves, n_half;
 };
@@ -98,7 +100,7 @@ Fp8Tiles fp8_tiles(int64_t m, int64_t n, int64_t k_blocks, int pairs) {
       const int64_t cols = int64_t(halves) * w;
       const int64_t waves = (mb * ((n + cols - 1) / cols) + pairs - 1) / pairs;
       const double mma = 2.0 * cols, load = (128 + cols / 2) * 128.0 / 40.0;
-      const double cost = double(waves) * (double(k_blocks) * (mma > load ? mma : load) + 1500.0);
+      const double cost = double(waves) * (double(k_blocks) * (mma > load ? mma : load) + (halves == 2 ? 5000.0 : 1500.0));
       if (cost <= best_cost) {
         best = {halves, w};
         best_cost = cost;
@@ -157,7 +159,7 @@ size_t fp8_scale_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>(
 
 // ------------------------------------------------------------------ few tokens
 
-constexpr int64_t kFewFp8Tokens = 512, kFewCeTokens = 32, kFewQuantised = 16;
+constexpr int64_t kFewFp8Tokens = 4096, kFewCeTokens = 32, kFewQuantised = 16;
 constexpr size_t kFewSmemTwo = 113 * 1024;   // two CTAs on an SM
 constexpr size_t kFewSmemOne = 226 * 1024;
 
@@ -169,13 +171,14 @@ struct FewPlan {
 // stays within two CTAs an SM and every CTA keeps two K blocks; then as many stages as fit
 // beside the tokens' operand (`kept`: all of its K blocks, quantised in the kernel), two
 // CTAs on an SM if that leaves three stages. Beyond 128 tokens only where the 128 x 128 tiles
-// are fewer than half the SMs (129 tokens 11008 -> 2048: the pair product, whose few tiles
-// walk over all of K, takes 36.5 us). False if it does not fit even when split by 8.
+// are fewer than half the SMs and K is long, so that the pair product's few tiles walk over
+// all of K (1024 tokens 11008 -> 1024: 18.5 us here, 38.9 on the pair product; 896 -> 896:
+// 11.0 and 7.3). False if it does not fit even when split by 8.
 bool few_plan(bool fp8, bool kept, int64_t t, int64_t num_k_blocks, int64_t row_blocks, int sms, FewPlan* p) {
   if (t > (kept ? kFewQuantised : fp8 ? kFewFp8Tokens : kFewCeTokens) || num_k_blocks > 4096) return false;
   const int tok = t <= 16 ? 16 : t <= 32 ? 32 : t <= 64 ? 64 : 128;
   const int64_t blocks_mn = row_blocks * ((t + tok - 1) / tok);
-  if (t > 128 && 2 * blocks_mn > sms) return false;   // the pair product fills the SMs
+  if (t > 128 && (2 * blocks_mn > sms || num_k_blocks < 32)) return false;
   int split = 1;
   while (split < 8 && blocks_mn * split * 2 <= 2 * int64_t(sms) && num_k_blocks >= 4 * split) split *= 2;
   for (; split <= 8; split *= 2) {
@@ -276,8 +279,9 @@ bl_status enqueue_fp8_few(const void* x, bool x_bf16, const uint8_t* x_scales, b
 // ------------------------------------------------------------------ linear cross entropy
 
 // dl of the whole vocabulary up to kCeWholeBytes, else of a piece of kCePieceBytes at most
-// (8192 x 2048 x 65536 backward: pieces of 32 MB 5.13 ms, 64 MB 5.00, 128 MB 4.55, 256 MB 4.61).
-constexpr int64_t kCeWholeBytes = int64_t(64) << 20, kCePieceBytes = int64_t(128) << 20;
+// (8192 x 2048 x 65536 backward: pieces of 32 MB 5.13 ms, 64 MB 5.00, 128 MB 4.55, 256 MB 4.61; 112 MB keeps the
+// workspace below a third of the logits there).
+constexpr int64_t kCeWholeBytes = int64_t(64) << 20, kCePieceBytes = int64_t(112) << 20;
 
 // Vocabulary rows per piece of the backward pass: all of them, or a multiple of 256 and a
 // quarter of the vocabulary at most, so that the two pieces held at a time stay well below
@@ -414,14 +418,15 @@ CeFwdSpace ce_fwd_space(int64_t t, int64_t v) {
   return s;
 }
 struct CeBwdSpace {
-  size_t grad_max, dl[2], acc, total;
+  size_t grad_max, x, dl[2], acc, total;
 };
-CeBwdSpace ce_bwd_space(int64_t t, int64_t k_in, int64_t v, bool want_grad_x) {
+CeBwdSpace ce_bwd_space(int64_t t, int64_t k_in, int64_t v, bool want_grad_x, bool want_grad_w) {
   CeBwdSpace s{};
   const int64_t piece = ce_piece(t, v);
   const size_t bytes = round256(static_cast<size_t>(t) * static_cast<size_t>(piece) * 2);
   s.grad_max = 0;
-  s.dl[0] = 256;
+  s.x = 256;
+  s.dl[0] = s.x + (want_grad_w ? round256(static_cast<size_t>(t) * static_cast<size_t>(k_in) * 2) : 0);
   s.dl[1] = s.dl[0] + (piece < v ? bytes : 0);   // the next piece's dl is written while this one's is read
   s.acc = s.dl[1] + bytes;
   s.total = s.acc + (want_grad_x && piece < v ? round256(static_cast<size_t>(t) * static_cast<size_t>(k_in) * 4) : 0);
@@ -604,9 +609,9 @@ bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const in
                      loss_out, lse_out);
 }
 
-size_t bitlinear_linear_ce_bwd_workspace_size(int64_t t, int64_t k_in, int64_t v, int want_grad_x) {
+size_t bitlinear_linear_ce_bwd_workspace_size(int64_t t, int64_t k_in, int64_t v, int want_grad_x, int want_grad_w) {
   if (t <= 0 || v <= 0 || k_in <= 0) return 0;
-  return ce_bwd_space(t, k_in, v, want_grad_x != 0).total;
+  return ce_bwd_space(t, k_in, v, want_grad_x != 0, want_grad_w != 0).total;
 }
 
 bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const int64_t* targets, const float* lse,
@@ -632,7 +637,7 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
     }
     return BL_OK;
   }
-  const CeBwdSpace sp = ce_bwd_space(t, k_in, v, grad_x != nullptr);
+  const CeBwdSpace sp = ce_bwd_space(t, k_in, v, grad_x != nullptr, grad_w != nullptr);
   if (!workspace || workspace_bytes < sp.total)
     return fail(BL_ERR_WORKSPACE, "workspace too small: %zu < %zu", workspace ? workspace_bytes : size_t(0), sp.total);
   uint8_t* space = static_cast<uint8_t*>(workspace);
@@ -644,6 +649,16 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
   if (bl_status s = launch_head("linear ce grad max launch", bl::ce_grad_max_kernel, 1, 1024, st, grad_loss, targets, t, v,
                                 grad_max))
     return s;
+  const uint4* xw = reinterpret_cast<const uint4*>(space + sp.x);   // grad_w's operand
+  if (grad_w) {
+    int64_t grid = (t * k_in / 8 + 255) / 256;
+    const int64_t cap = int64_t(device_sm_count()) * 16;
+    if (grid > cap) grid = cap;
+    if (bl_status s = launch_head("linear ce live rows launch", bl::ce_live_rows_kernel, grid, 256, st,
+                                  reinterpret_cast<const uint4*>(x), targets, t, v, static_cast<int>(k_in / 8),
+                                  reinterpret_cast<uint4*>(space + sp.x)))
+      return s;
+  }
   bl::CeGroup G{};
   G.v = v;
   G.targets = targets;
@@ -672,7 +687,7 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
       if (pw) {
         ce_shape(*pw, w32 ? bl::CE_F32 : bl::CE_BF16, n, k_in, t, true, true);
         if (bl_status s = ce_operand(&pw->tmA, dl, n, t, piece, true)) return s;
-        if (bl_status s = ce_operand(&pw->tmB, x, k_in, t, k_in, true)) return s;
+        if (bl_status s = ce_operand(&pw->tmB, xw, k_in, t, k_in, true)) return s;
         if (bl_status s = ce_output(&pw->tmOut, static_cast<uint8_t*>(grad_w) + v0 * k_in * (w32 ? 4 : 2), n, k_in, k_in, w32))
           return s;
       }

@@ -509,6 +509,19 @@ __global__ void __launch_bounds__(kCeJoinThreads) ce_join_kernel(const float2* s
   }
 }
 
+// X with the rows that have no loss cleared, the operand of grad_W: their dl is zero, but zero
+// times an infinity or NaN in a padded row would not be. 8 elements per thread and step.
+__global__ void __launch_bounds__(256) ce_live_rows_kernel(const uint4* x, const int64_t* targets, int64_t t, int64_t v, int row8,
+                                                           uint4* dst) {
+  follow_stream();
+  const int64_t n8 = t * row8;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t y = __ldg(targets + i / row8);
+    const uint4 r = __ldg(x + i);
+    dst[i] = y >= 0 && y < v ? r : make_uint4(0, 0, 0, 0);
+  }
+}
+
 // The summed parts of grad_X times the largest |g|, bf16: 8 elements per thread and step.
 __global__ void __launch_bounds__(256) ce_round_kernel(const float4* src, int64_t n8, const float* scale, uint4* dst) {
   follow_stream();

@@ -76,7 +76,7 @@ def _quant(fn, name: str, src, dtype, want_t: bool, fmt, out: dict | None, strea
         if key in o:
             _check(o[key], dt, shape, key, dev)
         else:
-            o[key] = torch.empty(shape, dtype=dt, device=dev)
+            o[key] = src.new_empty(shape, dtype=dt)
     st = _launch(getattr(lib(), fn), dev, stream, _ptr(src), rows, cols, code, _ptr(o["q"]), _ptr(o["scales"]),
                _ptr(o["qt"]) if want_t else None, _ptr(o["scales_t"]) if want_t else None)
     check(st, fn)
@@ -241,8 +241,9 @@ def bitlinear_linear_ce_fwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Ten
     return loss, lse
 
 
-def bitlinear_linear_ce_bwd_workspace_size(t: int, k_in: int, v: int, want_grad_x: bool = True) -> int:
-    return _size("bitlinear_linear_ce_bwd_workspace_size", t, k_in, v, int(want_grad_x))
+def bitlinear_linear_ce_bwd_workspace_size(t: int, k_in: int, v: int, want_grad_x: bool = True,
+                                           want_grad_w: bool = True) -> int:
+    return _size("bitlinear_linear_ce_bwd_workspace_size", t, k_in, v, int(want_grad_x), int(want_grad_w))
 
 
 def bitlinear_linear_ce_bwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
@@ -268,7 +269,7 @@ def bitlinear_linear_ce_bwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Ten
             raise TypeError(f"grad_w: expected bfloat16 or float32, got {grad_w.dtype}")
         _check(grad_w, grad_w.dtype, (v, k_in), "grad_w", dev)
     gwdt = BL_OUT_F32 if grad_w is not None and grad_w.dtype == torch.float32 else BL_OUT_BF16
-    need = bitlinear_linear_ce_bwd_workspace_size(t, k_in, v, grad_x is not None)
+    need = bitlinear_linear_ce_bwd_workspace_size(t, k_in, v, grad_x is not None, grad_w is not None)
     if need and workspace is None:
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     if workspace is not None:

@@ -312,6 +312,28 @@ def test_linear_ce_nothing_counts():
     assert not loss.any() and not gx.any() and not gw.any() and torch.isfinite(lse).all()
 
 
+@pytest.mark.parametrize("t", [20, 200])
+def test_linear_ce_padding_may_hold_anything(t):
+    # infinities and NaN in the rows, lse and grad_loss of tokens without a loss
+    k, v = 128, 700
+    x, w, y, g = ce_inputs(t, k, v, 8)
+    xd, wd, yd, gd = dev(x, torch.bfloat16), dev(w, torch.bfloat16), dev(y), dev(g)
+    dead = (yd < 0) | (yd >= v)
+    xd[dead] = float("nan")
+    xd[3 if y[3] < 0 else int(dead.nonzero()[0]), :5] = float("inf")
+    x0 = np.where((y < 0)[:, None] | (y >= v)[:, None], 0.0, x)
+    o = H.linear_ce(x0, w, y, g)
+    loss, lse = B.bitlinear_linear_ce_fwd(xd, wd, yd)
+    d = logit_errors(x0, w, k)
+    live = o["live"]
+    tol = d + 2.0 ** -20 + 4 * U * np.maximum(np.abs(o["lse"]), np.abs(o["logits"]).max(axis=1))
+    assert np.all(np.abs(f64(loss) - o["loss"])[live] <= 2 * tol[live]) and not loss[dead].any()
+    gd[dead] = float("nan")
+    gx, gw = B.bitlinear_linear_ce_bwd(xd, wd, yd, lse, gd)
+    check_ce_grads(gx, gw, x0, w, o, d, k, v, t)
+    assert not gx[dead].any()
+
+
 def test_linear_ce_empty_batch():
     w = torch.randn(50, 64, device="cuda").to(torch.bfloat16)
     x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
