@@ -681,6 +681,61 @@ def mma_peak(kind: str, iters: int = 4000, reps: int = 3) -> float:
     return best
 
 
+HEAD_CASES = ("fp8_quant", "fp8_quant_weight", "fp8_fwd", "fp8_bwd", "linear_ce_fwd", "linear_ce_bwd")
+
+
+def run_head_case(args) -> None:
+    """One of the head's operators alone on the --case-t/k/n shape: warm-up calls, then
+    ``--steps`` timed calls; prints one JSON line."""
+    import torch
+
+    import sparsity_step_b200 as B
+
+    dev = torch.device("cuda", 0)
+    t, k, n = args.case_t, args.case_k, args.case_n
+    gen = torch.Generator(device=dev).manual_seed(21)
+
+    def rand(*shape, std=1.0):
+        return torch.randn(*shape, generator=gen, device=dev) * std
+
+    x, w = rand(t, k).to(torch.bfloat16), rand(n, k, std=0.02)
+    flops, unit = 2.0 * t * k * n, "TFLOP/s"
+    if args.case.startswith("linear_ce"):
+        wb, y = w.to(torch.bfloat16), torch.randint(0, n, (t,), generator=gen, device=dev)
+        g = torch.full((t,), 1.0 / t, device=dev)
+        loss, lse = B.bitlinear_linear_ce_fwd(x, wb, y)
+        gx, gw = torch.empty_like(x), torch.empty_like(wb)
+        fn, work = ((lambda: B.bitlinear_linear_ce_fwd(x, wb, y, loss=loss, lse=lse), flops)
+                    if args.case == "linear_ce_fwd" else
+                    # three products: the logits again and both gradients
+                    (lambda: B.bitlinear_linear_ce_bwd(x, wb, y, lse, g, grad_x=gx, grad_w=gw), 3 * flops))
+    else:
+        xq, wq = B.bitlinear_fp8_quant(x, want_t=True), B.bitlinear_fp8_quant_weight(w, want_t=True)
+        if args.case == "fp8_quant":
+            fn, unit, work = (lambda: B.bitlinear_fp8_quant(x, want_t=True, out=xq)), "GB/s", 4.0 * t * k
+        elif args.case == "fp8_quant_weight":
+            fn, unit, work = (lambda: B.bitlinear_fp8_quant_weight(w, want_t=True, out=wq)), "GB/s", 6.0 * n * k
+        elif args.case == "fp8_fwd":
+            yo = torch.empty((t, n), dtype=torch.bfloat16, device=dev)
+            fn, work = (lambda: B.bitlinear_fp8_fwd(xq["q"], wq["q"], wq["scales"], x_scales=xq["scales"], y=yo)), flops
+        else:
+            dyq = B.bitlinear_fp8_quant(rand(t, n, std=1e-2).to(torch.bfloat16), want_t=True)
+            gx, gw = torch.empty_like(x), torch.empty((n, k), dtype=torch.bfloat16, device=dev)
+            fn, work = (lambda: B.bitlinear_fp8_bwd(dyq, xq, wq, grad_x=gx, grad_w=gw)), 2 * flops
+    for _ in range(args.warmup):
+        fn()
+    torch.cuda.synchronize()
+    s, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    s.record()
+    for _ in range(args.steps):
+        fn()
+    e.record()
+    torch.cuda.synchronize()
+    ms = s.elapsed_time(e) / args.steps
+    print(json.dumps({"case": args.case, "t": t, "k_in": k, "n_out": n, "ms_per_launch": round(ms, 5),
+                      "rate": round(work / (ms * 1e-3) / (1e9 if unit == "GB/s" else 1e12), 1), "unit": unit}), flush=True)
+
+
 def run_case(args) -> None:
     """One kernel class alone on a chosen shape (for ncu captures and tuning):
     warm-up launches, then ``--steps`` timed launches; prints one JSON line."""
@@ -690,6 +745,8 @@ def run_case(args) -> None:
     import sparsity_step_b200 as B
     from sparsity_step_b200 import synth
 
+    if args.case in HEAD_CASES:
+        return run_head_case(args)
     if args.case.startswith("mma_peak"):
         kind = args.case[len("mma_peak_"):]
         print(json.dumps({"case": args.case, "rate": round(mma_peak(kind), 1),
@@ -996,8 +1053,9 @@ def main(argv=None) -> None:
     ap.add_argument("--no-extra", action="store_true", help="skip the N:M sweep and decode sub-records")
     ap.add_argument("--case", choices=["quant_mask", "sgd_quant_mask", "act_quant", "fwd", "fwd_sp", "fwd_codes", "grad_x", "grad_w",
                                        "grad_w_grouped",
-                                       "grad_x_i8", "mask_hist", "mma_peak_i8", "mma_peak_bf16", "mma_peak_sp_i8"],
-                    help="time one kernel class alone on the --case-t/k/n shape")
+                                       "grad_x_i8", "mask_hist", "mma_peak_i8", "mma_peak_bf16", "mma_peak_sp_i8",
+                                       *HEAD_CASES],
+                    help="time one kernel class alone on the --case-t/k/n shape (linear_ce_*: n is the vocabulary)")
     ap.add_argument("--case-t", type=int, default=TOKENS)
     ap.add_argument("--case-k", type=int, default=2048)
     ap.add_argument("--case-n", type=int, default=11008)

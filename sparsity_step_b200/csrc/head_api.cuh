@@ -314,7 +314,7 @@ void ce_shares(bl::CeGroup& G, int pairs) {
   int64_t load[bl::kMaxCePairs] = {};
   for (int j = 0; j < G.count; ++j) {
     bl::CeShares& S = G.share[j];
-    const int64_t n = int64_t(G.p[j].num_m_blocks) * G.p[j].num_n_blocks, cost = G.p[j].num_k_blocks + kTileCost;
+    const int64_t n = int64_t(G.p[j].num_m_blocks) * G.p[j].num_n_blocks * G.p[j].splits, cost = G.p[j].split_blocks + kTileCost;
     int64_t top = 0;
     for (int i = 0; i < pairs; ++i) top = top > load[i] ? top : load[i];
     // no pair may be more than the table's rounds ahead of another
@@ -368,7 +368,7 @@ bl_status launch_ce(bl::CeGroup& G, cudaStream_t st) {
   int max_clusters = 0;
   if (bl_status s = pair_setup(setup, bl::ce_gemm_kernel, bl::kGemmThreads, smem, &max_clusters)) return s;
   int64_t tiles = 0;
-  for (int j = 0; j < G.count; ++j) tiles += int64_t(G.p[j].num_m_blocks) * G.p[j].num_n_blocks;
+  for (int j = 0; j < G.count; ++j) tiles += int64_t(G.p[j].num_m_blocks) * G.p[j].num_n_blocks * G.p[j].splits;
   if (tiles > INT32_MAX) return fail(BL_ERR_UNSUPPORTED_SHAPE, "too much work in one call");
   if (max_clusters > bl::kMaxCePairs) max_clusters = bl::kMaxCePairs;
   ce_shares(G, static_cast<int>(tiles < max_clusters ? tiles : max_clusters));
@@ -400,6 +400,8 @@ void ce_shape(bl::CeProblem& P, int mode, int64_t m, int64_t n, int64_t k, bool 
   P.part_blocks = mode == bl::CE_LSE ? bl::kCePartBlocks : P.num_k_blocks;
   P.num_m_blocks = static_cast<int>((m + 255) / 256);
   P.num_n_blocks = static_cast<int>((n + 255) / 256);
+  P.splits = 1;
+  P.split_blocks = P.num_k_blocks;
   P.m_fastest = m <= n ? 1 : 0;   // the smaller operand stays in L2 while the other streams by once
 }
 
@@ -417,6 +419,23 @@ CeFwdSpace ce_fwd_space(int64_t t, int64_t v) {
   s.total = s.target_logit + round256(static_cast<size_t>(t) * sizeof(float));
   return s;
 }
+// Runs of a piece of the vocabulary that grad_X's product is split into when it has fewer
+// tiles than there are CTA pairs (one token: 8 tiles of 2048 columns, each over the whole
+// vocabulary); at least 16 K blocks a run. A function of the sizes alone: the order of the
+// sums must not depend on the device.
+struct CeRuns {
+  int splits, blocks;   // runs of a whole piece, K blocks of a run
+};
+CeRuns ce_grad_x_runs(int64_t t, int64_t k_in, int64_t piece) {
+  constexpr int64_t kPairs = 74;
+  const int64_t tiles = ((t + 255) / 256) * ((k_in + 255) / 256), blocks = (piece + 63) / 64;
+  int64_t s = tiles < kPairs ? kPairs / tiles : 1;
+  if (s > blocks / 16) s = blocks / 16;
+  if (s < 1) s = 1;
+  const int64_t per = (blocks + s - 1) / s;
+  return {static_cast<int>((blocks + per - 1) / per), static_cast<int>(per)};
+}
+
 struct CeBwdSpace {
   size_t grad_max, x, dl[2], acc, total;
 };
@@ -429,7 +448,10 @@ CeBwdSpace ce_bwd_space(int64_t t, int64_t k_in, int64_t v, bool want_grad_x, bo
   s.dl[0] = s.x + (want_grad_w ? round256(static_cast<size_t>(t) * static_cast<size_t>(k_in) * 2) : 0);
   s.dl[1] = s.dl[0] + (piece < v ? bytes : 0);   // the next piece's dl is written while this one's is read
   s.acc = s.dl[1] + bytes;
-  s.total = s.acc + (want_grad_x && piece < v ? round256(static_cast<size_t>(t) * static_cast<size_t>(k_in) * 4) : 0);
+  const int splits = ce_grad_x_runs(t, k_in, piece < v ? piece : v).splits;
+  s.total = s.acc + (want_grad_x && (piece < v || splits > 1)
+                         ? static_cast<size_t>(splits) * static_cast<size_t>(round_up(t, 256)) * static_cast<size_t>(k_in) * 4
+                         : 0);
   return s;
 }
 
@@ -645,7 +667,8 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
   float* acc = reinterpret_cast<float*>(space + sp.acc);
   const int64_t piece = ce_piece(t, v);
   const int64_t pieces = (v + piece - 1) / piece;
-  const bool one = pieces == 1;   // a single piece: grad_X needs no fp32 sum in memory
+  const CeRuns runs = ce_grad_x_runs(t, k_in, piece < v ? piece : v);
+  const bool one = pieces == 1 && runs.splits == 1;   // grad_X needs no fp32 sums in memory
   if (bl_status s = launch_head("linear ce grad max launch", bl::ce_grad_max_kernel, 1, 1024, st, grad_loss, targets, t, v,
                                 grad_max))
     return s;
@@ -672,16 +695,18 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
       const int64_t v0 = (i - 1) * piece, n = v - v0 < piece ? v - v0 : piece;
       const uint8_t* dl = space + sp.dl[(i - 1) & 1];
       bl::CeProblem *px = nullptr, *pw = nullptr;
-      const bool w_first = t >= n;   // the deeper product's tiles go first
+      const bool w_first = t >= 64 * int64_t(runs.blocks);   // the deeper product's tiles go first
       if (grad_w && w_first) pw = &G.p[G.count++];
       if (grad_x) px = &G.p[G.count++];
       if (grad_w && !w_first) pw = &G.p[G.count++];
       if (px) {
         ce_shape(*px, one ? bl::CE_BF16 : i == 1 ? bl::CE_PART : bl::CE_ADD_PART, t, k_in, n, false, true);
+        px->split_blocks = runs.blocks;
+        px->splits = (px->num_k_blocks + runs.blocks - 1) / runs.blocks;   // the last piece may have fewer
         if (bl_status s = ce_operand(&px->tmA, dl, n, t, piece, false)) return s;
         if (bl_status s = ce_operand(&px->tmB, w + v0 * k_in, k_in, n, k_in, true)) return s;
         if (bl_status s = one ? ce_output(&px->tmOut, grad_x, t, k_in, k_in, false)
-                              : ce_output(&px->tmOut, acc, t, k_in, k_in, true))
+                              : ce_output(&px->tmOut, acc, runs.splits * round_up(t, 256), k_in, k_in, true))
           return s;
       }
       if (pw) {
@@ -709,7 +734,7 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
     const int64_t cap = int64_t(device_sm_count()) * 16;
     if (grid > cap) grid = cap;
     if (bl_status s = launch_head("linear ce round launch", bl::ce_round_kernel, grid, 256, st, reinterpret_cast<const float4*>(acc),
-                                  n8, static_cast<const float*>(grad_max), reinterpret_cast<uint4*>(grad_x)))
+                                  n8, runs.splits, round_up(t, 256) * k_in / 4, static_cast<const float*>(grad_max), reinterpret_cast<uint4*>(grad_x)))
       return s;
   }
   return BL_OK;

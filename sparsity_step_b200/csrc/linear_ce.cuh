@@ -52,6 +52,9 @@ struct CeProblem {
   int num_k_blocks;              // ceil(K / 64)
   int part_blocks;               // K blocks per accumulation in TMEM
   int num_m_blocks, num_n_blocks;   // 256 x 256 tiles
+  // CE_PART, CE_ADD_PART: K in `splits` runs of split_blocks, run i to output rows from
+  // i * 256 num_m_blocks on (1 run otherwise)
+  int splits, split_blocks;
   int m_fastest;
   int v0;                        // first vocabulary row of the piece (CE_DLOGITS)
 };
@@ -104,14 +107,25 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
 __device__ __forceinline__ int ce_round_tile(const CeShares& S, int pairs, int pos, int r) {
   return (r < S.common ? r * pairs : S.start[r - S.common]) + pos;
 }
-__device__ __forceinline__ void ce_tile(const CeProblem& P, int tile, int& mb, int& nb) {
+// Blocks of a tile and its run of K blocks [kb0, kb1).
+struct CeTile {
+  int mb, nb, split, kb0, kb1;
+};
+__device__ __forceinline__ CeTile ce_tile(const CeProblem& P, int tile) {
+  CeTile T;
+  const int per = P.num_m_blocks * P.num_n_blocks;
+  T.split = P.splits > 1 ? tile / per : 0;
+  tile -= T.split * per;
   if (P.m_fastest) {
-    mb = tile % P.num_m_blocks;
-    nb = tile / P.num_m_blocks;
+    T.mb = tile % P.num_m_blocks;
+    T.nb = tile / P.num_m_blocks;
   } else {
-    mb = tile / P.num_n_blocks;
-    nb = tile % P.num_n_blocks;
+    T.mb = tile / P.num_n_blocks;
+    T.nb = tile % P.num_n_blocks;
   }
+  T.kb0 = T.split * P.split_blocks;
+  T.kb1 = min(T.kb0 + P.split_blocks, P.num_k_blocks);
+  return T;
 }
 
 constexpr int kCePartBlocks = 8;   // 512 of K per accumulation of the logits
@@ -297,11 +311,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
       const CeProblem& P = G.p[j];
       const int rounds = G.share[j].count[cluster], pos = G.share[j].pos[cluster];
       for (int r = 0; r < rounds; ++r) {
-        int mb, nb;
-        ce_tile(P, ce_round_tile(G.share[j], nclusters, pos, r), mb, nb);
-        const int m0 = mb * 256 + 128 * static_cast<int>(rank);
-        const int n0 = nb * 256 + 128 * static_cast<int>(rank);
-        for (int kb = 0; kb < P.num_k_blocks; ++kb) {
+        const CeTile T = ce_tile(P, ce_round_tile(G.share[j], nclusters, pos, r));
+        const int m0 = T.mb * 256 + 128 * static_cast<int>(rank);
+        const int n0 = T.nb * 256 + 128 * static_cast<int>(rank);
+        for (int kb = T.kb0; kb < T.kb1; ++kb) {
           live = wait_live<false>(live, empty0 + 8u * s, ph ^ 1u, abort_flag, peer_abort);
           const uint32_t fb = full_leader0 + 8u * s;
           const int kc = kb * 64;
@@ -346,16 +359,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
       uint32_t unit = 0;   // accumulations so far: unit u is in buffer u & 1
       for (int j = 0; j < G.count; ++j) {
         const CeProblem& P = G.p[j];
-        const int rounds = G.share[j].count[cluster];
+        const int rounds = G.share[j].count[cluster], pos = G.share[j].pos[cluster];
         const uint32_t idesc = make_idesc(1u, 1u, 1u, P.a_mn, P.b_mn, 256, 256);
         // a K step of 16 in the address field (16-byte units): K-major 32 B inside the
         // swizzled row, MN-major 16 K rows = 2 KB
         const uint64_t a_step = P.a_mn ? 128u : 2u, b_step = P.b_mn ? 128u : 2u;
         const uint32_t a_lbo = P.a_mn ? 8192u : 16u, b_lbo = P.b_mn ? 8192u : 16u;
         for (int r = 0; r < rounds; ++r) {
-          for (int k0 = 0; k0 < P.num_k_blocks; k0 += P.part_blocks, ++unit) {
+          const CeTile T = ce_tile(P, ce_round_tile(G.share[j], nclusters, pos, r));
+          for (int k0 = T.kb0; k0 < T.kb1; k0 += P.part_blocks, ++unit) {
             const uint32_t buf = unit & 1u;
-            const int end = min(k0 + P.part_blocks, P.num_k_blocks);
+            const int end = min(k0 + P.part_blocks, T.kb1);
             live = wait_live<false>(live, tempty0 + 8u * buf, ((unit >> 1) & 1u) ^ 1u, abort_flag, peer_abort);
             tc_fence_after_sync();
             const uint32_t d_tmem = tmem_base + buf * kBN;
@@ -397,13 +411,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
       const CeProblem& P = G.p[j];
       const int rounds = G.share[j].count[cluster], pos = G.share[j].pos[cluster];
       for (int r = 0; r < rounds && ok; ++r) {
-        int mb, nb;
-        ce_tile(P, ce_round_tile(G.share[j], nclusters, pos, r), mb, nb);
-        const int row0 = mb * 256 + 128 * static_cast<int>(rank) + quad * 32;
-        const int n0 = nb * 256 + 128 * half;
+        const CeTile T = ce_tile(P, ce_round_tile(G.share[j], nclusters, pos, r));
+        const int row0 = T.mb * 256 + 128 * static_cast<int>(rank) + quad * 32;
+        const int n0 = T.nb * 256 + 128 * half;
         CeAcc acc;
 #pragma unroll 1
-        for (int k0 = 0; k0 < P.num_k_blocks; k0 += P.part_blocks, ++unit) {
+        for (int k0 = T.kb0; k0 < T.kb1; k0 += P.part_blocks, ++unit) {
           const uint32_t buf = unit & 1u;
           const bool got = mbar_wait(tfull0 + 8u * buf, (unit >> 1) & 1u, abort_flag);
           if (!__all_sync(0xffffffffu, got)) {
@@ -412,7 +425,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
           }
           tc_fence_after_sync();
           const uint32_t t_row = tmem_base + buf * kBN + static_cast<uint32_t>(128 * half) + (static_cast<uint32_t>(quad * 32) << 16);
-          if (k0 == 0) {
+          if (k0 == T.kb0) {
             uint32_t(&r)[4][32] = reinterpret_cast<uint32_t(&)[4][32]>(acc);
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(c * 32), r[c]);
@@ -432,8 +445,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
           if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8u * buf);   // the accumulator is free again
         }
         if (!ok) break;
-        if (P.mode == CE_LSE) ce_strip(G, P, acc, row0 + lane, n0, nb * 2 + half);
-        else ce_store(G, P, acc, stg, row0, n0, lane);
+        if (P.mode == CE_LSE) ce_strip(G, P, acc, row0 + lane, n0, T.nb * 2 + half);
+        else ce_store(G, P, acc, stg, row0 + T.split * P.num_m_blocks * 256, n0, lane);
       }
     }
     if (!ok && lane == 0) {
@@ -522,12 +535,19 @@ __global__ void __launch_bounds__(256) ce_live_rows_kernel(const uint4* x, const
   }
 }
 
-// The summed parts of grad_X times the largest |g|, bf16: 8 elements per thread and step.
-__global__ void __launch_bounds__(256) ce_round_kernel(const float4* src, int64_t n8, const float* scale, uint4* dst) {
+// grad_X: its `splits` partial sums (`stride` float4 apart), added in order, times the largest
+// |g|, in bf16. 8 elements per thread and step.
+__global__ void __launch_bounds__(256) ce_round_kernel(const float4* src, int64_t n8, int splits, int64_t stride,
+                                                       const float* scale, uint4* dst) {
   follow_stream();
   const float f = *scale;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += static_cast<int64_t>(gridDim.x) * 256) {
-    const float4 a = __ldg(src + 2 * i), b = __ldg(src + 2 * i + 1);
+    float4 a = __ldg(src + 2 * i), b = __ldg(src + 2 * i + 1);
+    for (int s = 1; s < splits; ++s) {
+      const float4 c = __ldg(src + s * stride + 2 * i), e = __ldg(src + s * stride + 2 * i + 1);
+      a = make_float4(a.x + c.x, a.y + c.y, a.z + c.z, a.w + c.w);
+      b = make_float4(b.x + e.x, b.y + e.y, b.z + e.z, b.w + e.w);
+    }
     dst[i] = make_uint4(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f), pack_bf16x2(b.x * f, b.y * f),
                         pack_bf16x2(b.z * f, b.w * f));
   }

@@ -277,6 +277,22 @@ def check_ce_grads(gx, gw, x, w, o, d, k, v, t):
         assert worst <= 1.0, f"worst error {worst:.3f} of its bound"
 
 
+@pytest.mark.parametrize("t,k,v", [(2, 64, 70001), (300, 64, 40000), (3000, 64, 30011)])
+def test_linear_ce_few_tiles(t, k, v):
+    # grad_x has so few tiles that its sum over the vocabulary is split, with and without
+    # several pieces, the last one short
+    x, w, y, g = ce_inputs(t, k, v, 6)
+    o = H.linear_ce(x, w, y, g)
+    xd, wd, yd, gd = dev(x, torch.bfloat16), dev(w, torch.bfloat16), dev(y), dev(g)
+    loss, lse = B.bitlinear_linear_ce_fwd(xd, wd, yd)
+    d = logit_errors(x, w, k)
+    check_loss(loss, lse, o, d)
+    gx, gw = B.bitlinear_linear_ce_bwd(xd, wd, yd, lse, gd)
+    check_ce_grads(gx, gw, x, w, o, d, k, v, t)
+    again = B.bitlinear_linear_ce_bwd(xd, wd, yd, lse, gd)
+    assert torch.equal(again[0], gx) and torch.equal(again[1], gw)
+
+
 def test_linear_ce_pieces():
     # more than one piece of the vocabulary, the last one ragged
     t, k, v = 4500, 64, 9001
