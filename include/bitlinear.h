@@ -426,12 +426,13 @@ bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const in
  *   dl[t, v] = (exp(l[t, v] - lse[t]) - [v == targets[t]]) * grad_loss[t]
  *   grad_x [t, k_in] bf16 = dl . w,   grad_w [v, k_in] (grad_w_dtype) = dl^T . x.
  * dl is rounded to bf16 for these products, relative to the largest |grad_loss|. A token
- * without a loss contributes nothing, whatever its x, lse and grad_loss hold.
+ * without a loss contributes nothing, whatever its x, lse and grad_loss hold, and costs
+ * nothing in the products.
  * The logits are computed again, one piece of the vocabulary after another; the workspace
  * holds two pieces of dl, an fp32 sum of grad_x and a copy of x, and all of dl [t, v] only
  * where that is below 64 MB. Sums are fp32 and in a fixed order.
  */
-size_t bitlinear_linear_ce_bwd_workspace_size(int64_t t, int64_t k_in, int64_t v, int want_grad_x, int want_grad_w);
+size_t bitlinear_linear_ce_bwd_workspace_size(int64_t t, int64_t k_in, int64_t v, int want_grad_x);
 bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const int64_t* targets, const float* lse,
                                   const float* grad_loss, int64_t t, int64_t k_in, int64_t v, uint16_t* grad_x,
                                   void* grad_w, int grad_w_dtype, void* workspace, size_t workspace_bytes, void* stream);

@@ -64,7 +64,7 @@ SIGNATURES = {
     "bitlinear_fp8_bwd": (_INT, [_P, _P, _P, _P, _INT, _P, _P, _INT, _P, _P, _INT, _I64, _I64, _I64, _P, _P, _INT, _P]),
     "bitlinear_linear_ce_fwd_workspace_size": (_SZ, [_I64, _I64]),
     "bitlinear_linear_ce_fwd": (_INT, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _SZ, _P]),
-    "bitlinear_linear_ce_bwd_workspace_size": (_SZ, [_I64, _I64, _I64, _INT, _INT]),
+    "bitlinear_linear_ce_bwd_workspace_size": (_SZ, [_I64, _I64, _I64, _INT]),
     "bitlinear_linear_ce_bwd": (_INT, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _INT, _P, _SZ, _P]),
     "bitlinear_device_status": (_INT, [_c.POINTER(_c.c_uint)]),
     "bitlinear_last_error": (_c.c_char_p, []),

@@ -128,7 +128,7 @@ __device__ __forceinline__ void few_fp8_operand(const FewArgs& a, uint32_t sB, u
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int tok = tok0 + 32 * c + (i & 31);
-      w[c] = !a.x_bf16 && tok < a.t ? __ldg(a.xs + static_cast<int64_t>(kb0 / 4 + (i >> 5)) * a.t + tok) : 0u;
+      w[c] = !a.x_bf16 && tok < a.t ? ld_plain(a.xs + static_cast<int64_t>(kb0 / 4 + (i >> 5)) * a.t + tok) : 0u;
     }
     st_shared_v4(sSfb + 16u * static_cast<uint32_t>(i), w[0], w[1], w[2], w[3]);
   }
@@ -150,8 +150,8 @@ __device__ __forceinline__ void few_fp8_operand(const FewArgs& a, uint32_t sB, u
       const int i = i0 + u * kFewThreads, j = i & 7, tok = (i >> 3) % a.t, kb = kb0 + (i >> 3) / a.t;
       const bool in = i < items && kb * 128 + j * 16 < a.k;
       const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(tok) * a.k + kb * 128 + j * 16);
-      lo[u] = in ? __ldg(p) : zero;
-      hi[u] = in ? __ldg(p + 1) : zero;
+      lo[u] = in ? ld_plain(p) : zero;
+      hi[u] = in ? ld_plain(p + 1) : zero;
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kFp8QuantThreads) fp8_quant_kernel(const Fp8Qu
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       v[i] = make_uint4(0, 0, 0, 0);
-      if (col_ok && i < rows_in) v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.src) + at0 + i * a.cols));
+      if (col_ok && i < rows_in) v[i] = ld_plain(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.src) + at0 + i * a.cols));
     }
     uint32_t rm[4] = {0, 0, 0, 0};   // maxima of row pairs (i, i + 4) as 16-bit |bf16| patterns
     uint32_t cm[4] = {0, 0, 0, 0};   // column pairs
@@ -207,8 +207,8 @@ __global__ void __launch_bounds__(kFp8QuantThreads) fp8_quant_kernel(const Fp8Qu
       v[i][0] = v[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (col_ok && i < rows_in) {
         const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.src) + at0 + i * a.cols);
-        v[i][0] = __ldg(p);
-        v[i][1] = __ldg(p + 1);
+        v[i][0] = ld_plain(p);
+        v[i][1] = ld_plain(p + 1);
       }
     }
 #pragma unroll

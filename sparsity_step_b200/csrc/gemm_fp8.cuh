@@ -355,11 +355,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       const uint32_t* pa = g.sa + static_cast<int64_t>(kg) * g.M;
       const uint32_t* pb = g.sb + static_cast<int64_t>(kg) * g.N;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) w[c] = m0 + 32 * c < g.M ? __ldg(pa + m0 + 32 * c) : 0u;
+      for (int c = 0; c < 4; ++c) w[c] = m0 + 32 * c < g.M ? ld_plain(pa + m0 + 32 * c) : 0u;
 #pragma unroll
       for (int c = 0; c < 8 * kHalves; ++c) {
         const int in_half = 32 * (c & 7), n = n0 + (c >> 3) * g.n_half + in_half;
-        w[4 + c] = in_half < g.n_half && n < g.N ? __ldg(pb + n) : 0u;
+        w[4 + c] = in_half < g.n_half && n < g.N ? ld_plain(pb + n) : 0u;
       }
     };
     if (cluster < num_tiles) load(cluster, 0);

@@ -402,6 +402,7 @@ void ce_shape(bl::CeProblem& P, int mode, int64_t m, int64_t n, int64_t k, bool 
   P.num_n_blocks = static_cast<int>((n + 255) / 256);
   P.splits = 1;
   P.split_blocks = P.num_k_blocks;
+  P.live_m = P.live_k = 0;
   P.m_fastest = m <= n ? 1 : 0;   // the smaller operand stays in L2 while the other streams by once
 }
 
@@ -437,21 +438,25 @@ CeRuns ce_grad_x_runs(int64_t t, int64_t k_in, int64_t piece) {
 }
 
 struct CeBwdSpace {
-  size_t grad_max, x, dl[2], acc, total;
+  size_t head, place, from, target, lse2, grad, x, dl[2], acc, total;
 };
-CeBwdSpace ce_bwd_space(int64_t t, int64_t k_in, int64_t v, bool want_grad_x, bool want_grad_w) {
+CeBwdSpace ce_bwd_space(int64_t t, int64_t k_in, int64_t v, bool want_grad_x) {
   CeBwdSpace s{};
   const int64_t piece = ce_piece(t, v);
   const size_t bytes = round256(static_cast<size_t>(t) * static_cast<size_t>(piece) * 2);
-  s.grad_max = 0;
-  s.x = 256;
-  s.dl[0] = s.x + (want_grad_w ? round256(static_cast<size_t>(t) * static_cast<size_t>(k_in) * 2) : 0);
+  const size_t rows = static_cast<size_t>(round_up(t, 256));
+  s.head = 0;   // the live tokens' number and the largest |grad_loss|
+  s.place = 256;
+  s.from = s.place + rows * 4;
+  s.target = s.from + rows * 4;
+  s.lse2 = s.target + rows * 4;
+  s.grad = s.lse2 + rows * 4;
+  s.x = s.grad + rows * 4;
+  s.dl[0] = s.x + round256(rows * static_cast<size_t>(k_in) * 2);
   s.dl[1] = s.dl[0] + (piece < v ? bytes : 0);   // the next piece's dl is written while this one's is read
   s.acc = s.dl[1] + bytes;
-  const int splits = ce_grad_x_runs(t, k_in, piece < v ? piece : v).splits;
-  s.total = s.acc + (want_grad_x && (piece < v || splits > 1)
-                         ? static_cast<size_t>(splits) * static_cast<size_t>(round_up(t, 256)) * static_cast<size_t>(k_in) * 4
-                         : 0);
+  const size_t splits = static_cast<size_t>(ce_grad_x_runs(t, k_in, piece < v ? piece : v).splits);
+  s.total = s.acc + (want_grad_x ? splits * rows * static_cast<size_t>(k_in) * 4 : 0);
   return s;
 }
 
@@ -631,9 +636,9 @@ bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const in
                      loss_out, lse_out);
 }
 
-size_t bitlinear_linear_ce_bwd_workspace_size(int64_t t, int64_t k_in, int64_t v, int want_grad_x, int want_grad_w) {
+size_t bitlinear_linear_ce_bwd_workspace_size(int64_t t, int64_t k_in, int64_t v, int want_grad_x) {
   if (t <= 0 || v <= 0 || k_in <= 0) return 0;
-  return ce_bwd_space(t, k_in, v, want_grad_x != 0, want_grad_w != 0).total;
+  return ce_bwd_space(t, k_in, v, want_grad_x != 0).total;
 }
 
 bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const int64_t* targets, const float* lse,
@@ -659,34 +664,37 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
     }
     return BL_OK;
   }
-  const CeBwdSpace sp = ce_bwd_space(t, k_in, v, grad_x != nullptr, grad_w != nullptr);
+  const CeBwdSpace sp = ce_bwd_space(t, k_in, v, grad_x != nullptr);
   if (!workspace || workspace_bytes < sp.total)
     return fail(BL_ERR_WORKSPACE, "workspace too small: %zu < %zu", workspace ? workspace_bytes : size_t(0), sp.total);
   uint8_t* space = static_cast<uint8_t*>(workspace);
-  float* grad_max = reinterpret_cast<float*>(space + sp.grad_max);
+  int* live = reinterpret_cast<int*>(space + sp.head);
+  float* grad_max = reinterpret_cast<float*>(space + sp.head) + 1;
+  int* place = reinterpret_cast<int*>(space + sp.place);
+  int* from = reinterpret_cast<int*>(space + sp.from);
+  int* row_target = reinterpret_cast<int*>(space + sp.target);
+  float* row_lse2 = reinterpret_cast<float*>(space + sp.lse2);
+  float* row_grad = reinterpret_cast<float*>(space + sp.grad);
+  uint8_t* x_live = space + sp.x;
   float* acc = reinterpret_cast<float*>(space + sp.acc);
-  const int64_t piece = ce_piece(t, v);
-  const int64_t pieces = (v + piece - 1) / piece;
+  const int64_t rows = round_up(t, 256), piece = ce_piece(t, v), pieces = (v + piece - 1) / piece;
   const CeRuns runs = ce_grad_x_runs(t, k_in, piece < v ? piece : v);
-  const bool one = pieces == 1 && runs.splits == 1;   // grad_X needs no fp32 sums in memory
-  if (bl_status s = launch_head("linear ce grad max launch", bl::ce_grad_max_kernel, 1, 1024, st, grad_loss, targets, t, v,
+  const int row8 = static_cast<int>(k_in / 8);
+  const int64_t cap = int64_t(device_sm_count()) * 16;   // blocks of the gather and scatter kernels
+  if (bl_status s = launch_head("linear ce live launch", bl::ce_live_kernel, 1, 1024, st, grad_loss, targets, t, v, place, from, live,
                                 grad_max))
     return s;
-  const uint4* xw = reinterpret_cast<const uint4*>(space + sp.x);   // grad_w's operand
-  if (grad_w) {
-    int64_t grid = (t * k_in / 8 + 255) / 256;
-    const int64_t cap = int64_t(device_sm_count()) * 16;
-    if (grid > cap) grid = cap;
-    if (bl_status s = launch_head("linear ce live rows launch", bl::ce_live_rows_kernel, grid, 256, st,
-                                  reinterpret_cast<const uint4*>(x), targets, t, v, static_cast<int>(k_in / 8),
-                                  reinterpret_cast<uint4*>(space + sp.x)))
-      return s;
-  }
+  if (bl_status s = launch_head("linear ce gather launch", bl::ce_gather_kernel, rows / 8 < cap ? rows / 8 : cap, 256, st,
+                                reinterpret_cast<const uint4*>(x), targets, lse, grad_loss, static_cast<const int*>(from),
+                                static_cast<const int*>(live), static_cast<const float*>(grad_max), row8,
+                                reinterpret_cast<uint4*>(x_live), row_target, row_lse2, row_grad))
+    return s;
   bl::CeGroup G{};
   G.v = v;
-  G.targets = targets;
-  G.lse = lse;
-  G.grad = grad_loss;
+  G.live = live;
+  G.row_target = row_target;
+  G.row_lse2 = row_lse2;
+  G.row_grad = row_grad;
   G.grad_max = grad_max;
   // launch i: the two products of piece i - 1 and dl of piece i
   for (int64_t i = 0; i <= pieces; ++i) {
@@ -700,19 +708,19 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
       if (grad_x) px = &G.p[G.count++];
       if (grad_w && !w_first) pw = &G.p[G.count++];
       if (px) {
-        ce_shape(*px, one ? bl::CE_BF16 : i == 1 ? bl::CE_PART : bl::CE_ADD_PART, t, k_in, n, false, true);
+        ce_shape(*px, i == 1 ? bl::CE_PART : bl::CE_ADD_PART, t, k_in, n, false, true);
+        px->live_m = 1;
         px->split_blocks = runs.blocks;
         px->splits = (px->num_k_blocks + runs.blocks - 1) / runs.blocks;   // the last piece may have fewer
         if (bl_status s = ce_operand(&px->tmA, dl, n, t, piece, false)) return s;
         if (bl_status s = ce_operand(&px->tmB, w + v0 * k_in, k_in, n, k_in, true)) return s;
-        if (bl_status s = one ? ce_output(&px->tmOut, grad_x, t, k_in, k_in, false)
-                              : ce_output(&px->tmOut, acc, runs.splits * round_up(t, 256), k_in, k_in, true))
-          return s;
+        if (bl_status s = ce_output(&px->tmOut, acc, runs.splits * rows, k_in, k_in, true)) return s;
       }
       if (pw) {
         ce_shape(*pw, w32 ? bl::CE_F32 : bl::CE_BF16, n, k_in, t, true, true);
+        pw->live_k = 1;
         if (bl_status s = ce_operand(&pw->tmA, dl, n, t, piece, true)) return s;
-        if (bl_status s = ce_operand(&pw->tmB, xw, k_in, t, k_in, true)) return s;
+        if (bl_status s = ce_operand(&pw->tmB, x_live, k_in, rows, k_in, true)) return s;
         if (bl_status s = ce_output(&pw->tmOut, static_cast<uint8_t*>(grad_w) + v0 * k_in * (w32 ? 4 : 2), n, k_in, k_in, w32))
           return s;
       }
@@ -722,19 +730,18 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
       bl::CeProblem& P = G.p[G.count++];
       ce_shape(P, bl::CE_DLOGITS, t, n, k_in, false, false);
       P.v0 = static_cast<int>(v0);
-      if (bl_status s = ce_operand(&P.tmA, x, k_in, t, k_in, false)) return s;
+      P.live_m = 1;
+      if (bl_status s = ce_operand(&P.tmA, x_live, k_in, rows, k_in, false)) return s;
       if (bl_status s = ce_operand(&P.tmB, w + v0 * k_in, k_in, n, k_in, false)) return s;
       if (bl_status s = ce_output(&P.tmOut, space + sp.dl[i & 1], t, n, piece, false)) return s;
     }
     if (bl_status s = launch_ce(G, st)) return s;
   }
-  if (grad_x && !one) {
-    const int64_t n8 = t * k_in / 8;
-    int64_t grid = (n8 + 255) / 256;
-    const int64_t cap = int64_t(device_sm_count()) * 16;
-    if (grid > cap) grid = cap;
-    if (bl_status s = launch_head("linear ce round launch", bl::ce_round_kernel, grid, 256, st, reinterpret_cast<const float4*>(acc),
-                                  n8, runs.splits, round_up(t, 256) * k_in / 4, static_cast<const float*>(grad_max), reinterpret_cast<uint4*>(grad_x)))
+  if (grad_x) {
+    const int64_t n8 = t * row8, blocks = (n8 + 255) / 256;
+    if (bl_status s = launch_head("linear ce scatter launch", bl::ce_scatter_kernel, blocks < cap ? blocks : cap, 256, st,
+                                  reinterpret_cast<const float4*>(acc), static_cast<const int*>(place), n8, row8, runs.splits,
+                                  rows * k_in / 4, static_cast<const float*>(grad_max), reinterpret_cast<uint4*>(grad_x)))
       return s;
   }
   return BL_OK;

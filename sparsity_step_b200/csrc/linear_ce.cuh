@@ -15,7 +15,9 @@
 // Backward, one piece of the vocabulary after another: the logits of the piece are computed
 // again, their epilogue writes dl of the piece in bf16 (the operand type of the tensor
 // cores: one rounding of at most half a step per factor), and two products consume it,
-// grad_W of the piece's rows and the piece's addend of grad_X, summed in fp32. Four
+// grad_W of the piece's rows and the piece's addend of grad_X, summed in fp32. Tokens without
+// a loss (padding, prompts) are left out first: the others' rows are gathered to the front,
+// the products stop after them, and grad_X is scattered back. Four
 // products of 2 T V K operations in all against three with all logits kept (T x V). g is
 // divided by its largest magnitude before that rounding and the gradients multiplied by it
 // after: with the usual constant g, dl of a target is then p - 1 itself, not a product whose
@@ -55,6 +57,7 @@ struct CeProblem {
   // CE_PART, CE_ADD_PART: K in `splits` runs of split_blocks, run i to output rows from
   // i * 256 num_m_blocks on (1 run otherwise)
   int splits, split_blocks;
+  int live_m, live_k;            // rows (A's rows) or K blocks end with the live tokens
   int m_fastest;
   int v0;                        // first vocabulary row of the piece (CE_DLOGITS)
 };
@@ -76,10 +79,13 @@ struct CeGroup {
   CeShares share[kMaxCeGroup];
   int count;
   int64_t v;                     // vocabulary size
-  const int64_t* targets;        // [T]
-  const float* lse;              // [T]  (CE_DLOGITS)
-  const float* grad;             // [T]  (CE_DLOGITS)
-  const float* grad_max;         // largest |grad| of the tokens with a loss
+  const int64_t* targets;        // [T]  (CE_LSE)
+  // backward: the tokens with a loss in order, then zeros (target -1) up to 256 rows
+  const int* live;               // their number, at least 1
+  const int* row_target;
+  const float* row_lse2;         // lse in units of log2
+  const float* row_grad;         // g over the largest |g|
+  const float* grad_max;         // the largest |g|
   float2* strips;                // [2 * n blocks, T] (max, sum)  (CE_LSE)
   float* target_logit;           // [T]  (CE_LSE)
 };
@@ -107,11 +113,11 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
 __device__ __forceinline__ int ce_round_tile(const CeShares& S, int pairs, int pos, int r) {
   return (r < S.common ? r * pairs : S.start[r - S.common]) + pos;
 }
-// Blocks of a tile and its run of K blocks [kb0, kb1).
+// Blocks of a tile and its run of K blocks [kb0, kb1), empty behind the live tokens.
 struct CeTile {
   int mb, nb, split, kb0, kb1;
 };
-__device__ __forceinline__ CeTile ce_tile(const CeProblem& P, int tile) {
+__device__ __forceinline__ CeTile ce_tile(const CeProblem& P, int tile, int live) {
   CeTile T;
   const int per = P.num_m_blocks * P.num_n_blocks;
   T.split = P.splits > 1 ? tile / per : 0;
@@ -124,7 +130,8 @@ __device__ __forceinline__ CeTile ce_tile(const CeProblem& P, int tile) {
     T.nb = tile % P.num_n_blocks;
   }
   T.kb0 = T.split * P.split_blocks;
-  T.kb1 = min(T.kb0 + P.split_blocks, P.num_k_blocks);
+  T.kb1 = min(T.kb0 + P.split_blocks, P.live_k ? min(P.num_k_blocks, (live + 63) >> 6) : P.num_k_blocks);
+  if (P.live_m && T.mb * 256 >= live) T.kb1 = T.kb0;
   return T;
 }
 
@@ -175,17 +182,9 @@ __device__ __forceinline__ void ce_strip(const CeGroup& G, const CeProblem& P, C
 __device__ __forceinline__ void ce_store(const CeGroup& G, const CeProblem& P, CeAcc& acc, uint32_t stg, int row0, int n0,
                                          int lane) {
   if (P.mode == CE_DLOGITS) {
-    float lse2 = 0.f, g = 0.f;
-    int64_t hit = -1;
-    if (row0 + lane < P.M) {
-      const int64_t y = G.targets[row0 + lane];
-      if (y >= 0 && y < G.v) {
-        g = G.grad[row0 + lane];
-        if (g != 0.f) g = __fdiv_rn(g, *G.grad_max);
-        lse2 = G.lse[row0 + lane] * kLog2e;
-        hit = y - P.v0 - n0;
-      }
-    }
+    const int row = row0 + lane;
+    const float lse2 = G.row_lse2[row], g = G.row_grad[row];
+    const int hit = G.row_target[row] - P.v0 - n0;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -195,9 +194,9 @@ __device__ __forceinline__ void ce_store(const CeGroup& G, const CeProblem& P, C
       for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          if (32 * c + j == static_cast<int>(hit)) acc[c][j] -= 1.f;
+          if (32 * c + j == hit) acc[c][j] -= 1.f;
     }
-    // a token without a loss has no gradient, whatever its logits are
+    // rows behind the last token: zeros
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -299,6 +298,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
   const uint32_t tmem_base = __reduce_or_sync(0xffffffffu, *tmem_slot);   // the same in every lane: a uniform register
   const uint32_t peer_abort = map_to_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
   const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  const int live_rows = G.live ? static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(ld_plain(G.live)))) : 0;
 
   if (warp == 0) {
     // ------------------------------------------------------------- TMA producer (both CTAs)
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
       const CeProblem& P = G.p[j];
       const int rounds = G.share[j].count[cluster], pos = G.share[j].pos[cluster];
       for (int r = 0; r < rounds; ++r) {
-        const CeTile T = ce_tile(P, ce_round_tile(G.share[j], nclusters, pos, r));
+        const CeTile T = ce_tile(P, ce_round_tile(G.share[j], nclusters, pos, r), live_rows);
         const int m0 = T.mb * 256 + 128 * static_cast<int>(rank);
         const int n0 = T.nb * 256 + 128 * static_cast<int>(rank);
         for (int kb = T.kb0; kb < T.kb1; ++kb) {
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
         const uint64_t a_step = P.a_mn ? 128u : 2u, b_step = P.b_mn ? 128u : 2u;
         const uint32_t a_lbo = P.a_mn ? 8192u : 16u, b_lbo = P.b_mn ? 8192u : 16u;
         for (int r = 0; r < rounds; ++r) {
-          const CeTile T = ce_tile(P, ce_round_tile(G.share[j], nclusters, pos, r));
+          const CeTile T = ce_tile(P, ce_round_tile(G.share[j], nclusters, pos, r), live_rows);
           for (int k0 = T.kb0; k0 < T.kb1; k0 += P.part_blocks, ++unit) {
             const uint32_t buf = unit & 1u;
             const int end = min(k0 + P.part_blocks, T.kb1);
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
       const CeProblem& P = G.p[j];
       const int rounds = G.share[j].count[cluster], pos = G.share[j].pos[cluster];
       for (int r = 0; r < rounds && ok; ++r) {
-        const CeTile T = ce_tile(P, ce_round_tile(G.share[j], nclusters, pos, r));
+        const CeTile T = ce_tile(P, ce_round_tile(G.share[j], nclusters, pos, r), live_rows);
         const int row0 = T.mb * 256 + 128 * static_cast<int>(rank) + quad * 32;
         const int n0 = T.nb * 256 + 128 * half;
         CeAcc acc;
@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
           if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8u * buf);   // the accumulator is free again
         }
         if (!ok) break;
+        if (T.kb0 >= T.kb1) continue;
         if (P.mode == CE_LSE) ce_strip(G, P, acc, row0 + lane, n0, T.nb * 2 + half);
         else ce_store(G, P, acc, stg, row0 + T.split * P.num_m_blocks * 256, n0, lane);
       }
@@ -465,22 +466,76 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
   }
 }
 
-// Largest |g| of the tokens that have a loss (0 if none): one block.
-__global__ void __launch_bounds__(1024) ce_grad_max_kernel(const float* grad, const int64_t* targets, int64_t t, int64_t v,
-                                                           float* out) {
+// The tokens with a loss, in order: place[t] among them (-1 for the others), from[i] the
+// i-th one, their number (1 if there is none: its row is zeros then) and the largest |g| of
+// them. One block: 1024 tokens a step.
+__global__ void __launch_bounds__(1024) ce_live_kernel(const float* grad, const int64_t* targets, int64_t t, int64_t v,
+                                                       int* place, int* from, int* live, float* grad_max) {
   __shared__ uint32_t s_max[32];
+  __shared__ int s_count[33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   follow_stream();
   uint32_t m = 0;   // |g| as its bit pattern: a NaN is larger than every number and stays one
-  for (int64_t i = threadIdx.x; i < t; i += 1024) {
-    const int64_t y = targets[i];
-    if (y >= 0 && y < v) m = max(m, __float_as_uint(grad[i]) & 0x7FFFFFFFu);
+  int before = 0;
+  for (int64_t t0 = 0; t0 < t; t0 += 1024) {
+    const int64_t i = t0 + threadIdx.x;
+    bool in = false;
+    if (i < t) {
+      const int64_t y = targets[i];
+      in = y >= 0 && y < v;
+    }
+    if (in) m = max(m, __float_as_uint(grad[i]) & 0x7FFFFFFFu);
+    const uint32_t votes = __ballot_sync(0xFFFFFFFFu, in);
+    if (lane == 0) s_count[warp] = __popc(votes);
+    __syncthreads();
+    if (warp == 0) {   // exclusive sums over the warps
+      int sum = s_count[lane];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, sum, off);
+        if (lane >= off) sum += o;
+      }
+      s_count[lane + 1] = sum;   // every lane has read its own count
+      if (lane == 0) s_count[0] = 0;
+    }
+    __syncthreads();
+    const int at = before + s_count[warp] + __popc(votes & ((1u << lane) - 1u));
+    if (i < t) place[i] = in ? at : -1;
+    if (in) from[at] = static_cast<int>(i);
+    before += s_count[32];
+    __syncthreads();
   }
   m = __reduce_max_sync(0xFFFFFFFFu, m);
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+  if (lane == 0) s_max[warp] = m;
   __syncthreads();
-  if (threadIdx.x < 32) {
-    m = __reduce_max_sync(0xFFFFFFFFu, s_max[threadIdx.x]);
-    if (threadIdx.x == 0) *out = __uint_as_float(m);
+  if (warp == 0) {
+    m = __reduce_max_sync(0xFFFFFFFFu, s_max[lane]);
+    if (lane == 0) {
+      *grad_max = __uint_as_float(m);
+      *live = before > 0 ? before : 1;
+      if (before == 0) from[0] = -1;
+    }
+  }
+}
+
+// Their rows of X and what dl needs of them, then zeros up to a multiple of 256 rows. A warp
+// per row.
+__global__ void __launch_bounds__(256) ce_gather_kernel(const uint4* x, const int64_t* targets, const float* lse, const float* grad,
+                                                        const int* from, const int* live, const float* grad_max, int row8,
+                                                        uint4* x_live, int* row_target, float* row_lse2, float* row_grad) {
+  follow_stream();
+  const int n = *live, end = (n + 255) / 256 * 256, lane = threadIdx.x & 31;
+  for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < end; r += gridDim.x * 8) {
+    const int t = r < n ? from[r] : -1;
+    uint4* dst = x_live + static_cast<int64_t>(r) * row8;
+    const uint4* src = x + static_cast<int64_t>(t < 0 ? 0 : t) * row8;
+    for (int i = lane; i < row8; i += 32) dst[i] = t < 0 ? make_uint4(0, 0, 0, 0) : ld_plain(src + i);
+    if (lane == 0) {
+      const float g = t < 0 ? 0.f : grad[t];
+      row_target[r] = t < 0 ? -1 : static_cast<int>(targets[t]);
+      row_lse2[r] = t < 0 ? 0.f : lse[t] * kLog2e;
+      row_grad[r] = g == 0.f ? 0.f : __fdiv_rn(g, *grad_max);
+    }
   }
 }
 
@@ -522,29 +577,24 @@ __global__ void __launch_bounds__(kCeJoinThreads) ce_join_kernel(const float2* s
   }
 }
 
-// X with the rows that have no loss cleared, the operand of grad_W: their dl is zero, but zero
-// times an infinity or NaN in a padded row would not be. 8 elements per thread and step.
-__global__ void __launch_bounds__(256) ce_live_rows_kernel(const uint4* x, const int64_t* targets, int64_t t, int64_t v, int row8,
-                                                           uint4* dst) {
-  follow_stream();
-  const int64_t n8 = t * row8;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t y = __ldg(targets + i / row8);
-    const uint4 r = __ldg(x + i);
-    dst[i] = y >= 0 && y < v ? r : make_uint4(0, 0, 0, 0);
-  }
-}
-
-// grad_X: its `splits` partial sums (`stride` float4 apart), added in order, times the largest
-// |g|, in bf16. 8 elements per thread and step.
-__global__ void __launch_bounds__(256) ce_round_kernel(const float4* src, int64_t n8, int splits, int64_t stride,
-                                                       const float* scale, uint4* dst) {
+// grad_X: the token's row of the `splits` partial sums (`stride` float4 apart), added in order,
+// times the largest |g|, in bf16; zeros for a token without a loss. 8 elements per thread and
+// step.
+__global__ void __launch_bounds__(256) ce_scatter_kernel(const float4* src, const int* place, int64_t n8, int row8, int splits,
+                                                         int64_t stride, const float* scale, uint4* dst) {
   follow_stream();
   const float f = *scale;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += static_cast<int64_t>(gridDim.x) * 256) {
-    float4 a = __ldg(src + 2 * i), b = __ldg(src + 2 * i + 1);
+    const int64_t t = i / row8;
+    const int p = ld_plain(place + t);
+    if (p < 0) {
+      dst[i] = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const float4* at = src + 2 * (static_cast<int64_t>(p) * row8 + (i - t * row8));
+    float4 a = ld_plain(at), b = ld_plain(at + 1);
     for (int s = 1; s < splits; ++s) {
-      const float4 c = __ldg(src + s * stride + 2 * i), e = __ldg(src + s * stride + 2 * i + 1);
+      const float4 c = ld_plain(at + s * stride), e = ld_plain(at + s * stride + 1);
       a = make_float4(a.x + c.x, a.y + c.y, a.z + c.z, a.w + c.w);
       b = make_float4(b.x + e.x, b.y + e.y, b.z + e.z, b.w + e.w);
     }

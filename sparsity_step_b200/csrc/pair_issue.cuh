@@ -15,6 +15,14 @@ __device__ __forceinline__ void follow_stream() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// A load of data that a kernel before this one may have written: an ordinary one, ordered by
+// follow_stream(), and not through the read-only path, whose data must not change while a
+// kernel is resident, waiting included.
+template <class T>
+__device__ __forceinline__ T ld_plain(const T* p) {
+  return *p;
+}
+
 // One lane of a converged warp, always the same one. The MMA and producer warps run their
 // loops with all 32 lanes and branch on this only around the instructions themselves: from
 // such a branch the compiler issues them with descriptors and addresses kept in uniform

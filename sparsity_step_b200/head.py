@@ -241,9 +241,8 @@ def bitlinear_linear_ce_fwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Ten
     return loss, lse
 
 
-def bitlinear_linear_ce_bwd_workspace_size(t: int, k_in: int, v: int, want_grad_x: bool = True,
-                                           want_grad_w: bool = True) -> int:
-    return _size("bitlinear_linear_ce_bwd_workspace_size", t, k_in, v, int(want_grad_x), int(want_grad_w))
+def bitlinear_linear_ce_bwd_workspace_size(t: int, k_in: int, v: int, want_grad_x: bool = True) -> int:
+    return _size("bitlinear_linear_ce_bwd_workspace_size", t, k_in, v, int(want_grad_x))
 
 
 def bitlinear_linear_ce_bwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
@@ -269,7 +268,7 @@ def bitlinear_linear_ce_bwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Ten
             raise TypeError(f"grad_w: expected bfloat16 or float32, got {grad_w.dtype}")
         _check(grad_w, grad_w.dtype, (v, k_in), "grad_w", dev)
     gwdt = BL_OUT_F32 if grad_w is not None and grad_w.dtype == torch.float32 else BL_OUT_BF16
-    need = bitlinear_linear_ce_bwd_workspace_size(t, k_in, v, grad_x is not None, grad_w is not None)
+    need = bitlinear_linear_ce_bwd_workspace_size(t, k_in, v, grad_x is not None)
     if workspace is not None:
         _need_bytes(workspace, need, "workspace", dev)
     elif need:

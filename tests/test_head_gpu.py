@@ -403,3 +403,71 @@ def test_head_training_step_runs_together():
     for a, b, c in zip(first, again, captured):
         assert torch.equal(a, b) and torch.equal(a, c) and torch.isfinite(a.float()).all()
     assert float(first[0].mean()) > 1.0
+
+
+def test_two_streams_at_once():
+    """The same calls on two streams side by side, each with its own data, many times over:
+    every result is what the call alone gives."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    sets = []
+    for t, k, n, v in ((16, 1024, 2048, 3001), (300, 512, 1040, 2500)):
+        x = torch.randn(t, k, generator=gen, device="cuda").to(torch.bfloat16)
+        w = B.bitlinear_fp8_quant_weight(torch.randn(n, k, generator=gen, device="cuda"))
+        head = torch.randn(v, k, generator=gen, device="cuda").to(torch.bfloat16) * 0.1
+        y = torch.randint(-1, v, (t,), generator=gen, device="cuda")
+        sets.append((x, w, head, y, torch.randn(t, generator=gen, device="cuda")))
+
+    def run(x, w, head, y, g):
+        a = B.bitlinear_fp8_fwd(x, w["q"], w["scales"])
+        q = B.bitlinear_fp8_quant(x, want_t=True)
+        loss, lse = B.bitlinear_linear_ce_fwd(x, head, y)
+        return [a, q["qt"].view(torch.uint8), loss, *B.bitlinear_linear_ce_bwd(x, head, y, lse, g)]
+
+    alone = [run(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(run(*sets[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(r, alone[i]))
+    assert B.bitlinear_device_status()[0] == 0
+
+
+def test_chain_reads_what_the_call_before_wrote():
+    """Each call's input is the previous call's output in the same buffers, for many steps:
+    a kernel set up behind its predecessor must not read an earlier step's values."""
+    t, k = 64, 1024
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    w = B.bitlinear_fp8_quant_weight(torch.randn(k, k, generator=gen, device="cuda") / k ** 0.5)
+    x0 = torch.randn(t, k, generator=gen, device="cuda").to(torch.bfloat16)
+
+    def chain(sync):
+        a, b = x0.clone(), torch.empty_like(x0)
+        q = B.bitlinear_fp8_quant(a)
+        out = []
+        for _ in range(30):
+            B.bitlinear_fp8_quant(a, out=q)
+            B.bitlinear_fp8_fwd(q["q"], w["q"], w["scales"], x_scales=q["scales"], y=b)
+            if sync:
+                torch.cuda.synchronize()
+            a, b = b, a
+            out.append(a.clone())
+        return torch.stack(out)
+
+    assert torch.equal(chain(True), chain(False))
+
+
+def test_streams_other_than_the_current_one():
+    s = torch.cuda.Stream()
+    x = torch.randn(5, 256, device="cuda").to(torch.bfloat16)
+    w = B.bitlinear_fp8_quant_weight(torch.randn(64, 256, device="cuda"))
+    want = B.bitlinear_fp8_fwd(x, w["q"], w["scales"])
+    s.wait_stream(torch.cuda.current_stream())
+    got = B.bitlinear_fp8_fwd(x, w["q"], w["scales"], stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)

@@ -119,8 +119,8 @@ def test_linear_ce_refusals(L):
 def test_linear_ce_workspace_is_far_from_the_logits(L):
     t, k, v = 8192, 2048, 65536
     assert L.bitlinear_linear_ce_fwd_workspace_size(t, v) < 2 * t * v // 16
-    assert L.bitlinear_linear_ce_bwd_workspace_size(t, k, v, 1, 1) < 2 * t * v // 3
-    assert L.bitlinear_linear_ce_fwd_workspace_size(0, v) == 0 and L.bitlinear_linear_ce_bwd_workspace_size(0, k, v, 1, 1) == 0
+    assert L.bitlinear_linear_ce_bwd_workspace_size(t, k, v, 1) < 2 * t * v // 3
+    assert L.bitlinear_linear_ce_fwd_workspace_size(0, v) == 0 and L.bitlinear_linear_ce_bwd_workspace_size(0, k, v, 1) == 0
 
 
 # ------------------------------------------------------------------ the binding
