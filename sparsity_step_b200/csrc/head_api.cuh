@@ -307,71 +307,21 @@ bl_status check_ce(int64_t t, int64_t k_in, int64_t v) {
   return BL_OK;
 }
 
-// Shares of the products (deepest first) among `pairs` CTA pairs: every product raises the
-// pairs' loads, in K blocks, to a common level, its last tiles going to the least loaded.
-void ce_shares(bl::CeGroup& G, int pairs) {
-  constexpr int64_t kTileCost = 4;   // a tile's start and epilogue, in K blocks
-  int64_t load[bl::kMaxCePairs] = {};
-  for (int j = 0; j < G.count; ++j) {
-    bl::CeShares& S = G.share[j];
-    const int64_t n = int64_t(G.p[j].num_m_blocks) * G.p[j].num_n_blocks * G.p[j].splits, cost = G.p[j].split_blocks + kTileCost;
-    int64_t top = 0;
-    for (int i = 0; i < pairs; ++i) top = top > load[i] ? top : load[i];
-    // no pair may be more than the table's rounds ahead of another
-    for (int i = 0; i < pairs; ++i)
-      if (load[i] < top - (bl::kMaxCeExtra - 2) * cost) load[i] = top - (bl::kMaxCeExtra - 2) * cost;
-    auto taken = [&](int64_t level) {   // tiles that fit below a level
-      int64_t sum = 0;
-      for (int i = 0; i < pairs; ++i) sum += level > load[i] ? (level - load[i]) / cost : 0;
-      return sum;
-    };
-    int64_t lo = 0, hi = top + (n + 1) * cost;   // the highest level that takes at most n tiles
-    while (hi - lo > 1) {
-      const int64_t mid = lo + (hi - lo) / 2;
-      if (taken(mid) <= n) lo = mid;
-      else hi = mid;
-    }
-    int64_t left = n;
-    for (int i = 0; i < pairs; ++i) {
-      S.count[i] = lo > load[i] ? static_cast<int>((lo - load[i]) / cost) : 0;
-      load[i] += S.count[i] * cost;
-      left -= S.count[i];
-    }
-    for (; left > 0; --left) {   // fewer than there are pairs
-      int least = 0;
-      for (int i = 1; i < pairs; ++i)
-        if (load[i] < load[least]) least = i;
-      ++S.count[least];
-      load[least] += cost;
-    }
-    int common = S.count[0], most = S.count[0];
-    for (int i = 1; i < pairs; ++i) {
-      common = common < S.count[i] ? common : S.count[i];
-      most = most > S.count[i] ? most : S.count[i];
-    }
-    int at = 0;   // positions by falling count
-    for (int c = most; c >= common; --c)
-      for (int i = 0; i < pairs; ++i)
-        if (S.count[i] == c) S.pos[i] = static_cast<int16_t>(at++);
-    S.common = common;
-    int start = common * pairs;
-    for (int r = common; r < most; ++r) {
-      S.start[r - common] = start;
-      for (int i = 0; i < pairs; ++i) start += S.count[i] > r ? 1 : 0;
-    }
-  }
-}
-
 bl_status launch_ce(bl::CeGroup& G, cudaStream_t st) {
   constexpr size_t smem = bl::gemm2_smem_bytes();
   static PerDeviceSetup setup;
   int max_clusters = 0;
   if (bl_status s = pair_setup(setup, bl::ce_gemm_kernel, bl::kGemmThreads, smem, &max_clusters)) return s;
-  int64_t tiles = 0;
-  for (int j = 0; j < G.count; ++j) tiles += int64_t(G.p[j].num_m_blocks) * G.p[j].num_n_blocks * G.p[j].splits;
+  constexpr int64_t kTileCost = 4;   // a tile's start and epilogue, in K blocks
+  int64_t n[bl::kMaxCeGroup], cost[bl::kMaxCeGroup], tiles = 0;
+  for (int j = 0; j < G.count; ++j) {
+    n[j] = int64_t(G.p[j].num_m_blocks) * G.p[j].num_n_blocks * G.p[j].splits;
+    cost[j] = G.p[j].split_blocks + kTileCost;
+    tiles += n[j];
+  }
   if (tiles > INT32_MAX) return fail(BL_ERR_UNSUPPORTED_SHAPE, "too much work in one call");
   if (max_clusters > bl::kMaxCePairs) max_clusters = bl::kMaxCePairs;
-  ce_shares(G, static_cast<int>(tiles < max_clusters ? tiles : max_clusters));
+  bl::ce_shares(G.share, n, cost, G.count, static_cast<int>(tiles < max_clusters ? tiles : max_clusters));
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   head_config(cfg, attr, 2 * (tiles < max_clusters ? tiles : max_clusters), bl::kGemmThreads, smem, 2, st);

@@ -26,12 +26,11 @@
 //
 // The kernel takes up to three products with their own operand orders, depths and
 // epilogues in one launch, so that the two products of one piece and the logits of the next
-// fill the SMs together; each pair gets as many tiles of each as make its K blocks add up to
-// its share (tiles of different depth dealt out in turn left some pairs with twice the work
-// at 2047 x 1536 x 32003: 0.53 -> 0.42 ms).
+// fill the SMs together (ce_shares.cuh).
 // Stages, synchronisation and TMEM use as in gemm_tc2.cuh.
 #pragma once
 
+#include "ce_shares.cuh"
 #include "gemm_sp2.cuh"
 #include "pair_issue.cuh"
 
@@ -62,18 +61,6 @@ struct CeProblem {
   int v0;                        // first vocabulary row of the piece (CE_DLOGITS)
 };
 constexpr int kMaxCeGroup = 3;
-constexpr int kMaxCePairs = 80;
-constexpr int kMaxCeExtra = 48;
-// Which tiles of a product a CTA pair computes: `count` of them, one a round; the pairs stand
-// in the order of their counts (`pos`), so that a round's tiles are consecutive and its pairs
-// the first ones. Every pair takes part in the first `common` rounds; round common + i
-// begins at tile start[i].
-struct CeShares {
-  int16_t pos[kMaxCePairs];
-  int count[kMaxCePairs];
-  int common;
-  int start[kMaxCeExtra];
-};
 struct CeGroup {
   CeProblem p[kMaxCeGroup];
   CeShares share[kMaxCeGroup];
@@ -109,10 +96,6 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// Tile of round r for the pair at position pos.
-__device__ __forceinline__ int ce_round_tile(const CeShares& S, int pairs, int pos, int r) {
-  return (r < S.common ? r * pairs : S.start[r - S.common]) + pos;
-}
 // Blocks of a tile and its run of K blocks [kb0, kb1), empty behind the live tokens.
 struct CeTile {
   int mb, nb, split, kb0, kb1;
