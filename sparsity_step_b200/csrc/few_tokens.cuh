@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
   const uint32_t sSfb = sB + static_cast<uint32_t>((kept ? max_blocks : a.stages) * kTok * 128);
   const uint32_t bar0 = sSfb + (kFp8 ? static_cast<uint32_t>((max_blocks / 4 + 2) * kFewSfBytes) : 0u);
   const uint32_t full0 = bar0, empty0 = bar0 + 8u * kFewMaxStages, tfull0 = empty0 + 8u * kFewMaxStages, tempty0 = tfull0 + 16u;
-  const uint32_t slot = tempty0 + 16u;
+  const uint32_t done_bar = tempty0 + 16u, slot = done_bar + 8u;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem_raw + (slot - raw));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + (slot - raw) + 4);
 
@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
       mbar_init(tfull0 + 8u * b, 1);
       mbar_init(tempty0 + 8u * b, 4);   // epilogue warps
     }
+    mbar_init(done_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
     if (!kept) tma_prefetch_desc(&M.x);
@@ -307,7 +308,11 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
         }
       }
     }
-    if (!live && elect_one()) atomicOr(&g_device_status, DEV_ST_TIMEOUT_MMA);
+    if (elect_one()) {
+      if (!live) atomicOr(&g_device_status, DEV_ST_TIMEOUT_MMA);
+      tc_commit(done_bar);   // every MMA issued above has retired once this arrives
+      if (!mbar_wait_plain(done_bar, 0)) atomicOr(&g_device_status, DEV_ST_TIMEOUT_DRAIN);
+    }
   } else {
     // ------------------------------------------------------------- epilogue (4 warps)
     const int quad = warp & 3;

@@ -185,6 +185,23 @@ def test_fwd_row_scales_and_not_finite_rows(t):
     assert torch.equal(y[keep], clean[keep])
 
 
+@pytest.mark.parametrize("t", [3, 40, 300])
+def test_fwd_extreme_scales(t):
+    # scales near both ends that cancel in the product, blocks and rows of zeros
+    k, n = 640, 272
+    rng = np.random.default_rng(t)
+    x = bf16(rng, t, k, outliers=False) * 2.0 ** 90
+    w = (rng.normal(size=(n, k)) * 2.0 ** -95).astype(np.float32)
+    x[0], x[:, 256:384], w[128:256, 384:512] = 0.0, 0.0, 0.0
+    x[1] *= np.float32(2.0 ** -150)   # zeros too: half of the least fp32 number rounds to even
+    x[2] *= np.float32(2.0 ** -100)
+    xd, wq = dev(x, torch.bfloat16), B.bitlinear_fp8_quant_weight(dev(w))
+    x = f64(xd)
+    y = B.bitlinear_fp8_fwd(xd, wq["q"], wq["scales"], y_dtype=torch.float32)
+    product_close(y, H.fp8_quant(x, "e4m3")[2], H.fp8_quant(w, "e4m3", 128)[2], k)
+    assert not y[:2].any() and y[2].any()
+
+
 @pytest.mark.parametrize("t,k,n,df", [(1, 64, 16, "e4m3"), (5, 128, 48, "e5m2"), (16, 576, 224, "e4m3"), (37, 192, 1040, "e5m2"),
                                       (130, 1088, 256, "e4m3"), (600, 704, 272, "e5m2"), (1025, 320, 528, "e4m3")])
 def test_bwd(t, k, n, df):
