@@ -413,7 +413,8 @@ bl_status bitlinear_fp8_bwd(const uint8_t* dy_q, const uint8_t* dy_scales, const
  *
  *   x [t, k_in] bf16, w [v, k_in] bf16, any v >= 1; targets [t] int64.
  *   loss_out, lse_out [t] fp32 (lse_out also for tokens without a loss).
- * Logits are accumulated in fp32 and never rounded.
+ * Logits are accumulated in fp32 and never rounded; those of -infinity count nothing, and
+ * +infinity or NaN in a token's logits reaches that token's lse alone.
  */
 size_t bitlinear_linear_ce_fwd_workspace_size(int64_t t, int64_t v);
 bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const int64_t* targets, int64_t t, int64_t k_in,

@@ -371,6 +371,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
               float m = l2;
 #pragma unroll
               for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+              m = strip_max(m);
               float e = row < a.n ? ex2(fmaf(v[i], kLog2e, -m)) : 0.f;
 #pragma unroll
               for (int off = 16; off > 0; off >>= 1) e += __shfl_xor_sync(0xffffffffu, e, off);
@@ -430,6 +431,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        m = strip_max(m);
         float e = 0.f;
 #pragma unroll
         for (int h = 0; h < 2; ++h)

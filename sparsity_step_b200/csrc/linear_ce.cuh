@@ -17,11 +17,11 @@
 // cores: one rounding of at most half a step per factor), and two products consume it,
 // grad_W of the piece's rows and the piece's addend of grad_X, summed in fp32. Tokens without
 // a loss (padding, prompts) are left out first: the others' rows are gathered to the front,
-// the products stop after them, and grad_X is scattered back. Four
-// products of 2 T V K operations in all against three with all logits kept (T x V). g is
-// divided by its largest magnitude before that rounding and the gradients multiplied by it
-// after: with the usual constant g, dl of a target is then p - 1 itself, not a product whose
-// rounding error every token would share.
+// the products stop after them, and grad_X is scattered back. Four products of 2 T V K
+// operations in all against three with all logits kept (T x V). g is divided by its largest
+// magnitude before that rounding and the gradients multiplied by it after: with the usual
+// constant g, dl of a target is then p - 1 itself, not a product whose rounding error every
+// token would share.
 // Bound by the bf16 tensor pipe (and the power it draws).
 //
 // The kernel takes up to three products with their own operand orders, depths and
@@ -29,6 +29,8 @@
 // fill the SMs together (ce_shares.cuh).
 // Stages, synchronisation and TMEM use as in gemm_tc2.cuh.
 #pragma once
+
+#include <cfloat>
 
 #include "ce_shares.cuh"
 #include "gemm_sp2.cuh"
@@ -84,6 +86,9 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Maximum of a strip's logits in units of log2, kept finite: with logits of -infinity alone
+// its exponentials then add up to 0, with one of +infinity to infinity, never to inf - inf.
+__device__ __forceinline__ float strip_max(float m2) { return fminf(fmaxf(m2, -FLT_MAX), FLT_MAX); }
 // fp32 tile added to global memory by the TMA engine (one add per element and launch, so
 // the order of additions is the order of launches).
 __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {
@@ -151,7 +156,7 @@ __device__ __forceinline__ void ce_strip(const CeGroup& G, const CeProblem& P, C
 #pragma unroll
     for (int j = 1; j < 32; ++j) m[c] = fmaxf(m[c], acc[c][j]);
   }
-  const float m2 = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * kLog2e;   // in units of log2
+  const float m2 = strip_max(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * kLog2e);
   if (left > 0) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
@@ -537,7 +542,7 @@ __global__ void __launch_bounds__(kCeJoinThreads) ce_join_kernel(const float2* s
 #pragma unroll 4
     for (int i = slice; i < num_strips; i += 32) {
       const float2 p = strips[static_cast<int64_t>(i) * t + row];
-      const bool some = p.y != 0.f;   // else a strip past the vocabulary's end
+      const bool some = p.y != 0.f;   // else a strip past the vocabulary's end or of -infinity alone
       const float m2 = some ? fmaxf(m, p.x) : m;
       s = some ? s * ex2(m - m2) + p.y * ex2(p.x - m2) : s;
       m = m2;

@@ -367,6 +367,25 @@ def test_linear_ce_padding_may_hold_anything(t):
     assert not gx[dead].any()
 
 
+@pytest.mark.parametrize("t,v", [(1, 40), (3, 700), (20, 20001), (200, 700)])
+def test_linear_ce_infinite_logits(t, v):
+    # a vocabulary closed by weights of -infinity behind its first rows (and a token that
+    # turns them into +infinity): the others' loss is that of the first rows alone
+    k, first = 128, 24
+    x, w, y, _ = ce_inputs(t, k, v, 11)
+    x[:, 0], y[:] = 1.0, np.arange(t) % first
+    if t > 1:
+        x[1, 0] = -1.0
+    xd, wd, yd = dev(x, torch.bfloat16), dev(w, torch.bfloat16), dev(y)
+    wd[first:], wd[first:, 0] = 0.0, float("-inf")
+    loss, lse = B.bitlinear_linear_ce_fwd(xd, wd, yd)
+    o = H.linear_ce(x, w[:first], y)
+    d = logit_errors(x, w[:first], k)
+    keep = np.arange(t) != 1
+    check_loss(loss[dev(keep)], lse[dev(keep)], {n: a[keep] for n, a in o.items()}, d[keep])
+    assert t == 1 or (loss[1] == float("inf") and lse[1] == float("inf"))
+
+
 def test_linear_ce_empty_batch():
     w = torch.randn(50, 64, device="cuda").to(torch.bfloat16)
     x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
