@@ -74,7 +74,7 @@ struct CeGroup {
   const int* row_target;
   const float* row_lse2;         // lse in units of log2
   const float* row_grad;         // g over the largest |g|
-  const float* grad_max;         // the largest |g|
+  const float* grad_max;         // the largest finite |g|, or 1
   float2* strips;                // [2 * n blocks, T] (max, sum)  (CE_LSE)
   float* target_logit;           // [T]  (CE_LSE)
 };
@@ -455,15 +455,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
 }
 
 // The tokens with a loss, in order: place[t] among them (-1 for the others), from[i] the
-// i-th one, their number (1 if there is none: its row is zeros then) and the largest |g| of
-// them. One block: 1024 tokens a step.
+// i-th one, their number (1 if there is none: its row is zeros then) and the largest finite
+// |g| of them (1 if there is none above 0): an infinity or a NaN stays with its own token
+// and does not divide the others. One block: 1024 tokens a step.
 __global__ void __launch_bounds__(1024) ce_live_kernel(const float* grad, const int64_t* targets, int64_t t, int64_t v,
                                                        int* place, int* from, int* live, float* grad_max) {
   __shared__ uint32_t s_max[32];
   __shared__ int s_count[33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   follow_stream();
-  uint32_t m = 0;   // |g| as its bit pattern: a NaN is larger than every number and stays one
+  uint32_t m = 0;   // |g| as its bit pattern
   int before = 0;
   for (int64_t t0 = 0; t0 < t; t0 += 1024) {
     const int64_t i = t0 + threadIdx.x;
@@ -472,7 +473,10 @@ __global__ void __launch_bounds__(1024) ce_live_kernel(const float* grad, const 
       const int64_t y = targets[i];
       in = y >= 0 && y < v;
     }
-    if (in) m = max(m, __float_as_uint(grad[i]) & 0x7FFFFFFFu);
+    if (in) {
+      const uint32_t g = __float_as_uint(grad[i]) & 0x7FFFFFFFu;
+      if (g < 0x7F800000u) m = max(m, g);
+    }
     const uint32_t votes = __ballot_sync(0xFFFFFFFFu, in);
     if (lane == 0) s_count[warp] = __popc(votes);
     __syncthreads();
@@ -499,7 +503,7 @@ __global__ void __launch_bounds__(1024) ce_live_kernel(const float* grad, const 
   if (warp == 0) {
     m = __reduce_max_sync(0xFFFFFFFFu, s_max[lane]);
     if (lane == 0) {
-      *grad_max = __uint_as_float(m);
+      *grad_max = m ? __uint_as_float(m) : 1.f;
       *live = before > 0 ? before : 1;
       if (before == 0) from[0] = -1;
     }

@@ -386,6 +386,24 @@ def test_linear_ce_infinite_logits(t, v):
     assert t == 1 or (loss[1] == float("inf") and lse[1] == float("inf"))
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("t", [1, 20, 300])
+def test_linear_ce_not_finite_grad_loss(t, bad):
+    # it stays with its token: the other rows of grad_x are what they are with 0 in its place
+    k, v = 128, 700
+    x, w, y, g = ce_inputs(t, k, v, 12)
+    y[t // 2] = 5
+    g[t // 2] = 0.0
+    xd, wd, yd, gd = dev(x, torch.bfloat16), dev(w, torch.bfloat16), dev(y), dev(g)
+    _, lse = B.bitlinear_linear_ce_fwd(xd, wd, yd)
+    want, _ = B.bitlinear_linear_ce_bwd(xd, wd, yd, lse, gd)
+    gd[t // 2] = bad
+    gx, gw = B.bitlinear_linear_ce_bwd(xd, wd, yd, lse, gd)
+    keep = torch.arange(t, device="cuda") != t // 2
+    assert torch.equal(gx[keep], want[keep]) and not want[t // 2].any()
+    assert not torch.isfinite(gx[t // 2]).any() and not torch.isfinite(gw[5]).any()
+
+
 def test_linear_ce_empty_batch():
     w = torch.randn(50, 64, device="cuda").to(torch.bfloat16)
     x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
