@@ -54,6 +54,21 @@ def _size(fn: str, *args) -> int:
     return int(getattr(lib(), fn)(*args))
 
 
+def _workspace(given, need: int, x: torch.Tensor, stream):
+    """The caller's workspace, or one of this call. The latter goes back to the allocator as
+    soon as the call returns: work on a stream other than the current one has to be over
+    before its memory is handed out again."""
+    if given is not None:
+        _need_bytes(given, need, "workspace", x.device)
+        return given
+    if not need:
+        return None
+    own = x.new_empty((need,), dtype=torch.uint8)
+    if stream is not None:
+        own.record_stream(stream)
+    return own
+
+
 def fp8_scales_shape(rows: int, cols: int) -> tuple[int, int, int]:
     """Shape of the scales of [rows, cols] codes: block b of row r at [b // 4, r, b % 4]."""
     return (cols + 511) // 512, rows, 4
@@ -136,10 +151,7 @@ def bitlinear_fp8_fwd(x: torch.Tensor, w_q: torch.Tensor, w_scales: torch.Tensor
     if y.dtype != torch.bfloat16 and y.dtype != torch.float32:
         raise TypeError(f"y: expected bfloat16 or float32, got {y.dtype}")
     need = _size("bitlinear_fp8_fwd_workspace_size", t, k_in, x_type) if x_type == BL_X_BF16 else 0
-    if workspace is not None:
-        _need_bytes(workspace, need, "workspace", dev)
-    elif need:
-        workspace = x.new_empty((need,), dtype=torch.uint8)
+    workspace = _workspace(workspace, need, x, stream)
     st = _launch(lib().bitlinear_fp8_fwd, dev, stream, _ptr(x), x_type, _ptr(x_scales), _ptr(w_q), w_fmt, _ptr(w_scales),
                t, k_in, n_out, _ptr(y), BL_OUT_F32 if y.dtype == torch.float32 else BL_OUT_BF16, _ptr(workspace),
                0 if workspace is None else workspace.numel())
@@ -231,10 +243,7 @@ def bitlinear_linear_ce_fwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Ten
     else:
         _check(lse, torch.float32, (t,), "lse", dev)
     need = bitlinear_linear_ce_fwd_workspace_size(t, v)
-    if workspace is not None:
-        _need_bytes(workspace, need, "workspace", dev)
-    elif need:
-        workspace = x.new_empty((need,), dtype=torch.uint8)
+    workspace = _workspace(workspace, need, x, stream)
     st = _launch(lib().bitlinear_linear_ce_fwd, dev, stream, _ptr(x), _ptr(w), _ptr(targets), t, k_in, v, _ptr(loss),
                _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel())
     check(st, "bitlinear_linear_ce_fwd")
@@ -269,10 +278,7 @@ def bitlinear_linear_ce_bwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Ten
         _check(grad_w, grad_w.dtype, (v, k_in), "grad_w", dev)
     gwdt = BL_OUT_F32 if grad_w is not None and grad_w.dtype == torch.float32 else BL_OUT_BF16
     need = bitlinear_linear_ce_bwd_workspace_size(t, k_in, v, grad_x is not None)
-    if workspace is not None:
-        _need_bytes(workspace, need, "workspace", dev)
-    elif need:
-        workspace = x.new_empty((need,), dtype=torch.uint8)
+    workspace = _workspace(workspace, need, x, stream)
     st = _launch(lib().bitlinear_linear_ce_bwd, dev, stream, _ptr(x), _ptr(w), _ptr(targets), _ptr(lse), _ptr(grad_loss), t,
                k_in, v, _ptr(grad_x), _ptr(grad_w), gwdt, _ptr(workspace), 0 if workspace is None else workspace.numel())
     check(st, "bitlinear_linear_ce_bwd")

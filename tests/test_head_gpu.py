@@ -525,3 +525,23 @@ def test_streams_other_than_the_current_one():
     got = B.bitlinear_fp8_fwd(x, w["q"], w["scales"], stream=s)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_own_workspace_on_another_stream():
+    # the call's own workspace is not handed out again while its stream still has the work
+    # before it: an allocation of the same size right after the call must not be that memory
+    t, k, n = 300, 512, 64
+    x = torch.randn(t, k, device="cuda").to(torch.bfloat16)
+    w = B.bitlinear_fp8_quant_weight(torch.randn(n, k, device="cuda"))
+    need = B.bitlinear_fp8_fwd_workspace_size(t, k)
+    assert need > 0
+    want, y = B.bitlinear_fp8_fwd(x, w["q"], w["scales"]), torch.empty(t, n, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    B.bitlinear_fp8_fwd(x, w["q"], w["scales"], y=y, stream=s)
+    ran = s.query()
+    junk = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert not ran and torch.equal(y, want) and junk.numel() == need

@@ -166,3 +166,23 @@ def test_scales_shape():
     assert B.fp8_scales_shape(7, 64) == (1, 7, 4) and B.fp8_scales_shape(1, 513) == (2, 1, 4)
     assert B.fp8_scales_shape(5, 0) == (0, 5, 4)
     assert set(head.__all__) <= set(dir(head))
+
+
+def test_own_workspace_is_recorded_on_a_given_stream():
+    class Memory:
+        stream = None
+
+        def record_stream(self, stream):
+            self.stream = stream
+
+    class X:
+        device = torch.device("cpu")
+
+        def new_empty(self, shape, dtype):
+            assert shape == (64,) and dtype == torch.uint8
+            return Memory()
+
+    side = object()
+    assert head._workspace(None, 64, X(), side).stream is side
+    assert head._workspace(None, 64, X(), None).stream is None
+    assert head._workspace(None, 0, X(), side) is None
