@@ -545,3 +545,40 @@ def test_own_workspace_on_another_stream():
     junk = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     assert not ran and torch.equal(y, want) and junk.numel() == need
+
+
+def test_more_than_2_to_31_elements():
+    # 384 rows over and over: the last copy, whose offsets pass 32 bits, comes out as the first
+    reps, rows, k, n = 2732, 384, 2048, 16
+    rng = np.random.default_rng(13)
+    base = bf16(rng, rows, k, scale=2.0 / np.sqrt(k), outliers=False)
+    small = dev(base, torch.bfloat16)
+    big = small.repeat(reps, 1)
+    assert big.numel() > 2 ** 31
+    q, first = B.bitlinear_fp8_quant(big, want_t=True), B.bitlinear_fp8_quant(small, want_t=True)
+    last = slice((reps - 1) * rows, reps * rows)
+    for at in (slice(0, rows), last):
+        assert np.array_equal(u8(q["q"][at]), u8(first["q"])) and np.array_equal(u8(q["qt"][:, at]), u8(first["qt"]))
+        assert torch.equal(q["scales"][:, at], first["scales"])
+    w = B.bitlinear_fp8_quant_weight(dev(rng.normal(size=(n, k)).astype(np.float32)))
+    y = B.bitlinear_fp8_fwd(q["q"], w["q"], w["scales"], x_scales=q["scales"])
+    assert torch.equal(y[last], y[:rows]) and y[last].any()
+    del q, y
+
+    for t in (3, 40):   # `big` as the vocabulary, targets in its last copy
+        x, g = bf16(rng, t, k, outliers=False), rng.normal(size=t).astype(np.float32)
+        y = rng.integers(0, rows, t)
+        xd, yd = dev(x, torch.bfloat16), dev(y) + (reps - 1) * rows
+        loss, lse = B.bitlinear_linear_ce_fwd(xd, big, yd)
+        o, d = H.linear_ce(x, base, y, g), logit_errors(x, base, k)
+        p, onehot = o["p"] / reps, np.zeros((t, rows))
+        onehot[np.arange(t), y] = 1.0
+        o.update(lse=o["lse"] + np.log(reps), loss=o["loss"] + np.log(reps))
+        check_loss(loss, lse, o, d)
+        gw = B.bitlinear_linear_ce_bwd(xd, big, yd, lse, dev(g), want_grad_x=False)[1][last]
+        dl = p * np.sign(g)[:, None] - onehot * g[:, None]
+        spread = 2 * d + 2.0 ** -20 + 8 * U * np.abs(o["logits"]).max(axis=1) + 4 * U * np.abs(o["lse"])   # as in check_ce_grads
+        err = (BF16 * np.abs(dl) + (1 + BF16) * p * np.expm1(spread)[:, None]).T @ np.abs(x)
+        want = dl.T @ x
+        tol = err + acc_bound(t + 256, 16, np.abs(dl).T @ np.abs(x)) + BF16 * (np.abs(want) + err) + 1e-37
+        assert np.all(np.abs(f64(gw) - want) <= tol)
