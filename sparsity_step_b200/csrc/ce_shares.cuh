@@ -1,5 +1,5 @@
-// Which tiles of the products of one launch every CTA pair computes (linear_ce.cuh). Host
-// code but for ce_round_tile.
+// Which tiles of the products of one launch every CTA pair computes (linear_ce.cuh,
+// gemm_fp8.cuh). Host code but for ce_round_tile.
 #pragma once
 
 #include <stdint.h>

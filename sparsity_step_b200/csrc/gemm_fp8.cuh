@@ -21,6 +21,10 @@
 //     the epilogue still drains half 1, then on half 1, so the tensor cores do not wait.
 //   kHalves = 1: one accumulator per tile, the other one drained meanwhile; 30 KB per 448
 //     MMA cycles. For products with too few wide tiles to fill the SMs evenly, or short K.
+// A launch takes up to two products, the two gradients of a backward pass, so that the
+// second fills the SMs while the first runs out (ce_shares.cuh): both gradients of 4095 x
+// 896 x 4864 took 40.0 us in two launches and take 28.2, of 777 x 1536 x 8960 45.2 and 28.1,
+// of 4096 x 11008 x 2048 157 and 140.
 // What bounds it: 8192 tokens, 2048 -> 11008 take 133-145 us (2.5-2.8 PFLOP/s), the loads
 // alone 84, the MMAs alone 110, and with all-zero operands the whole kernel 126 at full
 // clock, while with real ones the card runs into its 1000 W (1432 MHz in a long loop, 168
@@ -40,6 +44,7 @@
 // Every wait is bounded. No load uses multicast.
 #pragma once
 
+#include "ce_shares.cuh"
 #include "pair_issue.cuh"
 
 namespace bl {
@@ -78,7 +83,8 @@ constexpr size_t gemm_fp8_smem_bytes() {
 }
 static_assert(gemm_fp8_smem_bytes() <= 232448, "fp8 GEMM exceeds the shared memory of a CTA");
 
-struct Fp8GemmArgs {
+struct Fp8Problem {
+  CUtensorMap tmA, tmB, tmOut;
   const uint32_t* sa;   // [ceil(K / 512), M] words of A's scale bytes
   const uint32_t* sb;   // [ceil(K / 512), N]
   int M, N;
@@ -88,6 +94,13 @@ struct Fp8GemmArgs {
   int m_fastest;
   int a_e5m2, b_e5m2;
   int out_f32;
+};
+// The products of one launch, the tiles of each shared out by ce_shares.cuh.
+constexpr int kMaxFp8Group = 2;
+struct Fp8Group {
+  Fp8Problem p[kMaxFp8Group];
+  CeShares share[kMaxFp8Group];
+  int count;
 };
 
 // Instruction descriptor of a block-scaled MMA (kind::mxf8f6f4): b scale id [4,6),
@@ -114,7 +127,7 @@ __device__ __forceinline__ uint64_t make_sf_desc(uint32_t saddr) {   // 8-row co
   return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(1) << 16 |
          static_cast<uint64_t>(128 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
 }
-__device__ __forceinline__ void fp8_tile_coords(const Fp8GemmArgs& g, int tile, int& mb, int& nb) {
+__device__ __forceinline__ void fp8_tile_coords(const Fp8Problem& g, int tile, int& mb, int& nb) {
   if (g.m_fastest) {
     mb = tile % g.num_m_blocks;
     nb = tile / g.num_m_blocks;
@@ -125,9 +138,7 @@ __device__ __forceinline__ void fp8_tile_coords(const Fp8GemmArgs& g, int tile, 
 }
 
 template <int kHalves>
-__global__ void __launch_bounds__(kF8Threads, 1)
-    gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const __grid_constant__ CUtensorMap tmOut, const Fp8GemmArgs g) {
+__global__ void __launch_bounds__(kF8Threads, 1) gemm_fp8_kernel(const __grid_constant__ Fp8Group G) {
   using S = F8Stage<kHalves>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -167,9 +178,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     mbar_init(done_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
-    tma_prefetch_desc(&tmOut);
+    for (int j = 0; j < G.count; ++j) {
+      tma_prefetch_desc(&G.p[j].tmA);
+      tma_prefetch_desc(&G.p[j].tmB);
+      tma_prefetch_desc(&G.p[j].tmOut);
+    }
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), 512);
@@ -181,39 +194,40 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   follow_stream();
   const uint32_t tmem_base = __reduce_or_sync(0xffffffffu, *tmem_slot);   // the same in every lane: a uniform register
   const uint32_t peer_abort = map_to_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
-  const int num_tiles = g.num_m_blocks * g.num_n_blocks;
-  const int num_k_groups = (g.num_k_blocks + 3) >> 2;
   const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
-  const int n_tile = kHalves * g.n_half;
 
   if (warp == 0) {
     // ------------------------------------------------------------- TMA producer (both CTAs)
     const uint32_t full_leader0 = __reduce_or_sync(0xffffffffu, map_to_rank(full0, 0));
-    const int my_n = g.n_half >> 1;   // columns of each half that this CTA loads
-    const uint32_t stage_bytes = 2u * static_cast<uint32_t>(kF8ABytes + kHalves * my_n * 128);   // of both CTAs
     uint32_t live = 1;   // 0 after a wait gave up: the loops run out without issuing or waiting
     int s = 0;
     uint32_t ph = 0;
     uint32_t issued = 0;
-    for (int tile = cluster; tile < num_tiles; tile += nclusters) {
-      int mb, nb;
-      fp8_tile_coords(g, tile, mb, nb);
-      const int m0 = mb * 256 + 128 * static_cast<int>(rank);
-      const int n0 = nb * n_tile + my_n * static_cast<int>(rank);
-      for (int kb = 0; kb < g.num_k_blocks; ++kb) {
-        live = wait_live<false>(live, empty0 + 8u * s, ph ^ 1u, abort_flag, peer_abort);
-        const uint32_t fb = full_leader0 + 8u * s;
-        if (elect_one() && live) {
-          if (leader) mbar_arrive_expect_tx(full0 + 8u * s, stage_bytes);
-          tma_load_2d_pair(st_a(s), &tmA, fb, kb * 128, m0);
+    for (int j = 0; j < G.count; ++j) {
+      const Fp8Problem& P = G.p[j];
+      const int rounds = G.share[j].count[cluster], pos = G.share[j].pos[cluster];
+      const int my_n = P.n_half >> 1;   // columns of each half that this CTA loads
+      const uint32_t stage_bytes = 2u * static_cast<uint32_t>(kF8ABytes + kHalves * my_n * 128);   // of both CTAs
+      for (int r = 0; r < rounds; ++r) {
+        int mb, nb;
+        fp8_tile_coords(P, ce_round_tile(G.share[j], nclusters, pos, r), mb, nb);
+        const int m0 = mb * 256 + 128 * static_cast<int>(rank);
+        const int n0 = nb * kHalves * P.n_half + my_n * static_cast<int>(rank);
+        for (int kb = 0; kb < P.num_k_blocks; ++kb) {
+          live = wait_live<false>(live, empty0 + 8u * s, ph ^ 1u, abort_flag, peer_abort);
+          const uint32_t fb = full_leader0 + 8u * s;
+          if (elect_one() && live) {
+            if (leader) mbar_arrive_expect_tx(full0 + 8u * s, stage_bytes);
+            tma_load_2d_pair(st_a(s), &P.tmA, fb, kb * 128, m0);
 #pragma unroll
-          for (int half = 0; half < kHalves; ++half)
-            tma_load_2d_pair(st_b(s, half), &tmB, fb, kb * 128, n0 + half * g.n_half);
-        }
-        issued += live;
-        if (++s == S::kCount) {
-          s = 0;
-          ph ^= 1u;
+            for (int half = 0; half < kHalves; ++half)
+              tma_load_2d_pair(st_b(s, half), &P.tmB, fb, kb * 128, n0 + half * P.n_half);
+          }
+          issued += live;
+          if (++s == S::kCount) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
       }
     }
@@ -229,8 +243,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA issuer (leader only)
     if (leader) {
-      const uint32_t idesc0 = make_idesc_mxf8(g.a_e5m2, g.b_e5m2, g.n_half, 256, 0);
-      const bool wide = g.n_half > 128;
+      uint32_t idesc0 = 0;       // of the current product
+      bool wide = false;
       uint32_t live = 1;         // 0 after a wait gave up: the loops run out without issuing or waiting
       int s = 0, f = 0;          // next stage and scale slot
       uint32_t ph = 0, fph = 0;
@@ -272,67 +286,73 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         }
       };
       uint32_t tph = 1;   // phase of the accumulators' buffers
-      for (int tile = cluster, local = 0; tile < num_tiles; tile += nclusters, ++local) {
-        if constexpr (kHalves == 1) {
-          const int buf = local & 1;
-          live = wait_live<false>(live, tempty0 + 8u * buf, tph, abort_flag, peer_abort);
-          tc_fence_after_sync();
-          for (int kb = 0; kb < g.num_k_blocks; ++kb) {
-            if ((kb & 3) == 0) scales();
-            live = wait_live<false>(live, full0 + 8u * s, ph, abort_flag, peer_abort);
+      int local = 0;
+      for (int j = 0; j < G.count; ++j) {
+        const int rounds = G.share[j].count[cluster], num_k_blocks = G.p[j].num_k_blocks;
+        idesc0 = __reduce_or_sync(0xffffffffu, make_idesc_mxf8(G.p[j].a_e5m2, G.p[j].b_e5m2, G.p[j].n_half, 256, 0));
+        wide = G.p[j].n_half > 128;
+        for (int r = 0; r < rounds; ++r, ++local) {
+          if constexpr (kHalves == 1) {
+            const int buf = local & 1;
+            live = wait_live<false>(live, tempty0 + 8u * buf, tph, abort_flag, peer_abort);
             tc_fence_after_sync();
-            if (elect_one() && live) {
-              block(s, 0, buf, kb);
-              tc_commit_pair(empty0 + 8u * s);
-              if (kb + 1 == g.num_k_blocks) tc_commit_pair(tfull0 + 8u * buf);
+            for (int kb = 0; kb < num_k_blocks; ++kb) {
+              if ((kb & 3) == 0) scales();
+              live = wait_live<false>(live, full0 + 8u * s, ph, abort_flag, peer_abort);
+              tc_fence_after_sync();
+              if (elect_one() && live) {
+                block(s, 0, buf, kb);
+                tc_commit_pair(empty0 + 8u * s);
+                if (kb + 1 == num_k_blocks) tc_commit_pair(tfull0 + 8u * buf);
+              }
+              next_stage();
             }
-            next_stage();
-          }
-          tph ^= static_cast<uint32_t>(buf);
-        } else {
-          // the first K blocks (at most a ring of them, one scale group) on half 0, then on half 1
-          const int lead = min(S::kCount, g.num_k_blocks);
-          live = wait_live<false>(live, tempty0, tph, abort_flag, peer_abort);
-          scales();
-          int st = s;
-          uint32_t sph = ph;
-          for (int kb = 0; kb < lead; ++kb) {
-            live = wait_live<false>(live, full0 + 8u * st, sph, abort_flag, peer_abort);
+            tph ^= static_cast<uint32_t>(buf);
+          } else {
+            // the first K blocks (at most a ring of them, one scale group) on half 0, then on half 1
+            const int lead = min(S::kCount, num_k_blocks);
+            live = wait_live<false>(live, tempty0, tph, abort_flag, peer_abort);
+            scales();
+            int st = s;
+            uint32_t sph = ph;
+            for (int kb = 0; kb < lead; ++kb) {
+              live = wait_live<false>(live, full0 + 8u * st, sph, abort_flag, peer_abort);
+              tc_fence_after_sync();
+              if (elect_one() && live) {
+                block(st, 0, 0, kb);
+                if (kb == num_k_blocks - 1) tc_commit_pair(tfull0);
+              }
+              if (++st == S::kCount) {
+                st = 0;
+                sph ^= 1u;
+              }
+            }
+            live = wait_live<false>(live, tempty0 + 8u, tph, abort_flag, peer_abort);
             tc_fence_after_sync();
-            if (elect_one() && live) {
-              block(st, 0, 0, kb);
-              if (kb == g.num_k_blocks - 1) tc_commit_pair(tfull0);
+            for (int kb = 0; kb < lead; ++kb) {
+              if (elect_one() && live) {
+                block(s, 1, 1, kb);
+                tc_commit_pair(empty0 + 8u * s);
+                if (kb == num_k_blocks - 1) tc_commit_pair(tfull0 + 8u);
+              }
+              next_stage();
             }
-            if (++st == S::kCount) {
-              st = 0;
-              sph ^= 1u;
+            for (int kb = lead; kb < num_k_blocks; ++kb) {
+              if ((kb & 3) == 0) scales();
+              live = wait_live<false>(live, full0 + 8u * s, ph, abort_flag, peer_abort);
+              tc_fence_after_sync();
+              if (elect_one() && live) {
+                const bool end = kb == num_k_blocks - 1;
+                block(s, 0, 0, kb);
+                if (end) tc_commit_pair(tfull0);
+                block(s, 1, 1, kb);
+                tc_commit_pair(empty0 + 8u * s);
+                if (end) tc_commit_pair(tfull0 + 8u);
+              }
+              next_stage();
             }
+            tph ^= 1u;
           }
-          live = wait_live<false>(live, tempty0 + 8u, tph, abort_flag, peer_abort);
-          tc_fence_after_sync();
-          for (int kb = 0; kb < lead; ++kb) {
-            if (elect_one() && live) {
-              block(s, 1, 1, kb);
-              tc_commit_pair(empty0 + 8u * s);
-              if (kb == g.num_k_blocks - 1) tc_commit_pair(tfull0 + 8u);
-            }
-            next_stage();
-          }
-          for (int kb = lead; kb < g.num_k_blocks; ++kb) {
-            if ((kb & 3) == 0) scales();
-            live = wait_live<false>(live, full0 + 8u * s, ph, abort_flag, peer_abort);
-            tc_fence_after_sync();
-            if (elect_one() && live) {
-              const bool end = kb == g.num_k_blocks - 1;
-              block(s, 0, 0, kb);
-              if (end) tc_commit_pair(tfull0);
-              block(s, 1, 1, kb);
-              tc_commit_pair(empty0 + 8u * s);
-              if (end) tc_commit_pair(tfull0 + 8u);
-            }
-            next_stage();
-          }
-          tph ^= 1u;
         }
       }
       if (elect_one()) {
@@ -348,45 +368,68 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     uint32_t fph = 0;
     bool ok = true;
     uint32_t w[4 * S::kSfGroups];
-    auto load = [&](int tile, int kg) {   // rows past the operands' ends (zero codes) get scale byte 0
+    // The next words' place: coordinates are worked out once a tile. (Once every four K
+    // blocks they held up the products with little else to do: 2048 x 11008 x 2048 took 40.4
+    // us instead of 36.)
+    const uint32_t *pa = nullptr, *pb = nullptr;
+    int M = 0, N = 0, n_half = 0, m0 = 0, n0 = 0;
+    int j = 0, r = 0, left = 0;   // product, round, and what the tile has left of four K blocks each
+    auto aim = [&]() {            // at the pair's next tile; none: left stays 0
+      while (j < G.count && r == G.share[j].count[cluster]) {
+        ++j;
+        r = 0;
+      }
+      if (j == G.count) return;
+      const Fp8Problem& P = G.p[j];
       int mb, nb;
-      fp8_tile_coords(g, tile, mb, nb);
-      const int m0 = mb * 256 + 128 * static_cast<int>(rank) + lane, n0 = nb * n_tile + lane;
-      const uint32_t* pa = g.sa + static_cast<int64_t>(kg) * g.M;
-      const uint32_t* pb = g.sb + static_cast<int64_t>(kg) * g.N;
+      fp8_tile_coords(P, ce_round_tile(G.share[j], nclusters, G.share[j].pos[cluster], r), mb, nb);
+      m0 = mb * 256 + 128 * static_cast<int>(rank) + lane;
+      n0 = nb * kHalves * P.n_half + lane;
+      M = P.M;
+      N = P.N;
+      n_half = P.n_half;
+      pa = P.sa + m0;
+      pb = P.sb + n0;
+      left = (P.num_k_blocks + 3) >> 2;
+    };
+    auto load = [&]() {   // rows past the operands' ends (zero codes) get scale byte 0
 #pragma unroll
-      for (int c = 0; c < 4; ++c) w[c] = m0 + 32 * c < g.M ? ld_plain(pa + m0 + 32 * c) : 0u;
+      for (int c = 0; c < 4; ++c) w[c] = m0 + 32 * c < M ? ld_plain(pa + 32 * c) : 0u;
 #pragma unroll
       for (int c = 0; c < 8 * kHalves; ++c) {
-        const int in_half = 32 * (c & 7), n = n0 + (c >> 3) * g.n_half + in_half;
-        w[4 + c] = in_half < g.n_half && n < g.N ? ld_plain(pb + n) : 0u;
+        const int in_half = 32 * (c & 7), at = (c >> 3) * n_half + in_half;
+        w[4 + c] = in_half < n_half && n0 + at < N ? ld_plain(pb + at) : 0u;
       }
+      pa += M;
+      pb += N;
     };
-    if (cluster < num_tiles) load(cluster, 0);
-    for (int tile = cluster; tile < num_tiles && ok; tile += nclusters) {
-      for (int kg = 0; kg < num_k_groups; ++kg) {
-        const bool got = mbar_wait(sfempty0 + 8u * f, fph ^ 1u, abort_flag);
-        if (!__all_sync(0xffffffffu, got)) {
-          ok = false;
-          break;
-        }
-        const uint32_t dst = sSf + static_cast<uint32_t>(f * S::kSfGroups * 512 + lane * 16);
+    aim();
+    if (left) load();
+    while (left) {
+      const bool got = mbar_wait(sfempty0 + 8u * f, fph ^ 1u, abort_flag);
+      if (!__all_sync(0xffffffffu, got)) {
+        ok = false;
+        break;
+      }
+      const uint32_t dst = sSf + static_cast<uint32_t>(f * S::kSfGroups * 512 + lane * 16);
 #pragma unroll
-        for (int j = 0; j < S::kSfGroups; ++j)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512u * j), "r"(w[4 * j]), "r"(w[4 * j + 1]),
-                       "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
-                       : "memory");
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(sffull_leader0 + 8u * f);
-        // after the fence, which would wait for them: the next group's words travel while
-        // this warp waits for a free slot
-        if (kg + 1 < num_k_groups) load(tile, kg + 1);
-        else if (tile + nclusters < num_tiles) load(tile + nclusters, 0);
-        if (++f == S::kSfSlots) {
-          f = 0;
-          fph ^= 1u;
-        }
+      for (int i = 0; i < S::kSfGroups; ++i)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512u * i), "r"(w[4 * i]), "r"(w[4 * i + 1]),
+                     "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+                     : "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(sffull_leader0 + 8u * f);
+      // after the fence, which would wait for them: the next group's words travel while
+      // this warp waits for a free slot
+      if (--left == 0) {
+        ++r;
+        aim();
+      }
+      if (left) load();
+      if (++f == S::kSfSlots) {
+        f = 0;
+        fph ^= 1u;
       }
     }
     if (!ok && lane == 0) {
@@ -399,73 +442,79 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     // TMEM -> registers -> staging (swizzled by the store's tensor map) -> TMA store
     const int e = warp - 2;
     const int quad = warp & 3;
-    const int pieces = g.n_half >> 5;
-    const int first = (e >> 2) ? (pieces + 1) >> 1 : 0, last = (e >> 2) ? pieces : (pieces + 1) >> 1;
     const uint32_t stg0 = sOut + static_cast<uint32_t>(e * kF8StgBytes);
     const uint32_t tempty_leader0 = map_to_rank(tempty0, 0);
     int cnt = 0;
     int unit = 0;   // accumulators so far: unit u is in buffer u & 1
     bool ok = true;
-    for (int tile = cluster; tile < num_tiles && ok; tile += nclusters) {
-      int mb, nb;
-      fp8_tile_coords(g, tile, mb, nb);
-      const int row0 = mb * 256 + 128 * static_cast<int>(rank) + quad * 32;
+    for (int j = 0; j < G.count && ok; ++j) {
+      const Fp8Problem& P = G.p[j];
+      const int rounds = G.share[j].count[cluster], pos = G.share[j].pos[cluster];
+      const int pieces = P.n_half >> 5;
+      const int first = (e >> 2) ? (pieces + 1) >> 1 : 0, last = (e >> 2) ? pieces : (pieces + 1) >> 1;
+      if (lane == 0) bulk_wait_group_read<0>();   // the staging buffer's use depends on the output type
+      __syncwarp();
+      for (int r = 0; r < rounds && ok; ++r) {
+        int mb, nb;
+        fp8_tile_coords(P, ce_round_tile(G.share[j], nclusters, pos, r), mb, nb);
+        const int row0 = mb * 256 + 128 * static_cast<int>(rank) + quad * 32;
 #pragma unroll 1
-      for (int half = 0; half < kHalves; ++half, ++unit) {
-        const int buf = unit & 1;
-        const int n0 = nb * n_tile + half * g.n_half;
-        const bool got = mbar_wait(tfull0 + 8u * buf, static_cast<uint32_t>(unit >> 1) & 1u, abort_flag);
-        if (!__all_sync(0xffffffffu, got)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        // all of the warp's columns to registers at once, so that the accumulator is free
-        // again after one TMEM latency, not after the conversion and the stores
-        const uint32_t t_row = tmem_base + static_cast<uint32_t>(buf * kF8MaxN + first * 32) + (static_cast<uint32_t>(quad * 32) << 16);
-        uint32_t r[4][32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (first + i < last) tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(i * 32), r[i]);
-        tmem_ld_wait();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8u * buf);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (first + i >= last) break;
-          const int col = n0 + (first + i) * 32;
-          if (lane == 0) {   // the buffer's previous store has finished reading it
-            if (g.out_f32) bulk_wait_group_read<0>();
-            else bulk_wait_group_read<1>();
+        for (int half = 0; half < kHalves; ++half, ++unit) {
+          const int buf = unit & 1;
+          const int n0 = (nb * kHalves + half) * P.n_half;
+          const bool got = mbar_wait(tfull0 + 8u * buf, static_cast<uint32_t>(unit >> 1) & 1u, abort_flag);
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
           }
+          tc_fence_after_sync();
+          // all of the warp's columns to registers at once, so that the accumulator is free
+          // again after one TMEM latency, not after the conversion and the stores
+          const uint32_t t_row = tmem_base + static_cast<uint32_t>(buf * kF8MaxN + first * 32) + (static_cast<uint32_t>(quad * 32) << 16);
+          uint32_t v[4][32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (first + i < last) tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(i * 32), v[i]);
+          tmem_ld_wait();
+          tc_fence_before_sync();
           __syncwarp();
-          const uint32_t stg = g.out_f32 ? stg0 : stg0 + static_cast<uint32_t>((cnt++ & 1) * 2048);
-          if (g.out_f32) {   // 128-byte rows, 128B swizzle: chunk j at j ^ (row & 7)
-            const uint32_t row_addr = stg + static_cast<uint32_t>(lane) * 128u;
+          if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8u * buf);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_addr + static_cast<uint32_t>((j ^ (lane & 7)) * 16)),
-                           "r"(r[i][4 * j]), "r"(r[i][4 * j + 1]), "r"(r[i][4 * j + 2]), "r"(r[i][4 * j + 3])
-                           : "memory");
-          } else {           // 64-byte rows, 64B swizzle: chunk j at j ^ ((row >> 1) & 3)
-            const uint32_t row_addr = stg + static_cast<uint32_t>(lane) * 64u;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t w[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                w[q] = pack_bf16x2(__uint_as_float(r[i][8 * j + 2 * q]), __uint_as_float(r[i][8 * j + 2 * q + 1]));
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_addr + static_cast<uint32_t>((j ^ ((lane >> 1) & 3)) * 16)),
-                           "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                           : "memory");
+          for (int i = 0; i < 4; ++i) {
+            if (first + i >= last) break;
+            const int col = n0 + (first + i) * 32;
+            if (lane == 0) {   // the buffer's previous store has finished reading it
+              if (P.out_f32) bulk_wait_group_read<0>();
+              else bulk_wait_group_read<1>();
             }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (col < g.N) tma_store_2d(&tmOut, stg, col, row0);
-            bulk_commit_group();
+            __syncwarp();
+            const uint32_t stg = P.out_f32 ? stg0 : stg0 + static_cast<uint32_t>((cnt++ & 1) * 2048);
+            if (P.out_f32) {   // 128-byte rows, 128B swizzle: chunk j at j ^ (row & 7)
+              const uint32_t row_addr = stg + static_cast<uint32_t>(lane) * 128u;
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_addr + static_cast<uint32_t>((j ^ (lane & 7)) * 16)),
+                             "r"(v[i][4 * j]), "r"(v[i][4 * j + 1]), "r"(v[i][4 * j + 2]), "r"(v[i][4 * j + 3])
+                             : "memory");
+            } else {           // 64-byte rows, 64B swizzle: chunk j at j ^ ((row >> 1) & 3)
+              const uint32_t row_addr = stg + static_cast<uint32_t>(lane) * 64u;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t w[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  w[q] = pack_bf16x2(__uint_as_float(v[i][8 * j + 2 * q]), __uint_as_float(v[i][8 * j + 2 * q + 1]));
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_addr + static_cast<uint32_t>((j ^ ((lane >> 1) & 3)) * 16)),
+                             "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                             : "memory");
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (col < P.N) tma_store_2d(&P.tmOut, stg, col, row0);
+              bulk_commit_group();
+            }
           }
         }
       }

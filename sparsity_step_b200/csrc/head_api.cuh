@@ -81,6 +81,14 @@ struct Fp8Operand {
   int e5m2;
 };
 
+// out[m, n] = A B^T with both operands' reduction of length k (codes [rows, k], k % 16 == 0).
+struct Fp8Job {
+  Fp8Operand A, B;
+  int64_t k;
+  void* out;
+  bool f32;
+};
+
 // Tiles of the pair product: one or two accumulators of a multiple of 32 columns, whichever
 // has the least modelled time in cycles. Per 128 of K a tile costs the larger of its MMAs (2
 // a column) and its operand loads (128 rows of A and half its columns of B, 128 bytes each,
@@ -88,71 +96,115 @@ struct Fp8Operand {
 // two accumulators are drained one after the other, 5000; whole waves of tiles over the
 // pairs decide. Over 16 shapes (300 to 16384 rows, K 896 to 11008) the choice was within 3%
 // of the best of all 14 tiles; the widest tile alone would be up to 1.5 times slower.
+// Two products in one launch are taken by their common end (the levels of ce_shares.cuh),
+// over the wider tiles: over 12 shapes the choice was within 1.3% of the best of 72 pairs of
+// tiles on average (6% at most); the least sum of work, which may leave one deep tile behind,
+// within 12% (46%).
 struct Fp8Tiles {
-  int halves, n_half;
+  int halves, n_half[bl::kMaxFp8Group];
+  int64_t tiles[bl::kMaxFp8Group], cost[bl::kMaxFp8Group];
 };
-Fp8Tiles fp8_tiles(int64_t m, int64_t n, int64_t k_blocks, int pairs) {
-  const int64_t mb = (m + 255) / 256;
-  Fp8Tiles best{1, 32};
-  double best_cost = 1e300;
+// When `pairs` pairs end that take n0 tiles of cost c0 in turn and then n1 of c1, each on the
+// least loaded pair: the least level below which n1 of them fit.
+int64_t fp8_common_end(int64_t n0, int64_t c0, int64_t n1, int64_t c1, int64_t pairs) {
+  const int64_t above = n0 % pairs, low = n0 / pairs * c0, high = above ? low + c0 : low;   // loads after the first product
+  const int64_t alone = low + (n1 + pairs - above - 1) / (pairs - above) * c1;   // on the less loaded pairs
+  if (alone < high + c1) return alone > high ? alone : high;
+  int64_t level = (n0 * c0 + n1 * c1) / pairs;   // the mean load: no end is earlier
+  if (level < high) level = high;
+  for (;;) {
+    const int64_t l = (level - low) / c1, h = (level - high) / c1;
+    if (above * h + (pairs - above) * l >= n1) return level;
+    const int64_t next_l = low + (l + 1) * c1, next_h = high + (h + 1) * c1;
+    level = next_l < next_h ? next_l : next_h;
+  }
+}
+Fp8Tiles fp8_tiles(const Fp8Job* jobs, int count, int pairs) {
+  auto cover = [&](int j, int halves, int w, int64_t* tiles, int64_t* cost) {
+    const int64_t cols = int64_t(halves) * w, k_blocks = (jobs[j].k + 127) / 128;
+    *tiles = (jobs[j].A.rows + 255) / 256 * ((jobs[j].B.rows + cols - 1) / cols);
+    const double mma = 2.0 * cols, load = (128 + cols / 2) * 128.0 / 40.0;
+    *cost = static_cast<int64_t>(double(k_blocks) * (mma > load ? mma : load)) + (halves == 2 ? 5000 : 1500);
+  };
+  Fp8Tiles best{};
+  int64_t best_end = INT64_MAX;
   for (int halves = 1; halves <= 2; ++halves)
-    for (int w = 32; w <= bl::kF8MaxN; w += 32) {
-      const int64_t cols = int64_t(halves) * w;
-      const int64_t waves = (mb * ((n + cols - 1) / cols) + pairs - 1) / pairs;
-      const double mma = 2.0 * cols, load = (128 + cols / 2) * 128.0 / 40.0;
-      const double cost = double(waves) * (double(k_blocks) * (mma > load ? mma : load) + (halves == 2 ? 5000.0 : 1500.0));
-      if (cost <= best_cost) {
-        best = {halves, w};
-        best_cost = cost;
+    for (int w0 = 32; w0 <= bl::kF8MaxN; w0 += 32) {
+      Fp8Tiles t{};
+      t.halves = halves;
+      t.n_half[0] = w0;
+      cover(0, halves, w0, &t.tiles[0], &t.cost[0]);
+      if (count == 1) {
+        const int64_t end = (t.tiles[0] + pairs - 1) / pairs * t.cost[0];
+        if (end <= best_end) best = t, best_end = end;
+        continue;
+      }
+      if (w0 < 96 && halves * w0 < jobs[0].B.rows) continue;
+      for (int w1 = 32; w1 <= bl::kF8MaxN; w1 += 32) {
+        if (w1 < 96 && halves * w1 < jobs[1].B.rows) continue;
+        t.n_half[1] = w1;
+        cover(1, halves, w1, &t.tiles[1], &t.cost[1]);
+        const int64_t end = fp8_common_end(t.tiles[0], t.cost[0], t.tiles[1], t.cost[1], pairs);
+        if (end <= best_end) best = t, best_end = end;
       }
     }
   return best;
 }
 
 template <int kHalves>
-bl_status launch_fp8_gemm(const Fp8Operand& A, const Fp8Operand& B, int64_t k, void* out, bool f32, int n_half,
-                          int max_clusters, cudaStream_t st) {
-  bl::Fp8GemmArgs g{};
-  g.sa = reinterpret_cast<const uint32_t*>(A.scales);
-  g.sb = reinterpret_cast<const uint32_t*>(B.scales);
-  g.M = static_cast<int>(A.rows);
-  g.N = static_cast<int>(B.rows);
-  g.n_half = n_half;
-  g.num_k_blocks = static_cast<int>((k + 127) / 128);
-  g.num_m_blocks = static_cast<int>((A.rows + 255) / 256);
-  g.num_n_blocks = static_cast<int>((B.rows + kHalves * n_half - 1) / (kHalves * n_half));
-  g.a_e5m2 = A.e5m2;
-  g.b_e5m2 = B.e5m2;
-  g.out_f32 = f32 ? 1 : 0;
-  bl::GemmArgs order{};
-  set_raster(order, double(A.rows) * double(k), double(B.rows) * double(k));
-  g.m_fastest = order.m_fastest;
-  const int64_t tiles = int64_t(g.num_m_blocks) * g.num_n_blocks;
+bl_status launch_fp8_gemm(const Fp8Job* jobs, int count, const Fp8Tiles& t, int max_clusters, cudaStream_t st) {
+  bl::Fp8Group G{};
+  G.count = count;
+  int64_t tiles = 0;
+  for (int j = 0; j < count; ++j) {
+    const Fp8Operand &A = jobs[j].A, &B = jobs[j].B;
+    const int64_t k = jobs[j].k;
+    const int n_half = t.n_half[j];
+    const bool f32 = jobs[j].f32;
+    bl::Fp8Problem& P = G.p[j];
+    P.sa = reinterpret_cast<const uint32_t*>(A.scales);
+    P.sb = reinterpret_cast<const uint32_t*>(B.scales);
+    P.M = static_cast<int>(A.rows);
+    P.N = static_cast<int>(B.rows);
+    P.n_half = n_half;
+    P.num_k_blocks = static_cast<int>((k + 127) / 128);
+    P.num_m_blocks = static_cast<int>((A.rows + 255) / 256);
+    P.num_n_blocks = static_cast<int>((B.rows + kHalves * n_half - 1) / (kHalves * n_half));
+    P.a_e5m2 = A.e5m2;
+    P.b_e5m2 = B.e5m2;
+    P.out_f32 = f32 ? 1 : 0;
+    bl::GemmArgs order{};
+    set_raster(order, double(A.rows) * double(k), double(B.rows) * double(k));
+    P.m_fastest = order.m_fastest;
+    if (bl_status s = make_map(&P.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A.q, k, A.rows, 128, 128)) return s;
+    if (bl_status s = make_map(&P.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B.q, k, B.rows, 128, n_half / 2)) return s;
+    if (bl_status s = make_map_strided(&P.tmOut, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                       f32 ? 4 : 2, jobs[j].out, B.rows, A.rows, B.rows, 32, 32,
+                                       f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+      return s;
+    tiles += t.tiles[j];
+  }
   if (tiles > INT32_MAX) return fail(BL_ERR_UNSUPPORTED_SHAPE, "too much work in one call");
-  CUtensorMap ta, tb, to;
-  if (bl_status s = make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A.q, k, A.rows, 128, 128)) return s;
-  if (bl_status s = make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B.q, k, B.rows, 128, n_half / 2)) return s;
-  if (bl_status s = make_map_strided(&to, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                                     f32 ? 4 : 2, out, B.rows, A.rows, B.rows, 32, 32,
-                                     f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
-    return s;
+  if (max_clusters > bl::kMaxCePairs) max_clusters = bl::kMaxCePairs;
+  const int clusters = static_cast<int>(tiles < max_clusters ? tiles : max_clusters);
+  bl::ce_shares(G.share, t.tiles, t.cost, count, clusters);
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  head_config(cfg, attr, 2 * (tiles < max_clusters ? tiles : max_clusters), bl::kF8Threads, bl::gemm_fp8_smem_bytes(), 2, st);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, bl::gemm_fp8_kernel<kHalves>, ta, tb, to, g);
+  head_config(cfg, attr, 2 * clusters, bl::kF8Threads, bl::gemm_fp8_smem_bytes(), 2, st);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, bl::gemm_fp8_kernel<kHalves>, G);
   if (e != cudaSuccess) return cuda_fail(e, "fp8 gemm launch");
   return BL_OK;
 }
 
-// out[m, n] = A B^T with both operands' reduction of length k (codes [rows, k], k % 16 == 0).
-bl_status enqueue_fp8_gemm(const Fp8Operand& A, const Fp8Operand& B, int64_t k, void* out, bool f32, cudaStream_t st) {
+// One product, or two that share the pairs (the deeper one first).
+bl_status enqueue_fp8_gemm(const Fp8Job* jobs, int count, cudaStream_t st) {
   static PerDeviceSetup setup[2];
   int pairs = 0, pairs2 = 0;
   if (bl_status s = pair_setup(setup[0], bl::gemm_fp8_kernel<1>, bl::kF8Threads, bl::gemm_fp8_smem_bytes(), &pairs)) return s;
   if (bl_status s = pair_setup(setup[1], bl::gemm_fp8_kernel<2>, bl::kF8Threads, bl::gemm_fp8_smem_bytes(), &pairs2)) return s;
-  const Fp8Tiles tiles = fp8_tiles(A.rows, B.rows, (k + 127) / 128, pairs);
-  return tiles.halves == 2 ? launch_fp8_gemm<2>(A, B, k, out, f32, tiles.n_half, pairs2, st)
-                           : launch_fp8_gemm<1>(A, B, k, out, f32, tiles.n_half, pairs, st);
+  const Fp8Tiles tiles = fp8_tiles(jobs, count, pairs);
+  return tiles.halves == 2 ? launch_fp8_gemm<2>(jobs, count, tiles, pairs2, st)
+                           : launch_fp8_gemm<1>(jobs, count, tiles, pairs, st);
 }
 
 size_t fp8_scale_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>((cols + 511) / 512) * 4 * rows; }
@@ -483,7 +535,8 @@ bl_status bitlinear_fp8_fwd(const void* x, int x_type, const uint8_t* x_scales, 
   if (bl_status s = enqueue_fp8_few(x, bf16 && !need, x_scales, x5, w_q, w_scales, w5, t, k_in, n_out, y_out, f32, st, &done))
     return s;
   if (done) return BL_OK;
-  return enqueue_fp8_gemm({static_cast<const uint8_t*>(x), x_scales, t, x5}, {w_q, w_scales, n_out, w5}, k_in, y_out, f32, st);
+  const Fp8Job job{{static_cast<const uint8_t*>(x), x_scales, t, x5}, {w_q, w_scales, n_out, w5}, k_in, y_out, f32};
+  return enqueue_fp8_gemm(&job, 1, st);
 }
 
 bl_status bitlinear_fp8_bwd(const uint8_t* dy_q, const uint8_t* dy_scales, const uint8_t* dy_qt, const uint8_t* dy_scales_t,
@@ -517,15 +570,21 @@ bl_status bitlinear_fp8_bwd(const uint8_t* dy_q, const uint8_t* dy_scales, const
     }
     return BL_OK;
   }
+  const bool w5 = w_format == BL_FP8_E5M2;
+  bool done = false;   // grad_x of few tokens
   if (grad_x)
-    if (bl_status s = enqueue_fp8_gemm({dy_q, dy_scales, t, d5}, {w_qt, w_scales_t, k_in, w_format == BL_FP8_E5M2}, n_out,
-                                       grad_x, false, st))
+    if (bl_status s = enqueue_fp8_few(dy_q, false, dy_scales, d5, w_qt, w_scales_t, w5, t, n_out, k_in, grad_x, false, st, &done))
       return s;
-  if (grad_w)
-    if (bl_status s = enqueue_fp8_gemm({dy_qt, dy_scales_t, n_out, d5}, {x_qt, x_scales_t, k_in, x_format == BL_FP8_E5M2},
-                                       round_up(t, 16), grad_w, grad_w_dtype == BL_OUT_F32, st))
-      return s;
-  return BL_OK;
+  const Fp8Job x_job{{dy_q, dy_scales, t, d5}, {w_qt, w_scales_t, k_in, w5}, n_out, grad_x, false};
+  const Fp8Job w_job{{dy_qt, dy_scales_t, n_out, d5}, {x_qt, x_scales_t, k_in, x_format == BL_FP8_E5M2}, round_up(t, 16), grad_w,
+                     grad_w_dtype == BL_OUT_F32};
+  Fp8Job jobs[bl::kMaxFp8Group];
+  int count = 0;
+  const bool x_first = n_out >= t;   // the deeper product's tiles go first
+  if (grad_x && !done && x_first) jobs[count++] = x_job;
+  if (grad_w) jobs[count++] = w_job;
+  if (grad_x && !done && !x_first) jobs[count++] = x_job;
+  return count ? enqueue_fp8_gemm(jobs, count, st) : BL_OK;
 }
 
 size_t bitlinear_linear_ce_fwd_workspace_size(int64_t t, int64_t v) {

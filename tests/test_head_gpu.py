@@ -222,6 +222,27 @@ def test_bwd(t, k, n, df):
     assert B.bitlinear_device_status()[0] == 0
 
 
+@pytest.mark.parametrize("t,k,n", [(48, 128, 16), (300, 4864, 896), (700, 2048, 4096), (2100, 1088, 2064), (4095, 512, 4864)])
+@pytest.mark.parametrize("dw", [torch.bfloat16, torch.float32])
+def test_bwd_together_and_apart(t, k, n, dw):
+    # both gradients from one call (one launch where both take the pair product) are those of two
+    gen = torch.Generator(device="cuda").manual_seed(t)
+    x = B.bitlinear_fp8_quant(torch.randn(t, k, generator=gen, device="cuda").to(torch.bfloat16), want_t=True)
+    dy = B.bitlinear_fp8_quant(torch.randn(t, n, generator=gen, device="cuda").to(torch.bfloat16), want_t=True,
+                               fmt=torch.float8_e5m2)
+    w = B.bitlinear_fp8_quant_weight(torch.randn(n, k, generator=gen, device="cuda"), want_t=True)
+    gx, gw = B.bitlinear_fp8_bwd(dy, x, w, grad_w_dtype=dw)
+    gx1, none = B.bitlinear_fp8_bwd(dy, x, w, want_grad_w=False)
+    assert none is None and torch.equal(gx, gx1)
+    none, gw1 = B.bitlinear_fp8_bwd(dy, x, w, want_grad_x=False, grad_w_dtype=dw)
+    assert none is None and torch.equal(gw, gw1) and gw.any()
+    rows = torch.arange(0, n, max(1, n // 16), device="cuda")   # some rows against 64 bits
+    codes = lambda d, r: d["qt"][:, :t].double() * torch.exp2(   # values of a transposed copy
+        d["scales_t"].permute(1, 0, 2).reshape(r, -1)[:, :(t + 127) // 128].double() - 127.0).repeat_interleave(128, 1)[:, :t]
+    product_close(gw[rows], f64(codes(dy, n)[rows]), f64(codes(x, k)), (t + 15) // 16 * 16)
+    assert B.bitlinear_device_status()[0] == 0
+
+
 def test_fp8_empty_batch():
     w = B.bitlinear_fp8_quant_weight(torch.randn(32, 128, device="cuda"), want_t=True)
     x = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")
