@@ -33,13 +33,16 @@
 //
 // Scales. A 32-bit word holds a row's bytes of four consecutive K blocks ([K / 512, rows, 4]
 // in memory), so one copy serves 16 MMAs per half, which select their byte by the
-// instruction descriptor's scale ids. Warp 10 gathers the words of the CTA's 128 rows of A
-// and of the tile's rows of B (both CTAs need all of them) into the order that
-// tcgen05.cp.32x128b.warpx4 takes: row r of a 128-row group at 16 (r % 32) + 4 (r / 32).
+// instruction descriptor's scale ids. Warps 10 and 11 take turns to gather the words of the
+// CTA's 128 rows of A and of the tile's rows of B (both CTAs need all of them) into the order
+// that tcgen05.cp.32x128b.warpx4 takes: row r of a 128-row group at 16 (r % 32) + 4 (r / 32).
+// One warp's round of waiting for its loads outlasts four K blocks of a narrow tile: with two
+// 777 x 8960 -> 1536 takes 18.3 us instead of 22.6 and 4096 x 11008 -> 2048 70.8 instead of
+// 74.5; shapes with enough MMAs a block lose 0 to 2%.
 // The leader's MMA thread copies them to both CTAs' TMEM in issue order with its MMAs.
 //
 // Synchronisation as in gemm_tc2.cuh, plus the scale ring:
-//   sffull[b] (leader)   : the scale warps of both CTAs arrive after filling slot b.
+//   sffull[b] (leader)   : a scale warp of each CTA arrives after filling slot b.
 //   sfempty[b] (each CTA): the leader's commit after the copies of slot b (multicast).
 // Every wait is bounded. No load uses multicast.
 #pragma once
@@ -65,7 +68,8 @@ constexpr int kF8RingBytes = 6 * (kF8ABytes + kF8BBytes);   // 180 KB
 constexpr int kF8SfRingBytes = 3 * 5 * 512;
 constexpr int kF8EpiWarps = 8;
 constexpr int kF8SfWarp = 2 + kF8EpiWarps;
-constexpr int kF8Threads = 32 * (kF8SfWarp + 1);          // 352
+constexpr int kF8SfWarps = 2;
+constexpr int kF8Threads = 32 * (kF8SfWarp + kF8SfWarps);   // 384
 constexpr int kF8StgBytes = 32 * 128;                     // per epilogue warp: 32 rows x 32 columns fp32, or two of bf16
 constexpr uint32_t kF8SfCol0 = 2 * kF8MaxN;               // TMEM: scales after the accumulators
 constexpr int kF8BarBytes = 512;
@@ -168,7 +172,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) gemm_fp8_kernel(const __grid_co
       mbar_init(empty0 + 8u * s, 1);
     }
     for (int s = 0; s < S::kSfSlots; ++s) {
-      mbar_init(sffull0 + 8u * s, 2);    // the scale warps of both CTAs
+      mbar_init(sffull0 + 8u * s, 2);    // a scale warp of each CTA
       mbar_init(sfempty0 + 8u * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -361,16 +365,15 @@ __global__ void __launch_bounds__(kF8Threads, 1) gemm_fp8_kernel(const __grid_co
         if (!mbar_wait_plain(done_bar, 0)) atomicOr(&g_device_status, DEV_ST_TIMEOUT_DRAIN);
       }
     }
-  } else if (warp == kF8SfWarp) {
-    // ------------------------------------------------------------- scale warp (both CTAs)
+  } else if (warp >= kF8SfWarp) {
+    // ------------------------------------------------------------- scale warps (both CTAs)
     const uint32_t sffull_leader0 = map_to_rank(sffull0, 0);
-    int f = 0;
+    int f = warp - kF8SfWarp;   // every kF8SfWarps-th scale slot and group of K blocks
     uint32_t fph = 0;
     bool ok = true;
     uint32_t w[4 * S::kSfGroups];
-    // The next words' place: coordinates are worked out once a tile. (Once every four K
-    // blocks they held up the products with little else to do: 2048 x 11008 x 2048 took 40.4
-    // us instead of 36.)
+    // The next words' place: coordinates are worked out once a tile. (Worked out for every
+    // four K blocks they delayed the scales: 2048 x 11008 -> 2048 took 40.4 us instead of 34.5.)
     const uint32_t *pa = nullptr, *pb = nullptr;
     int M = 0, N = 0, n_half = 0, m0 = 0, n0 = 0;
     int j = 0, r = 0, left = 0;   // product, round, and what the tile has left of four K blocks each
@@ -400,10 +403,19 @@ __global__ void __launch_bounds__(kF8Threads, 1) gemm_fp8_kernel(const __grid_co
         const int in_half = 32 * (c & 7), at = (c >> 3) * n_half + in_half;
         w[4 + c] = in_half < n_half && n0 + at < N ? ld_plain(pb + at) : 0u;
       }
-      pa += M;
-      pb += N;
+    };
+    auto next = [&](int groups) {   // that many times four K blocks further
+      for (; left && groups > 0; --groups) {
+        pa += M;
+        pb += N;
+        if (--left == 0) {
+          ++r;
+          aim();
+        }
+      }
     };
     aim();
+    next(f);
     if (left) load();
     while (left) {
       const bool got = mbar_wait(sfempty0 + 8u * f, fph ^ 1u, abort_flag);
@@ -422,13 +434,11 @@ __global__ void __launch_bounds__(kF8Threads, 1) gemm_fp8_kernel(const __grid_co
       if (lane == 0) mbar_arrive_remote(sffull_leader0 + 8u * f);
       // after the fence, which would wait for them: the next group's words travel while
       // this warp waits for a free slot
-      if (--left == 0) {
-        ++r;
-        aim();
-      }
+      next(kF8SfWarps);
       if (left) load();
-      if (++f == S::kSfSlots) {
-        f = 0;
+      f += kF8SfWarps;
+      if (f >= S::kSfSlots) {
+        f -= S::kSfSlots;
         fph ^= 1u;
       }
     }
