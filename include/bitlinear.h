@@ -426,7 +426,8 @@ bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const in
  * the total with respect to each loss[t]; either output may be NULL:
  *   dl[t, v] = (exp(l[t, v] - lse[t]) - [v == targets[t]]) * grad_loss[t]
  *   grad_x [t, k_in] bf16 = dl . w,   grad_w [v, k_in] (grad_w_dtype) = dl^T . x.
- * dl is rounded to bf16 for these products, relative to the largest finite |grad_loss|. A token
+ * dl is rounded to bf16 for these products, relative to the largest finite |grad_loss|, and
+ * carried as the sum of two bf16 numbers where 32 tokens or fewer have a loss. A token
  * without a loss contributes nothing, whatever its x, lse and grad_loss hold, and costs
  * nothing in the products.
  * The logits are computed again, one piece of the vocabulary after another; the workspace

@@ -330,16 +330,19 @@ bl_status enqueue_fp8_few(const void* x, bool x_bf16, const uint8_t* x_scales, b
 
 // ------------------------------------------------------------------ linear cross entropy
 
+// Rows of dl: up to kCeSplitTokens tokens have two, whatever t is.
+int64_t ce_dl_rows(int64_t t) { return t >= 2 * bl::kCeSplitTokens ? t : t <= bl::kCeSplitTokens ? 2 * t : 2 * bl::kCeSplitTokens; }
+
 // dl of the whole vocabulary up to kCeWholeBytes, else of a piece of kCePieceBytes at most
-// (8192 x 2048 x 65536 backward: pieces of 32 MB 5.13 ms, 64 MB 5.00, 128 MB 4.55, 256 MB 4.61; 112 MB keeps the
-// workspace below a third of the logits there).
+// (8192 x 2048 x 65536 backward: pieces of 32 MB 5.13 ms, 64 MB 5.00, 128 MB 4.55, 256 MB
+// 4.61; 112 MB keeps the workspace below a third of the logits there).
 constexpr int64_t kCeWholeBytes = int64_t(64) << 20, kCePieceBytes = int64_t(112) << 20;
 
 // Vocabulary rows per piece of the backward pass: all of them, or a multiple of 256 and a
 // quarter of the vocabulary at most, so that the two pieces held at a time stay well below
 // the logits.
 int64_t ce_piece(int64_t t, int64_t v) {
-  const int64_t all = round_up(v, 256), row = 2 * (t > 0 ? t : 1);
+  const int64_t all = round_up(v, 256), row = 2 * (t > 0 ? ce_dl_rows(t) : 1);
   if (row * all <= kCeWholeBytes) return all;
   const int64_t fit = kCePieceBytes / row / 256 * 256, quarter = round_up((v + 3) / 4, 256);
   const int64_t p = fit < quarter ? fit : quarter;
@@ -445,9 +448,9 @@ struct CeBwdSpace {
 CeBwdSpace ce_bwd_space(int64_t t, int64_t k_in, int64_t v, bool want_grad_x) {
   CeBwdSpace s{};
   const int64_t piece = ce_piece(t, v);
-  const size_t bytes = round256(static_cast<size_t>(t) * static_cast<size_t>(piece) * 2);
+  const size_t bytes = round256(static_cast<size_t>(ce_dl_rows(t)) * static_cast<size_t>(piece) * 2);
   const size_t rows = static_cast<size_t>(round_up(t, 256));
-  s.head = 0;   // the live tokens' number and the largest |grad_loss|
+  s.head = 0;   // the live rows' number, the largest |grad_loss| and the first low half
   s.place = 256;
   s.from = s.place + rows * 4;
   s.target = s.from + rows * 4;
@@ -679,6 +682,7 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
   uint8_t* space = static_cast<uint8_t*>(workspace);
   int* live = reinterpret_cast<int*>(space + sp.head);
   float* grad_max = reinterpret_cast<float*>(space + sp.head) + 1;
+  int* low = live + 2;
   int* place = reinterpret_cast<int*>(space + sp.place);
   int* from = reinterpret_cast<int*>(space + sp.from);
   int* row_target = reinterpret_cast<int*>(space + sp.target);
@@ -686,21 +690,22 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
   float* row_grad = reinterpret_cast<float*>(space + sp.grad);
   uint8_t* x_live = space + sp.x;
   float* acc = reinterpret_cast<float*>(space + sp.acc);
-  const int64_t rows = round_up(t, 256), piece = ce_piece(t, v), pieces = (v + piece - 1) / piece;
+  const int64_t rows = round_up(t, 256), dl_rows = ce_dl_rows(t), piece = ce_piece(t, v), pieces = (v + piece - 1) / piece;
   const CeRuns runs = ce_grad_x_runs(t, k_in, piece < v ? piece : v);
   const int row8 = static_cast<int>(k_in / 8);
   const int64_t cap = int64_t(device_sm_count()) * 16;   // blocks of the gather and scatter kernels
   if (bl_status s = launch_head("linear ce live launch", bl::ce_live_kernel, 1, 1024, st, grad_loss, targets, t, v, place, from, live,
-                                grad_max))
+                                low, grad_max))
     return s;
   if (bl_status s = launch_head("linear ce gather launch", bl::ce_gather_kernel, rows / 8 < cap ? rows / 8 : cap, 256, st,
                                 reinterpret_cast<const uint4*>(x), targets, lse, grad_loss, static_cast<const int*>(from),
-                                static_cast<const int*>(live), static_cast<const float*>(grad_max), row8,
+                                static_cast<const int*>(live), static_cast<const int*>(low), static_cast<const float*>(grad_max), row8,
                                 reinterpret_cast<uint4*>(x_live), row_target, row_lse2, row_grad))
     return s;
   bl::CeGroup G{};
   G.v = v;
   G.live = live;
+  G.low = low;
   G.row_target = row_target;
   G.row_lse2 = row_lse2;
   G.row_grad = row_grad;
@@ -717,40 +722,40 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
       if (grad_x) px = &G.p[G.count++];
       if (grad_w && !w_first) pw = &G.p[G.count++];
       if (px) {
-        ce_shape(*px, i == 1 ? bl::CE_PART : bl::CE_ADD_PART, t, k_in, n, false, true);
+        ce_shape(*px, i == 1 ? bl::CE_PART : bl::CE_ADD_PART, dl_rows, k_in, n, false, true);
         px->live_m = 1;
         px->split_blocks = runs.blocks;
         px->splits = (px->num_k_blocks + runs.blocks - 1) / runs.blocks;   // the last piece may have fewer
-        if (bl_status s = ce_operand(&px->tmA, dl, n, t, piece, false)) return s;
+        if (bl_status s = ce_operand(&px->tmA, dl, n, dl_rows, piece, false)) return s;
         if (bl_status s = ce_operand(&px->tmB, w + v0 * k_in, k_in, n, k_in, true)) return s;
         if (bl_status s = ce_output(&px->tmOut, acc, runs.splits * rows, k_in, k_in, true)) return s;
       }
       if (pw) {
-        ce_shape(*pw, w32 ? bl::CE_F32 : bl::CE_BF16, n, k_in, t, true, true);
+        ce_shape(*pw, w32 ? bl::CE_F32 : bl::CE_BF16, n, k_in, dl_rows, true, true);
         pw->live_k = 1;
-        if (bl_status s = ce_operand(&pw->tmA, dl, n, t, piece, true)) return s;
+        if (bl_status s = ce_operand(&pw->tmA, dl, n, dl_rows, piece, true)) return s;
         if (bl_status s = ce_operand(&pw->tmB, x_live, k_in, rows, k_in, true)) return s;
         if (bl_status s = ce_output(&pw->tmOut, static_cast<uint8_t*>(grad_w) + v0 * k_in * (w32 ? 4 : 2), n, k_in, k_in, w32))
           return s;
       }
     }
-    if (i < pieces) {   // dl of the piece [t, n], row stride `piece`
+    if (i < pieces) {   // dl of the piece [dl_rows, n], row stride `piece`
       const int64_t v0 = i * piece, n = v - v0 < piece ? v - v0 : piece;
       bl::CeProblem& P = G.p[G.count++];
-      ce_shape(P, bl::CE_DLOGITS, t, n, k_in, false, false);
+      ce_shape(P, bl::CE_DLOGITS, dl_rows, n, k_in, false, false);
       P.v0 = static_cast<int>(v0);
       P.live_m = 1;
       if (bl_status s = ce_operand(&P.tmA, x_live, k_in, rows, k_in, false)) return s;
       if (bl_status s = ce_operand(&P.tmB, w + v0 * k_in, k_in, n, k_in, false)) return s;
-      if (bl_status s = ce_output(&P.tmOut, space + sp.dl[i & 1], t, n, piece, false)) return s;
+      if (bl_status s = ce_output(&P.tmOut, space + sp.dl[i & 1], dl_rows, n, piece, false)) return s;
     }
     if (bl_status s = launch_ce(G, st)) return s;
   }
   if (grad_x) {
     const int64_t n8 = t * row8, blocks = (n8 + 255) / 256;
     if (bl_status s = launch_head("linear ce scatter launch", bl::ce_scatter_kernel, blocks < cap ? blocks : cap, 256, st,
-                                  reinterpret_cast<const float4*>(acc), static_cast<const int*>(place), n8, row8, runs.splits,
-                                  rows * k_in / 4, static_cast<const float*>(grad_max), reinterpret_cast<uint4*>(grad_x)))
+                                  reinterpret_cast<const float4*>(acc), static_cast<const int*>(place), static_cast<const int*>(low), n8,
+                                  row8, runs.splits, rows * k_in / 4, static_cast<const float*>(grad_max), reinterpret_cast<uint4*>(grad_x)))
       return s;
   }
   return BL_OK;

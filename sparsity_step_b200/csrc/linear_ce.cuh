@@ -14,7 +14,8 @@
 // are added in registers, rounded to nearest, which stays below 1e-6 at any K.
 // Backward, one piece of the vocabulary after another: the logits of the piece are computed
 // again, their epilogue writes dl of the piece in bf16 (the operand type of the tensor
-// cores: one rounding of at most half a step per factor), and two products consume it,
+// cores: one rounding of at most half a step per factor; few tokens as the sum of two, see
+// kCeSplitTokens), and two products consume it,
 // grad_W of the piece's rows and the piece's addend of grad_X, summed in fp32. Tokens without
 // a loss (padding, prompts) are left out first: the others' rows are gathered to the front,
 // the products stop after them, and grad_X is scattered back. Four products of 2 T V K
@@ -31,6 +32,7 @@
 #pragma once
 
 #include <cfloat>
+#include <climits>
 
 #include "ce_shares.cuh"
 #include "gemm_sp2.cuh"
@@ -69,8 +71,10 @@ struct CeGroup {
   int count;
   int64_t v;                     // vocabulary size
   const int64_t* targets;        // [T]  (CE_LSE)
-  // backward: the tokens with a loss in order, then zeros (target -1) up to 256 rows
-  const int* live;               // their number, at least 1
+  // backward: the tokens with a loss in order (a few of them a second time, for their low
+  // halves), then zeros (target -1) up to 256 rows
+  const int* live;               // rows of them, at least 1
+  const int* low;                // first of their low halves' rows (INT_MAX: none)
   const int* row_target;
   const float* row_lse2;         // lse in units of log2
   const float* row_grad;         // g over the largest |g|
@@ -172,6 +176,7 @@ __device__ __forceinline__ void ce_store(const CeGroup& G, const CeProblem& P, C
   if (P.mode == CE_DLOGITS) {
     const int row = row0 + lane;
     const float lse2 = G.row_lse2[row], g = G.row_grad[row];
+    const bool low = row >= *G.low;
     const int hit = G.row_target[row] - P.v0 - n0;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
@@ -189,6 +194,12 @@ __device__ __forceinline__ void ce_store(const CeGroup& G, const CeProblem& P, C
     for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int j = 0; j < 32; ++j) acc[c][j] = g == 0.f ? 0.f : acc[c][j] * g;
+    if (low) {   // what the rounding of the token's first row leaves
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) acc[c][j] -= __bfloat162float(__float2bfloat16_rn(acc[c][j]));
+    }
   } else if (P.mode <= CE_F32) {
     const float scale = *G.grad_max;
 #pragma unroll
@@ -454,12 +465,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
   }
 }
 
+// The rounding of dl to bf16 is the same for a whole row of grad_W, so that of one token
+// shows in full: one token over 500 to 131072 columns left gradients 3.6e-3 off (rounding
+// the outputs alone: 1.7e-3), while over many tokens the errors meet the outputs' rounding
+// (2.0e-3 to 2.2e-3). So where there are few tokens dl is carried as the sum of two bf16
+// numbers. Up to 32 tokens their 64 rows are one K block of grad_W and part of one tile of
+// the other products: 32 x 1536 x 32003 takes 99 us, 33 tokens 91 (up to 128 tokens it cost
+// 10 to 20%).
+constexpr int kCeSplitTokens = 32;
+
 // The tokens with a loss, in order: place[t] among them (-1 for the others), from[i] the
 // i-th one, their number (1 if there is none: its row is zeros then) and the largest finite
 // |g| of them (1 if there is none above 0): an infinity or a NaN stays with its own token
-// and does not divide the others. One block: 1024 tokens a step.
+// and does not divide the others. Up to kCeSplitTokens of them get a second row each, from
+// row `low` on (live counts both). One block: 1024 tokens a step.
 __global__ void __launch_bounds__(1024) ce_live_kernel(const float* grad, const int64_t* targets, int64_t t, int64_t v,
-                                                       int* place, int* from, int* live, float* grad_max) {
+                                                       int* place, int* from, int* live, int* low, float* grad_max) {
   __shared__ uint32_t s_max[32];
   __shared__ int s_count[33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -504,7 +525,9 @@ __global__ void __launch_bounds__(1024) ce_live_kernel(const float* grad, const 
     m = __reduce_max_sync(0xFFFFFFFFu, s_max[lane]);
     if (lane == 0) {
       *grad_max = m ? __uint_as_float(m) : 1.f;
-      *live = before > 0 ? before : 1;
+      const bool split = before > 0 && before <= kCeSplitTokens;
+      *live = before == 0 ? 1 : split ? 2 * before : before;
+      *low = split ? before : INT_MAX;
       if (before == 0) from[0] = -1;
     }
   }
@@ -513,12 +536,13 @@ __global__ void __launch_bounds__(1024) ce_live_kernel(const float* grad, const 
 // Their rows of X and what dl needs of them, then zeros up to a multiple of 256 rows. A warp
 // per row.
 __global__ void __launch_bounds__(256) ce_gather_kernel(const uint4* x, const int64_t* targets, const float* lse, const float* grad,
-                                                        const int* from, const int* live, const float* grad_max, int row8,
+                                                        const int* from, const int* live, const int* low_row,
+                                                        const float* grad_max, int row8,
                                                         uint4* x_live, int* row_target, float* row_lse2, float* row_grad) {
   follow_stream();
-  const int n = *live, end = (n + 255) / 256 * 256, lane = threadIdx.x & 31;
+  const int n = *live, low = *low_row, end = (n + 255) / 256 * 256, lane = threadIdx.x & 31;
   for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < end; r += gridDim.x * 8) {
-    const int t = r < n ? from[r] : -1;
+    const int t = r < n ? from[r < low ? r : r - low] : -1;
     uint4* dst = x_live + static_cast<int64_t>(r) * row8;
     const uint4* src = x + static_cast<int64_t>(t < 0 ? 0 : t) * row8;
     for (int i = lane; i < row8; i += 32) dst[i] = t < 0 ? make_uint4(0, 0, 0, 0) : ld_plain(src + i);
@@ -569,13 +593,18 @@ __global__ void __launch_bounds__(kCeJoinThreads) ce_join_kernel(const float2* s
   }
 }
 
-// grad_X: the token's row of the `splits` partial sums (`stride` float4 apart), added in order,
-// times the largest |g|, in bf16; zeros for a token without a loss. 8 elements per thread and
-// step.
-__global__ void __launch_bounds__(256) ce_scatter_kernel(const float4* src, const int* place, int64_t n8, int row8, int splits,
-                                                         int64_t stride, const float* scale, uint4* dst) {
+// grad_X: the token's row of the `splits` partial sums (`stride` float4 apart), and its second
+// row from `low_row` on, added in order, times the largest |g|, in bf16; zeros for a token
+// without a loss. 8 elements per thread and step. With few tokens the runs are many and the
+// threads few: one load after the other took 8 us more (33 x 1536 x 32003).
+__global__ void __launch_bounds__(256) ce_scatter_kernel(const float4* src, const int* place, const int* low_row, int64_t n8,
+                                                         int row8, int splits, int64_t stride, const float* scale, uint4* dst) {
   follow_stream();
   const float f = *scale;
+  const int low = *low_row;
+  const bool two = low != INT_MAX;   // whether a token has two rows
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int64_t half = two ? 2 * static_cast<int64_t>(low) * row8 : 0;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t t = i / row8;
     const int p = ld_plain(place + t);
@@ -584,11 +613,27 @@ __global__ void __launch_bounds__(256) ce_scatter_kernel(const float4* src, cons
       continue;
     }
     const float4* at = src + 2 * (static_cast<int64_t>(p) * row8 + (i - t * row8));
-    float4 a = ld_plain(at), b = ld_plain(at + 1);
-    for (int s = 1; s < splits; ++s) {
-      const float4 c = ld_plain(at + s * stride), e = ld_plain(at + s * stride + 1);
+    float4 a = zero, b = zero;
+    auto add = [&](const float4& c, const float4& e) {
       a = make_float4(a.x + c.x, a.y + c.y, a.z + c.z, a.w + c.w);
       b = make_float4(b.x + e.x, b.y + e.y, b.z + e.z, b.w + e.w);
+    };
+    for (int s0 = 0; s0 < splits; s0 += 4) {   // four addends at a time, so that their loads overlap
+      float4 c[4][2], d[4][2];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float4* from = at + (s0 + u < splits ? s0 + u : s0) * stride;
+        c[u][0] = ld_plain(from);
+        c[u][1] = ld_plain(from + 1);
+        d[u][0] = two ? ld_plain(from + half) : zero;
+        d[u][1] = two ? ld_plain(from + half + 1) : zero;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (s0 + u < splits) {
+          add(c[u][0], c[u][1]);
+          add(d[u][0], d[u][1]);
+        }
     }
     dst[i] = make_uint4(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f), pack_bf16x2(b.x * f, b.y * f),
                         pack_bf16x2(b.z * f, b.w * f));

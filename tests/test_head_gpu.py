@@ -425,6 +425,29 @@ def test_linear_ce_not_finite_grad_loss(t, bad):
     assert not torch.isfinite(gx[t // 2]).any() and not torch.isfinite(gw[5]).any()
 
 
+@pytest.mark.parametrize("t,k,v,live", [(1, 64, 500, 1), (1, 1088, 5003, 1), (2, 128, 700, 2), (5, 2048, 1003, 4), (32, 64, 40001, 32),
+                                        (33, 320, 2500, 32), (64, 192, 600, 17), (200, 64, 513, 7), (300, 256, 1031, 32)])
+def test_linear_ce_few_tokens_keep_dl(t, k, v, live):
+    # up to 32 tokens with a loss: dl as two bf16 numbers, so that it is off by a half step
+    # (2^-8) of what a half step leaves (2^-8 of dl), where one number would be off by 2^-8
+    x, w, _, _ = ce_inputs(t, k, v, 14)
+    rng = np.random.default_rng(t + v)
+    y = np.full(t, -1)
+    y[rng.permutation(t)[:live]] = rng.integers(0, v, live)
+    g = np.where(rng.random(t) < 0.5, 1.0 / t, rng.normal(size=t)).astype(np.float32)
+    o, d = H.linear_ce(x, w, y, g), logit_errors(x, w, k)
+    xd, wd, yd = dev(x, torch.bfloat16), dev(w, torch.bfloat16), dev(y)
+    _, lse = B.bitlinear_linear_ce_fwd(xd, wd, yd)
+    gx, gw = B.bitlinear_linear_ce_bwd(xd, wd, yd, lse, dev(g), grad_w_dtype=torch.float32)
+    spread = 2 * d + 2.0 ** -20 + 8 * U * np.abs(o["logits"]).max(axis=1) + 4 * U * np.abs(o["lse"])   # as in check_ce_grads
+    ddl = (BF16 ** 2 + 4 * U) * np.abs(o["dl"]) + (1 + BF16) * o["p"] * np.expm1(spread)[:, None]
+    for got, want, err, s, depth in ((gx, o["grad_x"], ddl @ np.abs(w), np.abs(o["dl"]) @ np.abs(w), v),
+                                     (gw, o["grad_w"], ddl.T @ np.abs(x), np.abs(o["dl"]).T @ np.abs(x), t)):
+        tol = err + acc_bound(2 * depth + 256, 16, s) + (BF16 if got.dtype == torch.bfloat16 else U) * (np.abs(want) + err) + 1e-37
+        worst = np.max(np.abs(f64(got) - want) / tol)
+        assert worst <= 1.0, f"worst error {worst:.3f} of its bound"
+
+
 def test_linear_ce_empty_batch():
     w = torch.randn(50, 64, device="cuda").to(torch.bfloat16)
     x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
