@@ -37,11 +37,12 @@ constexpr int kFewThreads = 192;      // producer, MMA, four epilogue warps
 constexpr int kFewMaxStages = 8;
 constexpr int kFewStageBytes = 128 * 128;
 constexpr int kFewSfBytes = 512;
-// K blocks (64 of K) per accumulation of logits: with 8, as in linear_ce.cuh, a single token's
-// loss was 1.3e-6 off, with 4 half of that.
+// K blocks (64 of K) per accumulation of logits, at most: as few as fit in TMEM beside each
+// other are taken. One token's loss has nobody to average with: with 8, as in linear_ce.cuh,
+// it was 1.3e-6 off, with 4 half of that, with 2 a quarter.
 constexpr int kFewPartBlocks = 4;
-__host__ __device__ constexpr int few_parts(bool fp8, int blocks) {
-  return fp8 ? 1 : (blocks + kFewPartBlocks - 1) / kFewPartBlocks;
+__host__ __device__ constexpr int few_parts(bool fp8, int blocks, int part_blocks) {
+  return fp8 ? 1 : (blocks + part_blocks - 1) / part_blocks;
 }
 constexpr int kFewBarBytes = 256;
 
@@ -59,6 +60,7 @@ struct FewArgs {
   int num_k_blocks, num_row_blocks;
   int split;                  // CTAs of the cluster that share a row block
   int stages;
+  int part_blocks;            // K blocks per accumulation of logits
   int parts, bufs;            // accumulations per row block and row blocks in TMEM at a time
   uint32_t sf_col0, tmem_cols;
   void* y;                    // kFp8
@@ -281,8 +283,8 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
         tc_fence_after_sync();
         if (elect_one() && live) {
           const int b = kb - kb0;
-          const int part = kFp8 ? 0 : b / kFewPartBlocks;
-          const uint32_t add = (kFp8 ? b == 0 : b % kFewPartBlocks == 0) ? 0u : 1u;   // first MMA of an accumulation
+          const int part = kFp8 ? 0 : b / a.part_blocks;
+          const uint32_t add = (kFp8 ? b == 0 : b % a.part_blocks == 0) ? 0u : 1u;   // first MMA of an accumulation
           const uint32_t d = tmem_base + (buf * a.parts + part) * kTok;
           const uint64_t ad = make_sw128_desc(sRing + static_cast<uint32_t>(s * kFewStageBytes), 16, 1024);
           const uint64_t bd = make_sw128_desc(sB + static_cast<uint32_t>((kept ? b : s) * kTok * 128), 16, 1024);
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
       const uint32_t t_row = tmem_base + buf * a.parts * kTok + (static_cast<uint32_t>(quad * 32) << 16);
       const int local = kFp8 ? 4 * lane + quad : quad * 32 + lane;   // the weight row of this thread
       const int row = blk * 128 + local;
-      const int parts = few_parts(kFp8, kb1 - kb0);
+      const int parts = few_parts(kFp8, kb1 - kb0, a.part_blocks);
       constexpr int kCols = kTok < 32 ? kTok : 32;
 #pragma unroll 1
       for (int c0 = 0; c0 < kTok; c0 += kCols) {   // tokens, 16 or 32 at a time
@@ -366,7 +368,10 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
 #pragma unroll
           for (int i = 0; i < kCols; ++i)
             if (i < a.t) {
-              if (row < a.n && a.targets[i] == row) a.target_logit[i] = v[i];
+              if (row < a.n && a.targets[i] == row) {
+                a.target_logit[i] = v[i];
+                v[i] = -INFINITY;
+              }
               const float l2 = row < a.n ? v[i] * kLog2e : -INFINITY;
               float m = l2;
 #pragma unroll
@@ -425,7 +430,10 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
           l[h] = -INFINITY;
           if (32 * h + lane < per && row < a.n) {
             l[h] = total(i, local);
-            if (a.targets[i] == row) a.target_logit[i] = l[h];
+            if (a.targets[i] == row) {
+              a.target_logit[i] = l[h];
+              l[h] = -INFINITY;
+            }
           }
           m = fmaxf(m, l[h] * kLog2e);
         }

@@ -216,7 +216,7 @@ constexpr size_t kFewSmemTwo = 113 * 1024;   // two CTAs on an SM
 constexpr size_t kFewSmemOne = 226 * 1024;
 
 struct FewPlan {
-  int split, stages, tok;
+  int split, stages, tok, part_blocks;
   size_t smem;
 };
 // How a product of few tokens is spread: K is split over a cluster while row blocks x split
@@ -235,12 +235,14 @@ bool few_plan(bool fp8, bool kept, int64_t t, int64_t num_k_blocks, int64_t row_
   while (split < 8 && blocks_mn * split * 2 <= 2 * int64_t(sms) && num_k_blocks >= 4 * split) split *= 2;
   for (; split <= 8; split *= 2) {
     const int blocks = bl::few_blocks_max(static_cast<int>(num_k_blocks), split);
-    if (bl::few_parts(fp8, blocks) * tok > 256) continue;   // TMEM
+    int part = 1;
+    while (part < bl::kFewPartBlocks && bl::few_parts(fp8, blocks, part) * tok > 256) part *= 2;
+    if (bl::few_parts(fp8, blocks, part) * tok > 256) continue;   // TMEM
     for (const size_t room : {kFewSmemTwo, kFewSmemOne}) {
       int stages = bl::kFewMaxStages;
       while (stages >= 3 && bl::few_smem_bytes(fp8, kept, tok, stages, blocks) > room) --stages;
       if (stages < 3) continue;
-      *p = {split, stages, tok, bl::few_smem_bytes(fp8, kept, tok, stages, blocks)};
+      *p = {split, stages, tok, part, bl::few_smem_bytes(fp8, kept, tok, stages, blocks)};
       return true;
     }
   }
@@ -262,7 +264,8 @@ bl_status launch_few(const bl::FewMaps& M, bl::FewArgs& a, const FewPlan& p, cud
   a.split = p.split;
   a.stages = p.stages;
   const int blocks = bl::few_blocks_max(a.num_k_blocks, p.split);
-  a.parts = bl::few_parts(kFp8, blocks);
+  a.part_blocks = p.part_blocks;
+  a.parts = bl::few_parts(kFp8, blocks, p.part_blocks);
   const int cols = a.parts * kTok;
   a.bufs = 2 * cols + (kFp8 ? 64 : 0) <= 256 ? 2 : 1;
   a.sf_col0 = static_cast<uint32_t>(a.bufs * cols);

@@ -6,7 +6,7 @@
 //   grad_X = dl W,  grad_W = dl^T X
 //
 // Forward: one pass of a CTA-pair product whose epilogue reduces each 128-column strip of
-// logits in registers to its maximum and its sum of exponentials (fp32, the logits never
+// logits but the target's in registers to its maximum and its sum of exponentials (fp32, the logits never
 // rounded), so a token leaves 8 bytes per 128 columns of the vocabulary instead of 512; a
 // small kernel joins the strips in a fixed order. The tensor core's accumulator drops the
 // bits of an addend below its own last one, always towards zero: over K = 2048 the logits
@@ -143,7 +143,10 @@ __device__ __forceinline__ void ce_strip(const CeGroup& G, const CeProblem& P, C
     for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (32 * c + j == static_cast<int>(hit)) t = acc[c][j];
+        if (32 * c + j == static_cast<int>(hit)) {
+          t = acc[c][j];
+          acc[c][j] = -INFINITY;
+        }
     G.target_logit[row] = t;
   }
   if (left < 128) {
@@ -555,8 +558,10 @@ __global__ void __launch_bounds__(256) ce_gather_kernel(const uint4* x, const in
   }
 }
 
-// Joins the strips of each token: 32 tokens x 32 slices of the strips per block, the
-// slices' (max, sum) pairs joined in order.
+// Joins the strips of each token, which leave the target's logit out: with the others' sum
+// relative to it the loss, log(1 + sum exp(l_v - l_y)), is exact to the logits' error even
+// where it is nearly 0 (as lse - l_y a loss of 0.26 at a logit of 12 was 2.4e-6 off). 32
+// tokens x 32 slices of the strips per block, the slices' (max, sum) pairs joined in order.
 constexpr int kCeJoinThreads = 1024;
 __global__ void __launch_bounds__(kCeJoinThreads) ce_join_kernel(const float2* strips, int num_strips, int64_t t, int64_t v,
                                                                  const int64_t* targets, const float* target_logit,
@@ -586,10 +591,23 @@ __global__ void __launch_bounds__(kCeJoinThreads) ce_join_kernel(const float2* s
 #pragma unroll
     for (int i = 0; i < 32; ++i)
       if (s_part[i][lane].y != 0.f) ss += s_part[i][lane].y * ex2(s_part[i][lane].x - mm);
-    const float l = mm * 0.6931471805599453f + logf(ss);
+    // mm (base 2, the others' largest logit) back in logits in two parts; the factor is 1 /
+    // kLog2e as rounded
+    constexpr float kHigh = static_cast<float>(1.0 / static_cast<double>(kLog2e));
+    constexpr float kLow = static_cast<float>(1.0 / static_cast<double>(kLog2e) - static_cast<double>(kHigh));
     const int64_t y = targets[row];
-    lse[row] = l;
-    loss[row] = y >= 0 && y < v ? l - target_logit[row] : 0.f;
+    const bool counts = y >= 0 && y < v;
+    const float tl = counts ? target_logit[row] : -INFINITY;
+    const float d = fmaf(mm, kHigh, -tl) + mm * kLow;   // by how much it is above the target's
+    if (d > 0.f) {
+      const float sum = logf(ss + expf(-d));
+      lse[row] = fmaf(mm, kHigh, fmaf(mm, kLow, sum));
+      loss[row] = counts ? d + sum : 0.f;
+    } else {
+      const float l = log1pf(ss * expf(d));
+      lse[row] = tl + l;
+      loss[row] = counts ? l : 0.f;
+    }
   }
 }
 
