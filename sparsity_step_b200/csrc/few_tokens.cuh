@@ -1,9 +1,9 @@
-// Products of few tokens (blocks of up to 128, the logits up to 32) with a large weight matrix, on the
-// tensor cores with the weights as the M operand:
+// Products of few tokens (blocks of up to 128, the logits up to 32) with a large weight matrix,
+// on the tensor cores with the weights as the M operand:
 //
 //   kFp8:  y[t, n]  = sum_k xq[t, k] 2^ex * wq[n, k] 2^ew   (kind::mxf8f6f4, block-scaled)
 //   else:  l[t, v]  = sum_k X[t, k] W[v, k]                  (kind::f16), reduced to strips of
-//          (maximum, sum of exponentials) and the target's logit for the cross entropy
+//          (maximum, sum of exponentials) without the target for the cross entropy
 //
 // Bound by HBM: every weight is read once and used for a few multiplications. A CTA takes
 // 128 weight rows; its producer streams them through a ring of 16 KB K blocks (128 rows x
@@ -39,7 +39,8 @@ constexpr int kFewStageBytes = 128 * 128;
 constexpr int kFewSfBytes = 512;
 // K blocks (64 of K) per accumulation of logits, at most: as few as fit in TMEM beside each
 // other are taken. One token's loss has nobody to average with: with 8, as in linear_ce.cuh,
-// it was 1.3e-6 off, with 4 half of that, with 2 a quarter.
+// it was 1.3e-6 off, with 4 half of that, with 2 a quarter (medians of 40 draws). Where 4 do
+// not fit, more CTAs share K.
 constexpr int kFewPartBlocks = 4;
 __host__ __device__ constexpr int few_parts(bool fp8, int blocks, int part_blocks) {
   return fp8 ? 1 : (blocks + part_blocks - 1) / part_blocks;
@@ -51,7 +52,7 @@ struct FewMaps {
   CUtensorMap x;      // bf16 or codes (not x_bf16)
 };
 struct FewArgs {
-  const void* x;              // [t, k] bf16 (x_bf16)
+  const void* x;              // [t, k] bf16 (x_bf16, cross entropy)
   const uint32_t* xs;         // scale words of codes, [ceil(k / 512), t]
   int x_bf16;                 // kFp8: quantise x here (e4m3)
   const uint32_t* ws;         // kFp8: [ceil(k / 512), n]
@@ -65,7 +66,8 @@ struct FewArgs {
   uint32_t sf_col0, tmem_cols;
   void* y;                    // kFp8
   int y_f32;
-  const int64_t* targets;     // cross entropy
+  const void* rows;           // cross entropy: [n, k] bf16
+  const int64_t* targets;
   float2* strips;             // [num_row_blocks * (split > 1 ? split : 4), t]
   float* target_logit;
 };
@@ -174,6 +176,37 @@ __device__ __forceinline__ void few_fp8_operand(const FewArgs& a, uint32_t sB, u
         if (j == 0) st_shared_u8(sSfb + static_cast<uint32_t>((kb / 4 - kb0 / 4) * kFewSfBytes + tok * 16 + (kb & 3)), byte);
       }
     }
+  }
+}
+
+// Logits of the targets as fp32 dot products, a warp per token: the loss depends on them with
+// nothing to average over, and the tensor core's lost bits left one token's (2048 x 32768, 40
+// draws) up to 1.4e-6 off; now 2.1e-7. The epilogue warps do it while the weights stream by.
+__device__ __forceinline__ void few_target_logits(const FewArgs& a, int quad) {
+  auto low = [](uint32_t p) { return __uint_as_float(p << 16); };
+  auto high = [](uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); };
+  const int row8 = a.k / 8;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + quad; i < a.t; i += static_cast<int64_t>(gridDim.x) * 4) {
+    const int64_t y = a.targets[i];
+    if (y < 0 || y >= a.n) continue;
+    const uint4* x = static_cast<const uint4*>(a.x) + i * row8;
+    const uint4* w = static_cast<const uint4*>(a.rows) + y * row8;
+    float dot = 0.f;
+#pragma unroll 4
+    for (int j = lane_id(); j < row8; j += 32) {
+      const uint4 p = ld_plain(x + j), q = ld_plain(w + j);
+      float part = low(p.x) * low(q.x);
+      part = fmaf(high(p.x), high(q.x), part);
+      part = fmaf(low(p.y), low(q.y), part);
+      part = fmaf(high(p.y), high(q.y), part);
+      part = fmaf(low(p.z), low(q.z), part);
+      part = fmaf(high(p.z), high(q.z), part);
+      part = fmaf(low(p.w), low(q.w), part);
+      dot += fmaf(high(p.w), high(q.w), part);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+    if (lane_id() == 0) a.target_logit[i] = dot;
   }
 }
 
@@ -318,6 +351,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
   } else {
     // ------------------------------------------------------------- epilogue (4 warps)
     const int quad = warp & 3;
+    if constexpr (!kFp8) few_target_logits(a, quad);
     bool ok = true;
     uint32_t unit = 0;
     for (int blk = blk0; blk < a.num_row_blocks && ok; blk += blk_step, ++unit) {
@@ -368,10 +402,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
 #pragma unroll
           for (int i = 0; i < kCols; ++i)
             if (i < a.t) {
-              if (row < a.n && a.targets[i] == row) {
-                a.target_logit[i] = v[i];
-                v[i] = -INFINITY;
-              }
+              if (row < a.n && a.targets[i] == row) v[i] = -INFINITY;
               const float l2 = row < a.n ? v[i] * kLog2e : -INFINITY;
               float m = l2;
 #pragma unroll
@@ -430,10 +461,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
           l[h] = -INFINITY;
           if (32 * h + lane < per && row < a.n) {
             l[h] = total(i, local);
-            if (a.targets[i] == row) {
-              a.target_logit[i] = l[h];
-              l[h] = -INFINITY;
-            }
+            if (a.targets[i] == row) l[h] = -INFINITY;
           }
           m = fmaxf(m, l[h] * kLog2e);
         }

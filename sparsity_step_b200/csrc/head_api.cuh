@@ -627,6 +627,8 @@ bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const in
     a.n = static_cast<int>(v);
     a.num_k_blocks = static_cast<int>(k_in / 64);
     a.num_row_blocks = static_cast<int>((v + 127) / 128);
+    a.x = x;
+    a.rows = w;
     a.targets = targets;
     a.strips = strips;
     a.target_logit = target_logit;

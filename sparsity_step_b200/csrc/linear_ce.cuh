@@ -41,7 +41,7 @@
 namespace bl {
 
 enum CeMode : int {
-  CE_LSE = 0,       // strip maxima and sums of exponentials, and the target's logit
+  CE_LSE = 0,       // the target's logit, strip maxima and sums of exponentials of the others
   CE_DLOGITS = 1,   // dl in bf16
   CE_BF16 = 2,      // the product times the largest |g|, bf16
   CE_F32 = 3,       // the product times the largest |g|, fp32
@@ -143,10 +143,11 @@ __device__ __forceinline__ void ce_strip(const CeGroup& G, const CeProblem& P, C
     for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (32 * c + j == static_cast<int>(hit)) {
-          t = acc[c][j];
-          acc[c][j] = -INFINITY;
-        }
+      {   // two selects: a branch around them spills registers
+        const bool is = 32 * c + j == static_cast<int>(hit);
+        t = is ? acc[c][j] : t;
+        acc[c][j] = is ? -INFINITY : acc[c][j];
+      }
     G.target_logit[row] = t;
   }
   if (left < 128) {
