@@ -413,8 +413,11 @@ bl_status bitlinear_fp8_bwd(const uint8_t* dy_q, const uint8_t* dy_scales, const
  *
  *   x [t, k_in] bf16, w [v, k_in] bf16, any v >= 1; targets [t] int64.
  *   loss_out, lse_out [t] fp32 (lse_out also for tokens without a loss).
- * Logits are accumulated in fp32 and never rounded; those of -infinity count nothing, and
- * +infinity or NaN in a token's logits reaches that token's lse alone.
+ * Logits are accumulated in fp32 and never rounded. Those of -infinity count nothing (lse is
+ * -infinity where no other is left); +infinity or NaN in a token's logits reaches the lse and
+ * loss of that token alone. The loss is lse - l[target] there too: NaN where the target's
+ * logit is +infinity, or -infinity beside no larger one. A logit of magnitude 2.36e38 (2^128
+ * ln 2) or more counts as infinite.
  */
 size_t bitlinear_linear_ce_fwd_workspace_size(int64_t t, int64_t v);
 bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const int64_t* targets, int64_t t, int64_t k_in,

@@ -598,7 +598,16 @@ __global__ void __launch_bounds__(kCeJoinThreads) ce_join_kernel(const float2* s
     constexpr float kLow = static_cast<float>(1.0 / static_cast<double>(kLog2e) - static_cast<double>(kHigh));
     const int64_t y = targets[row];
     const bool counts = y >= 0 && y < v;
-    const float tl = counts ? target_logit[row] : -INFINITY;
+    float tl = counts ? target_logit[row] : -INFINITY;
+    const float t2 = tl * kLog2e;   // infinite from a logit of 2.36e38 on, as in the strips
+    if (isinf(t2)) tl = t2;
+    if (tl == INFINITY || (tl == -INFINITY && mm == -INFINITY)) {
+      // the target's logit beyond all numbers, or no logit above -infinity: log of the sum is
+      // that infinity (a NaN among the others stays one), the loss infinity minus itself
+      lse[row] = ss != ss ? ss : tl;
+      loss[row] = counts ? NAN : 0.f;
+      return;
+    }
     const float d = fmaf(mm, kHigh, -tl) + mm * kLow;   // by how much it is above the target's
     if (d > 0.f) {
       const float sum = logf(ss + expf(-d));

@@ -17,6 +17,7 @@ pytestmark = pytest.mark.gpu
 FMT = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
 BF16 = 2.0 ** -8
 U = 2.0 ** -23
+INF = float("inf")
 
 
 def dev(a, dtype=None):
@@ -405,6 +406,46 @@ def test_linear_ce_infinite_logits(t, v):
     keep = np.arange(t) != 1
     check_loss(loss[dev(keep)], lse[dev(keep)], {n: a[keep] for n, a in o.items()}, d[keep])
     assert t == 1 or (loss[1] == float("inf") and lse[1] == float("inf"))
+
+
+@pytest.mark.parametrize("t,v", [(1, 40), (5, 700), (20, 20001), (32, 50001), (33, 700), (300, 513)])
+def test_linear_ce_infinite_target_logit(t, v):
+    # row 5 of the head gives +infinity, for the second token -infinity: lse - l_y is infinity
+    # minus infinity where it is the target, whatever the others are
+    k = 128
+    x, w, _, _ = ce_inputs(t, k, v, 15)
+    x[:, 0] = 1.0
+    y = np.full(t, 5)
+    y[2:] = np.resize([5, 7, -100, 5, v], max(0, t - 2))
+    if t > 1:
+        x[1, 0] = -1.0
+    xd, wd, yd = dev(x, torch.bfloat16), dev(w, torch.bfloat16), dev(y)
+    wd[5], wd[5, 0] = 0.0, INF
+    loss, lse = (f64(a) for a in B.bitlinear_linear_ce_fwd(xd, wd, yd))
+    first = np.arange(t) != 1
+    assert np.all(lse[first] == INF)
+    assert np.all(np.isnan(loss[first & (y == 5)])) and np.all(loss[first & (y == 7)] == INF)
+    assert np.all(loss[(y < 0) | (y >= v)] == 0.0)
+    if t > 1:   # l_y is -infinity: the others' lse, and an infinite loss
+        o = H.linear_ce(x[1:2], np.delete(w, 5, 0), np.array([-1]))
+        assert loss[1] == INF and abs(lse[1] - o["lse"][0]) <= logit_errors(x, w, k)[1] + 2.0 ** -20 + 4 * U * abs(o["lse"][0])
+    wd[9 % v, 0] = INF   # another one beside it
+    loss, lse = (f64(a) for a in B.bitlinear_linear_ce_fwd(xd, wd, yd))
+    assert np.all(lse[first] == INF) and np.all(np.isnan(loss[first & (y == 5)]))
+
+
+@pytest.mark.parametrize("low", [-INF, -3.3895313892515355e38])
+@pytest.mark.parametrize("t,v", [(1, 1), (4, 1), (4, 700), (20, 20001), (40, 1), (200, 700)])
+def test_linear_ce_no_finite_logit(t, v, low):
+    # every logit -infinity, or the type's lowest value (2.36e38 and beyond count as infinite):
+    # the logarithm of an empty sum is -infinity, and the loss of a target there is no number
+    x, w, _, _ = ce_inputs(t, 64, v, 16)
+    x[:, 0] = 1.0
+    y = np.where(np.arange(t) % 2 == 0, v // 2, -100)
+    xd, wd, yd = dev(x, torch.bfloat16), dev(w, torch.bfloat16), dev(y)
+    wd[:], wd[:, 0] = 0.0, low
+    loss, lse = (f64(a) for a in B.bitlinear_linear_ce_fwd(xd, wd, yd))
+    assert np.all(lse == -INF) and np.all(np.isnan(loss[::2])) and np.all(loss[1::2] == 0.0)
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
