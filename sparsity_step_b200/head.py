@@ -1,6 +1,10 @@
 """Python binding of the head's operators (include/bitlinear.h): the block-scaled 8-bit
 float linear and the linear cross entropy. Argument checks and marshalling only, as in
-``bitlinear.py``."""
+``bitlinear.py``.
+
+A call with ``stream`` runs on that stream and orders it with no other: the caller lets it
+wait for the inputs, keeps them until it is through, and lets the current stream wait for the
+results. What the call allocates itself may be dropped at any time."""
 from __future__ import annotations
 
 import functools
@@ -54,6 +58,24 @@ def _size(fn: str, *args) -> int:
     return int(getattr(lib(), fn)(*args))
 
 
+def _empty(x: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """Memory on ``x``'s device for a call on ``stream``, out of that stream's pool. The current
+    stream's pool may hold memory that earlier calls there have yet to write, and hands this
+    call's on as soon as it is dropped: a given stream waits for neither."""
+    if stream is None or x.device.type != "cuda":
+        return x.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return x.new_empty(shape, dtype=dtype)
+
+
+def _result(x: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """``_empty``, for what the caller goes on using on the current stream."""
+    out = _empty(x, shape, dtype, stream)
+    if stream is not None:
+        out.record_stream(torch.cuda.current_stream(x.device))
+    return out
+
+
 def _workspace(given, need: int, x: torch.Tensor, stream):
     """The caller's workspace, or one of this call. The latter goes back to the allocator as
     soon as the call returns: work on a stream other than the current one has to be over
@@ -63,7 +85,7 @@ def _workspace(given, need: int, x: torch.Tensor, stream):
         return given
     if not need:
         return None
-    own = x.new_empty((need,), dtype=torch.uint8)
+    own = _empty(x, (need,), torch.uint8, stream)
     if stream is not None:
         own.record_stream(stream)
     return own
@@ -91,7 +113,7 @@ def _quant(fn, name: str, src, dtype, want_t: bool, fmt, out: dict | None, strea
         if key in o:
             _check(o[key], dt, shape, key, dev)
         else:
-            o[key] = src.new_empty(shape, dtype=dt)
+            o[key] = _result(src, shape, dt, stream)
     st = _launch(getattr(lib(), fn), dev, stream, _ptr(src), rows, cols, code, _ptr(o["q"]), _ptr(o["scales"]),
                _ptr(o["qt"]) if want_t else None, _ptr(o["scales_t"]) if want_t else None)
     check(st, fn)
@@ -145,7 +167,7 @@ def bitlinear_fp8_fwd(x: torch.Tensor, w_q: torch.Tensor, w_scales: torch.Tensor
     _check(w_q, w_q.dtype, (n_out, k_in), "w_q", dev)
     _check(w_scales, torch.uint8, fp8_scales_shape(n_out, k_in), "w_scales", dev)
     if y is None:
-        y = x.new_empty((t, n_out), dtype=y_dtype)
+        y = _result(x, (t, n_out), y_dtype, stream)
     else:
         _check(y, y.dtype, (t, n_out), "y", dev)
     if y.dtype != torch.bfloat16 and y.dtype != torch.float32:
@@ -190,7 +212,7 @@ def bitlinear_fp8_bwd(dy: dict, x: dict | None, w: dict | None, *, want_grad_x: 
         _check(w["qt"], w["qt"].dtype, (k_in, n_out), "w qt", dev)
         _check(w["scales_t"], torch.uint8, fp8_scales_shape(k_in, n_out), "w scales_t", dev)
         if grad_x is None:
-            grad_x = torch.empty((t, k_in), dtype=torch.bfloat16, device=dev)
+            grad_x = _result(dy["q"], (t, k_in), torch.bfloat16, stream)
         _check(grad_x, torch.bfloat16, (t, k_in), "grad_x", dev)
     if want_grad_w:
         _check(dy["qt"], dy["q"].dtype, (n_out, t16), "dy qt", dev)
@@ -199,7 +221,7 @@ def bitlinear_fp8_bwd(dy: dict, x: dict | None, w: dict | None, *, want_grad_x: 
         _check(x["qt"], x["qt"].dtype, (k_in, t16), "x qt", dev)
         _check(x["scales_t"], torch.uint8, fp8_scales_shape(k_in, t), "x scales_t", dev)
         if grad_w is None:
-            grad_w = torch.empty((n_out, k_in), dtype=grad_w_dtype, device=dev)
+            grad_w = _result(dy["q"], (n_out, k_in), grad_w_dtype, stream)
         if grad_w.dtype not in (torch.bfloat16, torch.float32):
             raise TypeError(f"grad_w: expected bfloat16 or float32, got {grad_w.dtype}")
         _check(grad_w, grad_w.dtype, (n_out, k_in), "grad_w", dev)
@@ -235,11 +257,11 @@ def bitlinear_linear_ce_fwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Ten
     t, k_in, v = _check_ce(x, w, targets)
     dev = x.device
     if loss is None:
-        loss = x.new_empty((t,), dtype=torch.float32)
+        loss = _result(x, (t,), torch.float32, stream)
     else:
         _check(loss, torch.float32, (t,), "loss", dev)
     if lse is None:
-        lse = x.new_empty((t,), dtype=torch.float32)
+        lse = _result(x, (t,), torch.float32, stream)
     else:
         _check(lse, torch.float32, (t,), "lse", dev)
     need = bitlinear_linear_ce_fwd_workspace_size(t, v)
@@ -267,9 +289,9 @@ def bitlinear_linear_ce_bwd(x: torch.Tensor, w: torch.Tensor, targets: torch.Ten
     _check(lse, torch.float32, (t,), "lse", dev)
     _check(grad_loss, torch.float32, (t,), "grad_loss", dev)
     if want_grad_x and grad_x is None:
-        grad_x = torch.empty((t, k_in), dtype=torch.bfloat16, device=dev)
+        grad_x = _result(x, (t, k_in), torch.bfloat16, stream)
     if want_grad_w and grad_w is None:
-        grad_w = torch.empty((v, k_in), dtype=grad_w_dtype, device=dev)
+        grad_w = _result(x, (v, k_in), grad_w_dtype, stream)
     if grad_x is not None:
         _check(grad_x, torch.bfloat16, (t, k_in), "grad_x", dev)
     if grad_w is not None:

@@ -632,6 +632,61 @@ def test_own_workspace_on_another_stream():
     assert not ran and torch.equal(y, want) and junk.numel() == need
 
 
+def test_results_are_not_written_by_an_earlier_call_on_the_current_stream():
+    # a call on the current stream whose results are dropped has yet to write them; a call on
+    # another stream must not be handed their memory, which the first would then write over
+    t, k, n, v = 300, 512, 64, 700
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    a, b = (torch.randn(t, k, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
+    w = B.bitlinear_fp8_quant_weight(torch.randn(n, k, generator=gen, device="cuda"), want_t=True)
+    ws = {id(x): torch.randn(n, k, generator=gen, device="cuda") for x in (a, b)}
+    head = (torch.randn(v, k, generator=gen, device="cuda") * 0.1).to(torch.bfloat16)
+    y, g = torch.randint(0, v, (t,), generator=gen, device="cuda"), torch.randn(t, generator=gen, device="cuda")
+    lses = {id(x): B.bitlinear_linear_ce_fwd(x, head, y)[1] for x in (a, b)}
+    quants = {id(x): B.bitlinear_fp8_quant(x, want_t=True) for x in (a, b)}
+    dy = B.bitlinear_fp8_quant(torch.randn(t, n, generator=gen, device="cuda").to(torch.bfloat16), want_t=True)
+    s = torch.cuda.Stream()
+    calls = {"quant": lambda x, **o: list(B.bitlinear_fp8_quant(x, want_t=True, **o).values()),
+             "quant_weight": lambda x, **o: list(B.bitlinear_fp8_quant_weight(ws[id(x)], want_t=True, **o).values()),
+             "fwd": lambda x, **o: [B.bitlinear_fp8_fwd(x, w["q"], w["scales"], **o)],
+             "bwd": lambda x, **o: list(B.bitlinear_fp8_bwd(dy, quants[id(x)], w, **o)),
+             "ce_fwd": lambda x, **o: list(B.bitlinear_linear_ce_fwd(x, head, y, **o)),
+             "ce_bwd": lambda x, **o: list(B.bitlinear_linear_ce_bwd(x, head, y, lses[id(x)], g, **o))}
+    for name, call in calls.items():
+        want = [r.clone() for r in call(b)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(50_000_000)
+        call(a)
+        got = call(b, stream=s)
+        s.synchronize()
+        waiting = not torch.cuda.current_stream().query()
+        torch.cuda.synchronize()
+        assert waiting, name
+        for i, (p, q) in enumerate(zip(got, want)):
+            assert torch.equal(p.view(torch.uint8), q.view(torch.uint8)), (name, i)
+
+
+def test_dropped_results_of_a_given_stream():
+    # the other way round: a result dropped at once, before the given stream has written it,
+    # must not become memory of the current stream
+    t, k, v = 300, 512, 700
+    gen = torch.Generator(device="cuda").manual_seed(18)
+    x = torch.randn(t, k, generator=gen, device="cuda").to(torch.bfloat16)
+    head = (torch.randn(v, k, generator=gen, device="cuda") * 0.1).to(torch.bfloat16)
+    y = torch.randint(0, v, (t,), generator=gen, device="cuda")
+    want = B.bitlinear_linear_ce_fwd(x, head, y)[0]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)
+    loss, _ = B.bitlinear_linear_ce_fwd(x, head, y, stream=s)
+    waiting = not s.query()
+    _ = None
+    junk = [torch.full((t,), 7.0, device="cuda") for _ in range(64)]
+    torch.cuda.synchronize()
+    assert waiting and torch.equal(loss, want) and all(bool((j == 7.0).all()) for j in junk)
+
+
 def test_more_than_2_to_31_elements():
     # 384 rows over and over: the last copy, whose offsets pass 32 bits, comes out as the first
     reps, rows, k, n = 2732, 384, 2048, 16

@@ -186,3 +186,39 @@ def test_own_workspace_is_recorded_on_a_given_stream():
     assert head._workspace(None, 64, X(), side).stream is side
     assert head._workspace(None, 64, X(), None).stream is None
     assert head._workspace(None, 0, X(), side) is None
+
+
+def test_memory_of_a_call_comes_from_its_stream(monkeypatch):
+    current = ["current"]
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *exc):
+            current.pop()
+
+    class Memory:
+        def __init__(self):
+            self.pool, self.used_on = current[-1], []
+
+        def record_stream(self, stream):
+            self.used_on.append(stream)
+
+    class X:
+        device = torch.device("cuda", 0)
+
+        def new_empty(self, shape, dtype):
+            return Memory()
+
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: current[-1])
+    for make in (head._empty, head._result):
+        assert make(X(), (4,), torch.uint8, None).pool == "current" and make(X(), (4,), torch.uint8, "side").pool == "side"
+    assert head._workspace(None, 64, X(), "side").pool == "side" and head._workspace(None, 64, X(), None).pool == "current"
+    # results go on to the current stream
+    assert head._result(X(), (4,), torch.uint8, "side").used_on == ["current"] and current == ["current"]
+    assert head._result(X(), (4,), torch.uint8, None).used_on == []
