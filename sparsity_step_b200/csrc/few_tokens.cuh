@@ -179,37 +179,6 @@ __device__ __forceinline__ void few_fp8_operand(const FewArgs& a, uint32_t sB, u
   }
 }
 
-// Logits of the targets as fp32 dot products, a warp per token: the loss depends on them with
-// nothing to average over, and the tensor core's lost bits left one token's (2048 x 32768, 40
-// draws) up to 1.4e-6 off; now 2.1e-7. The epilogue warps do it while the weights stream by.
-__device__ __forceinline__ void few_target_logits(const FewArgs& a, int quad) {
-  auto low = [](uint32_t p) { return __uint_as_float(p << 16); };
-  auto high = [](uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); };
-  const int row8 = a.k / 8;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + quad; i < a.t; i += static_cast<int64_t>(gridDim.x) * 4) {
-    const int64_t y = a.targets[i];
-    if (y < 0 || y >= a.n) continue;
-    const uint4* x = static_cast<const uint4*>(a.x) + i * row8;
-    const uint4* w = static_cast<const uint4*>(a.rows) + y * row8;
-    float dot = 0.f;
-#pragma unroll 4
-    for (int j = lane_id(); j < row8; j += 32) {
-      const uint4 p = ld_plain(x + j), q = ld_plain(w + j);
-      float part = low(p.x) * low(q.x);
-      part = fmaf(high(p.x), high(q.x), part);
-      part = fmaf(low(p.y), low(q.y), part);
-      part = fmaf(high(p.y), high(q.y), part);
-      part = fmaf(low(p.z), low(q.z), part);
-      part = fmaf(high(p.z), high(q.z), part);
-      part = fmaf(low(p.w), low(q.w), part);
-      dot += fmaf(high(p.w), high(q.w), part);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-    if (lane_id() == 0) a.target_logit[i] = dot;
-  }
-}
-
 template <bool kFp8, int kTok>
 __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_constant__ FewMaps M, const FewArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -351,7 +320,11 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
   } else {
     // ------------------------------------------------------------- epilogue (4 warps)
     const int quad = warp & 3;
-    if constexpr (!kFp8) few_target_logits(a, quad);
+    if constexpr (!kFp8) {   // the targets' logits, while the weights stream by
+      int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + quad;
+      ce_targets(static_cast<const uint4*>(a.x), static_cast<const uint4*>(a.rows), a.targets, nullptr, a.t, a.n, a.k / 8, i,
+                 static_cast<int64_t>(gridDim.x) * 4, INT_MAX, lane, a.target_logit);
+    }
     bool ok = true;
     uint32_t unit = 0;
     for (int blk = blk0; blk < a.num_row_blocks && ok; blk += blk_step, ++unit) {

@@ -352,6 +352,18 @@ int64_t ce_piece(int64_t t, int64_t v) {
   return p >= 1024 ? p : all < 1024 ? all : 1024;
 }
 
+// The few tokens' plan of the forward pass, if it takes that kernel.
+bool few_ce_plan(int64_t t, int64_t k_in, int64_t v, FewPlan* p) {
+  return few_plan(false, false, t, k_in / 64, (v + 127) / 128, device_sm_count(), p);
+}
+// Whether the targets' logits of more tokens are dot products too, in both passes, or the
+// tensor cores', in which case the backward pass adds them up in the forward's parts, so that
+// both passes' agree. Dot products read every token's rows of X and W once more, whatever v is;
+// short parts make the product over v longer. Forward and backward of 8192 x 2048, dot
+// products / parts: v 1000 184 / 176 us, 4096 424 / 421, 8192 828 / 826, 32768 2.99 / 3.05
+// ms; 2047 x 1536 x 32003 580 / 590 us, 65536 x 2048 x 1000 1.38 / 1.20 ms.
+bool ce_dots(int64_t v) { return v >= 8192; }
+
 // Shapes of the head's operators: those of every entry point, with tokens up to 2^30 (the
 // kernels count padded tiles in 32 bits).
 bl_status check_head_shape(int64_t t, int64_t k_in, int64_t n_out) {
@@ -405,7 +417,6 @@ void ce_shape(bl::CeProblem& P, int mode, int64_t m, int64_t n, int64_t k, bool 
   P.M = static_cast<int>(m);
   P.N = static_cast<int>(n);
   P.num_k_blocks = static_cast<int>((k + 63) / 64);
-  P.part_blocks = mode == bl::CE_LSE ? bl::kCePartBlocks : P.num_k_blocks;
   P.num_m_blocks = static_cast<int>((m + 255) / 256);
   P.num_n_blocks = static_cast<int>((n + 255) / 256);
   P.splits = 1;
@@ -446,7 +457,7 @@ CeRuns ce_grad_x_runs(int64_t t, int64_t k_in, int64_t piece) {
 }
 
 struct CeBwdSpace {
-  size_t head, place, from, target, lse2, grad, x, dl[2], acc, total;
+  size_t head, place, from, target_dl, target, lse, grad, x, dl[2], acc, total;
 };
 CeBwdSpace ce_bwd_space(int64_t t, int64_t k_in, int64_t v, bool want_grad_x) {
   CeBwdSpace s{};
@@ -456,9 +467,10 @@ CeBwdSpace ce_bwd_space(int64_t t, int64_t k_in, int64_t v, bool want_grad_x) {
   s.head = 0;   // the live rows' number, the largest |grad_loss| and the first low half
   s.place = 256;
   s.from = s.place + rows * 4;
-  s.target = s.from + rows * 4;
-  s.lse2 = s.target + rows * 4;
-  s.grad = s.lse2 + rows * 4;
+  s.target_dl = s.from + rows * 4;
+  s.target = s.target_dl + rows * 4;
+  s.lse = s.target + rows * 4;
+  s.grad = s.lse + rows * 4;
   s.x = s.grad + rows * 4;
   s.dl[0] = s.x + round256(rows * static_cast<size_t>(k_in) * 2);
   s.dl[1] = s.dl[0] + (piece < v ? bytes : 0);   // the next piece's dl is written while this one's is read
@@ -617,7 +629,7 @@ bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const in
   float* target_logit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.target_logit);
   int num_strips = 0;
   FewPlan plan;
-  if (few_plan(false, false, t, k_in / 64, (v + 127) / 128, device_sm_count(), &plan)) {
+  if (few_ce_plan(t, k_in, v, &plan)) {
     bl::FewMaps M{};
     if (bl_status s = ce_operand(&M.w[0], w, k_in, v, k_in, false)) return s;
     if (bl_status s = make_map(&M.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, k_in, t, 64, plan.tok)) return s;
@@ -641,6 +653,9 @@ bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const in
     G.targets = targets;
     G.strips = strips;
     G.target_logit = target_logit;
+    G.x = ce_dots(v) ? reinterpret_cast<const uint4*>(x) : nullptr;
+    G.w = reinterpret_cast<const uint4*>(w);
+    G.row8 = static_cast<int>(k_in / 8);
     bl::CeProblem& P = G.p[0];
     ce_shape(P, bl::CE_LSE, t, v, k_in, false, false);
     if (bl_status s = ce_operand(&P.tmA, x, k_in, t, k_in, false)) return s;
@@ -690,8 +705,9 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
   int* low = live + 2;
   int* place = reinterpret_cast<int*>(space + sp.place);
   int* from = reinterpret_cast<int*>(space + sp.from);
+  float* target_dl = reinterpret_cast<float*>(space + sp.target_dl);
   int* row_target = reinterpret_cast<int*>(space + sp.target);
-  float* row_lse2 = reinterpret_cast<float*>(space + sp.lse2);
+  float* row_lse = reinterpret_cast<float*>(space + sp.lse);
   float* row_grad = reinterpret_cast<float*>(space + sp.grad);
   uint8_t* x_live = space + sp.x;
   float* acc = reinterpret_cast<float*>(space + sp.acc);
@@ -702,17 +718,23 @@ bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const in
   if (bl_status s = launch_head("linear ce live launch", bl::ce_live_kernel, 1, 1024, st, grad_loss, targets, t, v, place, from, live,
                                 low, grad_max))
     return s;
-  if (bl_status s = launch_head("linear ce gather launch", bl::ce_gather_kernel, rows / 8 < cap ? rows / 8 : cap, 256, st,
-                                reinterpret_cast<const uint4*>(x), targets, lse, grad_loss, static_cast<const int*>(from),
-                                static_cast<const int*>(live), static_cast<const int*>(low), static_cast<const float*>(grad_max), row8,
-                                reinterpret_cast<uint4*>(x_live), row_target, row_lse2, row_grad))
+  FewPlan plan;
+  const bool dots = few_ce_plan(t, k_in, v, &plan) || ce_dots(v);   // as in the forward pass
+  const int64_t row_blocks = rows / 8 < cap ? rows / 8 : cap, dot_blocks = !dots ? 0 : (t + 7) / 8 < cap ? (t + 7) / 8 : cap;
+  if (bl_status s = launch_head("linear ce gather launch", bl::ce_gather_kernel, row_blocks + dot_blocks, 256, st,
+                                reinterpret_cast<const uint4*>(x), reinterpret_cast<const uint4*>(w), targets, lse, grad_loss, t, v,
+                                static_cast<int>(row_blocks), static_cast<const int*>(from), static_cast<const int*>(live),
+                                static_cast<const int*>(low), static_cast<const float*>(grad_max), row8,
+                                reinterpret_cast<uint4*>(x_live), row_target, row_lse, row_grad, target_dl))
     return s;
   bl::CeGroup G{};
   G.v = v;
   G.live = live;
   G.low = low;
   G.row_target = row_target;
-  G.row_lse2 = row_lse2;
+  G.row_lse = row_lse;
+  G.from = from;
+  G.target_dl = dots ? target_dl : nullptr;
   G.row_grad = row_grad;
   G.grad_max = grad_max;
   // launch i: the two products of piece i - 1 and dl of piece i

@@ -6,23 +6,27 @@
 //   grad_X = dl W,  grad_W = dl^T X
 //
 // Forward: one pass of a CTA-pair product whose epilogue reduces each 128-column strip of
-// logits but the target's in registers to its maximum and its sum of exponentials (fp32, the logits never
-// rounded), so a token leaves 8 bytes per 128 columns of the vocabulary instead of 512; a
-// small kernel joins the strips in a fixed order. The tensor core's accumulator drops the
-// bits of an addend below its own last one, always towards zero: over K = 2048 the logits
-// came out 4e-6 too small. So the accumulator starts afresh every 512 of K and the parts
-// are added in registers, rounded to nearest, which stays below 1e-6 at any K.
+// logits but the target's in registers to its maximum and its sum of exponentials (fp32, the
+// logits never rounded), so a token leaves 8 bytes per 128 columns of the vocabulary instead
+// of 512; a small kernel joins the strips in a fixed order. The tensor core's accumulator
+// drops the bits of an addend below its own last one, always towards zero, half a unit per MMA
+// on average: a logit of 18 over K = 2048 came out 4e-5 too small. So the accumulator starts
+// afresh every 512 of K and the parts are added in registers, rounded to nearest: 2^-20 of a
+// logit at any K.
 // Backward, one piece of the vocabulary after another: the logits of the piece are computed
-// again, their epilogue writes dl of the piece in bf16 (the operand type of the tensor
-// cores: one rounding of at most half a step per factor; few tokens as the sum of two, see
-// kCeSplitTokens), and two products consume it,
-// grad_W of the piece's rows and the piece's addend of grad_X, summed in fp32. Tokens without
-// a loss (padding, prompts) are left out first: the others' rows are gathered to the front,
-// the products stop after them, and grad_X is scattered back. Four products of 2 T V K
-// operations in all against three with all logits kept (T x V). g is divided by its largest
-// magnitude before that rounding and the gradients multiplied by it after: with the usual
-// constant g, dl of a target is then p - 1 itself, not a product whose rounding error every
-// token would share.
+// again, their epilogue writes dl of the piece in bf16 (the operand type of the tensor cores:
+// one rounding of at most half a step per factor; few tokens as the sum of two, see
+// kCeSplitTokens), and two products consume it, grad_W of the piece's rows and the piece's
+// addend of grad_X, summed in fp32. dl of a target is exp(l_y - lse) - 1, of a sure token a
+// small difference: l_y has to be off by what it was off by in the forward pass's lse (a
+// logit from one accumulation of K = 2048 made dl of one token 4.5e-5 instead of 0.9e-5). So
+// both passes take the same dot product, or the same parts (ce_dots). Tokens without a loss
+// (padding, prompts) are left out first: the others' rows are gathered to the front, the
+// products stop after them, and grad_X is scattered back. Four products of 2 T V K operations
+// in all against three with all logits kept (T x V). g is divided by its largest magnitude
+// before that rounding and the gradients multiplied by it after: with the usual constant g, dl
+// of a target is then p - 1 itself, not a product whose rounding error every token would
+// share.
 // Bound by the bf16 tensor pipe (and the power it draws).
 //
 // The kernel takes up to three products with their own operand orders, depths and
@@ -41,7 +45,7 @@
 namespace bl {
 
 enum CeMode : int {
-  CE_LSE = 0,       // the target's logit, strip maxima and sums of exponentials of the others
+  CE_LSE = 0,       // strip maxima and sums of exponentials, without the target's
   CE_DLOGITS = 1,   // dl in bf16
   CE_BF16 = 2,      // the product times the largest |g|, bf16
   CE_F32 = 3,       // the product times the largest |g|, fp32
@@ -55,7 +59,6 @@ struct CeProblem {
   int a_mn, b_mn;                // operand order: 0 K-major, 1 MN-major
   int M, N;
   int num_k_blocks;              // ceil(K / 64)
-  int part_blocks;               // K blocks per accumulation in TMEM
   int num_m_blocks, num_n_blocks;   // 256 x 256 tiles
   // CE_PART, CE_ADD_PART: K in `splits` runs of split_blocks, run i to output rows from
   // i * 256 num_m_blocks on (1 run otherwise)
@@ -70,15 +73,20 @@ struct CeGroup {
   CeShares share[kMaxCeGroup];
   int count;
   int64_t v;                     // vocabulary size
+  // CE_LSE: the targets' logits are dot products of these rows of 8 row8 (x null: the product's)
+  const uint4 *x, *w;
+  int row8;
   const int64_t* targets;        // [T]  (CE_LSE)
   // backward: the tokens with a loss in order (a few of them a second time, for their low
   // halves), then zeros (target -1) up to 256 rows
   const int* live;               // rows of them, at least 1
   const int* low;                // first of their low halves' rows (INT_MAX: none)
   const int* row_target;
-  const float* row_lse2;         // lse in units of log2
+  const float* row_lse;
   const float* row_grad;         // g over the largest |g|
   const float* grad_max;         // the largest finite |g|, or 1
+  const int* from;               // the live tokens
+  const float* target_dl;        // [T] dl of the targets over g (null: from the product's logits)
   float2* strips;                // [2 * n blocks, T] (max, sum)  (CE_LSE)
   float* target_logit;           // [T]  (CE_LSE)
 };
@@ -105,6 +113,10 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+__device__ __forceinline__ void st_shared_bf16(uint32_t addr, __nv_bfloat16 v) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(__bfloat16_as_ushort(v)) : "memory");
+}
+
 // Blocks of a tile and its run of K blocks [kb0, kb1), empty behind the live tokens.
 struct CeTile {
   int mb, nb, split, kb0, kb1;
@@ -127,7 +139,17 @@ __device__ __forceinline__ CeTile ce_tile(const CeProblem& P, int tile, int live
   return T;
 }
 
-constexpr int kCePartBlocks = 8;   // 512 of K per accumulation of the logits
+// K blocks per accumulation of the logits: 512 of K in the forward pass, where the backward
+// pass has its targets' logits from them too, and where dl is held as two numbers. Else one
+// bf16 number (half a step 2^-8) does not show what 4096 of K lose, 2^-17 of a logit, and
+// parts of 512 made the backward pass longer: 8192 x 2048 x 32768 2.28 -> 2.37 ms, 2047 x 1536
+// x 32003 440 -> 452 us.
+constexpr int kCePartBlocks = 8, kCeLongPartBlocks = 64;
+__device__ __forceinline__ int ce_part_blocks(const CeProblem& P, bool short_parts) {
+  return P.mode == CE_LSE || (P.mode == CE_DLOGITS && short_parts) ? kCePartBlocks
+         : P.mode == CE_DLOGITS                                    ? kCeLongPartBlocks
+                                                                   : P.num_k_blocks;
+}
 
 // The accumulator's 32 rows x 128 columns of one warp: thread = row, acc[c][j] = column 32 c + j.
 using CeAcc = float[4][32];
@@ -148,7 +170,7 @@ __device__ __forceinline__ void ce_strip(const CeGroup& G, const CeProblem& P, C
         t = is ? acc[c][j] : t;
         acc[c][j] = is ? -INFINITY : acc[c][j];
       }
-    G.target_logit[row] = t;
+    if (!G.x) G.target_logit[row] = t;
   }
   if (left < 128) {
 #pragma unroll
@@ -174,19 +196,67 @@ __device__ __forceinline__ void ce_strip(const CeGroup& G, const CeProblem& P, C
   G.strips[static_cast<int64_t>(strip) * P.M + row] = make_float2(m2, (s[0] + s[1]) + (s[2] + s[3]));
 }
 
+// x . w of one row each, by a warp in fp32: the loss and a target's dl depend on the target's
+// logit with nothing to average over, and the tensor core's lost bits left one token's loss
+// (2048 x 32768, 40 draws) up to 1.4e-6 off; now 2.1e-7. Every lane returns the sum.
+__device__ __forceinline__ float ce_dot(const uint4* x, const uint4* w, int row8, int lane) {
+  auto low = [](uint32_t p) { return __uint_as_float(p << 16); };
+  auto high = [](uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); };
+  float dot = 0.f;
+#pragma unroll 4
+  for (int j = lane; j < row8; j += 32) {
+    const uint4 p = ld_plain(x + j), q = ld_plain(w + j);
+    float part = low(p.x) * low(q.x);
+    part = fmaf(high(p.x), high(q.x), part);
+    part = fmaf(low(p.y), low(q.y), part);
+    part = fmaf(high(p.y), high(q.y), part);
+    part = fmaf(low(p.z), low(q.z), part);
+    part = fmaf(high(p.z), high(q.z), part);
+    part = fmaf(low(p.w), low(q.w), part);
+    dot += fmaf(high(p.w), high(q.w), part);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+  return dot;
+}
+
+// Of the targets of tokens i, i + step, ..., `most` of them at most, by a warp: the logits, or
+// with lse their dl over g, exp(l - lse) - 1 (in one: of a sure token it is far below the
+// roundings of exp(l - lse)). i is the next token after them.
+__device__ __forceinline__ void ce_targets(const uint4* x, const uint4* w, const int64_t* targets, const float* lse, int64_t t, int64_t v,
+                                           int row8, int64_t& i, int64_t step, int most, int lane, float* out) {
+  for (; i < t && most > 0; i += step, --most) {
+    const int64_t y = targets[i];
+    if (y < 0 || y >= v) continue;
+    const float l = ce_dot(x + i * row8, w + y * row8, row8, lane);
+    if (lane == 0) out[i] = lse ? expm1f(l - lse[i]) : l;
+  }
+}
+
+// dl of a row's target from that of its token.
+__device__ __forceinline__ __nv_bfloat16 ce_target_dl(const CeGroup& G, int row) {
+  const int first_low = *G.low;
+  const bool low = row >= first_low;
+  const float g = G.row_grad[row];
+  const float dl = g == 0.f ? 0.f : G.target_dl[G.from[low ? row - first_low : row]] * g;
+  const __nv_bfloat16 first = __float2bfloat16_rn(dl);
+  return low ? __float2bfloat16_rn(dl - __bfloat162float(first)) : first;
+}
+
 // 32 rows x 128 columns through shared memory: dl, or the product itself.
 __device__ __forceinline__ void ce_store(const CeGroup& G, const CeProblem& P, CeAcc& acc, uint32_t stg, int row0, int n0,
                                          int lane) {
+  const int row = row0 + lane;
+  int hit = -1;   // the target's column, if it is among these 128
   if (P.mode == CE_DLOGITS) {
-    const int row = row0 + lane;
-    const float lse2 = G.row_lse2[row], g = G.row_grad[row];
+    const float lse2 = G.row_lse[row] * kLog2e, g = G.row_grad[row];
     const bool low = row >= *G.low;
-    const int hit = G.row_target[row] - P.v0 - n0;
+    hit = G.row_target[row] - P.v0 - n0;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int j = 0; j < 32; ++j) acc[c][j] = ex2(fmaf(acc[c][j], kLog2e, -lse2));
-    if (hit >= 0 && hit < 128) {
+    if (!G.target_dl && hit >= 0 && hit < 128) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -249,6 +319,10 @@ __device__ __forceinline__ void ce_store(const CeGroup& G, const CeProblem& P, C
         const float* f = &acc[2 * h + (j >> 2)][8 * (j & 3)];
         put(j, pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
       }
+      if (G.target_dl && hit >> 6 == h) {   // the target's dl over the p that is there
+        const uint32_t at = row_addr + static_cast<uint32_t>(((hit >> 3 & 7) ^ (lane & 7)) * 16 + (hit & 7) * 2);
+        st_shared_bf16(at, ce_target_dl(G, row));
+      }
       store(64 * h);
     }
   }
@@ -301,6 +375,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
   const uint32_t tmem_base = __reduce_or_sync(0xffffffffu, *tmem_slot);   // the same in every lane: a uniform register
   const uint32_t peer_abort = map_to_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
   const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  const bool short_parts =
+      G.low && (!G.target_dl || __reduce_min_sync(0xffffffffu, static_cast<unsigned>(ld_plain(G.low))) != INT_MAX);
   const int live_rows = G.live ? static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(ld_plain(G.live)))) : 0;
 
   if (warp == 0) {
@@ -368,11 +444,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
         // swizzled row, MN-major 16 K rows = 2 KB
         const uint64_t a_step = P.a_mn ? 128u : 2u, b_step = P.b_mn ? 128u : 2u;
         const uint32_t a_lbo = P.a_mn ? 8192u : 16u, b_lbo = P.b_mn ? 8192u : 16u;
+        const int part = ce_part_blocks(P, short_parts);
         for (int r = 0; r < rounds; ++r) {
           const CeTile T = ce_tile(P, ce_round_tile(G.share[j], nclusters, pos, r), live_rows);
-          for (int k0 = T.kb0; k0 < T.kb1; k0 += P.part_blocks, ++unit) {
+          for (int k0 = T.kb0; k0 < T.kb1; k0 += part, ++unit) {
             const uint32_t buf = unit & 1u;
-            const int end = min(k0 + P.part_blocks, T.kb1);
+            const int end = min(k0 + part, T.kb1);
             live = wait_live<false>(live, tempty0 + 8u * buf, ((unit >> 1) & 1u) ^ 1u, abort_flag, peer_abort);
             tc_fence_after_sync();
             const uint32_t d_tmem = tmem_base + buf * kBN;
@@ -410,16 +487,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
     const uint32_t tempty_leader0 = map_to_rank(tempty0, 0);
     uint32_t unit = 0;
     bool ok = true;
+    // the targets' logits, while tiles are on their way: a few before each, so that no other
+    // warp waits long for this one, what is left of them at the end
+    int64_t token = static_cast<int64_t>(blockIdx.x) * kEpiWarps + e;
+    auto target_logits = [&](int most) {
+      ce_targets(G.x, G.w, G.targets, nullptr, G.p[0].M, G.v, G.row8, token, static_cast<int64_t>(gridDim.x) * kEpiWarps, most, lane,
+                 G.target_logit);
+    };
     for (int j = 0; j < G.count && ok; ++j) {
       const CeProblem& P = G.p[j];
       const int rounds = G.share[j].count[cluster], pos = G.share[j].pos[cluster];
+      const int part = ce_part_blocks(P, short_parts);
       for (int r = 0; r < rounds && ok; ++r) {
         const CeTile T = ce_tile(P, ce_round_tile(G.share[j], nclusters, pos, r), live_rows);
         const int row0 = T.mb * 256 + 128 * static_cast<int>(rank) + quad * 32;
         const int n0 = T.nb * 256 + 128 * half;
+        if (G.x) target_logits(8);
         CeAcc acc;
 #pragma unroll 1
-        for (int k0 = T.kb0; k0 < T.kb1; k0 += P.part_blocks, ++unit) {
+        for (int k0 = T.kb0; k0 < T.kb1; k0 += part, ++unit) {
           const uint32_t buf = unit & 1u;
           const bool got = mbar_wait(tfull0 + 8u * buf, (unit >> 1) & 1u, abort_flag);
           if (!__all_sync(0xffffffffu, got)) {
@@ -453,6 +539,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
         else ce_store(G, P, acc, stg, row0 + T.split * P.num_m_blocks * 256, n0, lane);
       }
     }
+    if (G.x) target_logits(INT_MAX);
     if (!ok && lane == 0) {
       pair_abort(abort_flag, peer_abort);
       atomicOr(&g_device_status, DEV_ST_TIMEOUT_EPILOGUE);
@@ -537,23 +624,32 @@ __global__ void __launch_bounds__(1024) ce_live_kernel(const float* grad, const 
   }
 }
 
-// Their rows of X and what dl needs of them, then zeros up to a multiple of 256 rows. A warp
-// per row.
-__global__ void __launch_bounds__(256) ce_gather_kernel(const uint4* x, const int64_t* targets, const float* lse, const float* grad,
-                                                        const int* from, const int* live, const int* low_row,
-                                                        const float* grad_max, int row8,
-                                                        uint4* x_live, int* row_target, float* row_lse2, float* row_grad) {
+// Their rows of X and what dl needs of them, then zeros up to a multiple of 256 rows, by the
+// first `row_blocks` blocks, a warp per row. The others, if any, meanwhile take all tokens'
+// target_dl: nothing here depends on those, and they on nothing of ce_live_kernel (32 tokens:
+// after the rows, or in that kernel, they took 4 us more).
+__global__ void __launch_bounds__(256) ce_gather_kernel(const uint4* x, const uint4* w, const int64_t* targets, const float* lse,
+                                                        const float* grad, int64_t t, int64_t v, int row_blocks, const int* from,
+                                                        const int* live, const int* low_row, const float* grad_max, int row8,
+                                                        uint4* x_live, int* row_target, float* row_lse, float* row_grad,
+                                                        float* target_dl) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, block = blockIdx.x;
   follow_stream();
-  const int n = *live, low = *low_row, end = (n + 255) / 256 * 256, lane = threadIdx.x & 31;
-  for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < end; r += gridDim.x * 8) {
-    const int t = r < n ? from[r < low ? r : r - low] : -1;
+  if (block >= row_blocks) {
+    int64_t i = static_cast<int64_t>(block - row_blocks) * 8 + warp;
+    ce_targets(x, w, targets, lse, t, v, row8, i, static_cast<int64_t>(gridDim.x - row_blocks) * 8, INT_MAX, lane, target_dl);
+    return;
+  }
+  const int n = *live, low = *low_row, end = (n + 255) / 256 * 256;
+  for (int r = block * 8 + warp; r < end; r += row_blocks * 8) {
+    const int at = r < n ? from[r < low ? r : r - low] : -1;
     uint4* dst = x_live + static_cast<int64_t>(r) * row8;
-    const uint4* src = x + static_cast<int64_t>(t < 0 ? 0 : t) * row8;
-    for (int i = lane; i < row8; i += 32) dst[i] = t < 0 ? make_uint4(0, 0, 0, 0) : ld_plain(src + i);
+    const uint4* src = x + static_cast<int64_t>(at < 0 ? 0 : at) * row8;
+    for (int i = lane; i < row8; i += 32) dst[i] = at < 0 ? make_uint4(0, 0, 0, 0) : ld_plain(src + i);
     if (lane == 0) {
-      const float g = t < 0 ? 0.f : grad[t];
-      row_target[r] = t < 0 ? -1 : static_cast<int>(targets[t]);
-      row_lse2[r] = t < 0 ? 0.f : lse[t] * kLog2e;
+      const float g = at < 0 ? 0.f : grad[at];
+      row_target[r] = at < 0 ? -1 : static_cast<int>(targets[at]);
+      row_lse[r] = at < 0 ? 0.f : lse[at];
       row_grad[r] = g == 0.f ? 0.f : __fdiv_rn(g, *grad_max);
     }
   }

@@ -489,6 +489,65 @@ def test_linear_ce_few_tokens_keep_dl(t, k, v, live):
         assert worst <= 1.0, f"worst error {worst:.3f} of its bound"
 
 
+def sure_inputs(t, k, v, seed, top=18.0):
+    """Hidden states whose targets' logits run from about 0 to `top` (others: N(0, 0.02^2 k))."""
+    rng = np.random.default_rng(seed)
+    w, y = bf16(rng, v, k, scale=0.02, outliers=False), rng.permutation(v)[:t]
+    push = np.linspace(top / t, top, t)[:, None]
+    x = rng.normal(size=(t, k)) + push * w[y] / (w[y] ** 2).sum(1, keepdims=True)
+    return torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16).float().numpy(), w, y.astype(np.int64)
+
+
+@pytest.mark.parametrize("t,k,v", [(1, 2048, 1000), (32, 2048, 1000), (33, 2048, 1000), (200, 2048, 1000), (20, 8192, 1000),
+                                   (100, 8192, 700), (40, 512, 5003), (64, 2048, 9001)])
+def test_linear_ce_gradient_of_sure_tokens(t, k, v):
+    """dl of tokens that are nearly sure of their target, one at a time (g is 0 elsewhere, so
+    that grad_w of row u is dl_u x): with 1 - p down to 1e-5 it has to come from l_y - lse as
+    the forward pass had them. The errors of the logits count by what they move the others'
+    sum, 1 - p of them; the rest is the rounding of l_y and lse, and of dl itself."""
+    x, w, y = sure_inputs(t, k, v, 20)
+    o, d = H.linear_ce(x, w, y, np.ones(t)), logit_errors(x, w, k)
+    xd, wd, yd = dev(x, torch.bfloat16), dev(w, torch.bfloat16), dev(y)
+    _, lse = B.bitlinear_linear_ce_fwd(xd, wd, yd)
+    for i in sorted({t - 1, t - 1 - t // 20, t - 1 - t // 10, t // 2}):
+        g = torch.zeros(t, device="cuda")
+        g[i] = 1.0
+        _, gw = B.bitlinear_linear_ce_bwd(xd, wd, yd, lse, g, want_grad_x=False, grad_w_dtype=torch.float32)
+        j = np.argmax(np.abs(x[i]))
+        dl, got = o["dl"][i], f64(gw[:, j]) / x[i, j]
+        l, rest = o["logits"][i], -o["dl"][i, y[i]]
+        spread = 2 * d[i] + 2.0 ** -18 + U * (8 * np.abs(l).max() + 4 * np.abs(o["lse"][i]))
+        err = np.where(np.arange(v) == y[i], rest * np.expm1(spread) + U * (abs(o["lse"][i]) + abs(l[y[i]])),
+                       o["p"][i] * np.expm1(spread))
+        half = BF16 ** 2 if t <= 32 else BF16
+        tol = err + (half + 8 * U) * (np.abs(dl) + err)
+        worst = np.max(np.abs(got - dl) / tol)
+        assert worst <= 1.0, f"token {i}: 1 - p {rest:.2e}, worst error {worst:.3f} of its bound"
+
+
+@pytest.mark.parametrize("t,k,v", [(1, 2048, 1000), (32, 2048, 1000), (33, 2048, 1000), (512, 2048, 700), (32, 8192, 1000),
+                                   (300, 8192, 1000), (1000, 896, 5003), (300, 2048, 8192)])
+def test_linear_ce_loss_to_its_stated_error(t, k, v):
+    """At the size the errors have, where the bounds above count every one at its largest and
+    of one sign. A tensor core's accumulation loses half a unit of its running sum per MMA (16
+    of K) on average, towards zero: over 512 of K the target's logit, which grows evenly, comes
+    out 32 / 2 * 2^-24 = 2^-20 of itself too small (twice that is allowed); as a dot product
+    (few tokens, large vocabularies) it is rounded to nearest, half a unit for each of the last
+    five halvings. The others' are off by 2^-20 of themselves, of sizes about 1 here. The loss
+    takes 1 - p of both, and three roundings of half a unit. lse has the target's error in full
+    where the token is sure."""
+    x, w, y = sure_inputs(t, k, v, 19)
+    o = H.linear_ce(x, w, y)
+    loss, lse = B.bitlinear_linear_ce_fwd(dev(x, torch.bfloat16), dev(w, torch.bfloat16), dev(y))
+    l = np.abs(o["logits"][np.arange(t), y])
+    own = l * (5 * 2.0 ** -24 if t <= 32 or v >= 8192 else 2.0 ** -19)
+    rest = -np.expm1(-o["loss"])
+    err = np.abs(f64(loss) - o["loss"])
+    assert np.all(err <= rest * (own + 1e-6) + 3 * 2.0 ** -24 * np.exp2(np.ceil(np.log2(np.maximum(o["loss"], 1e-30)))))
+    assert np.all(np.abs(f64(lse) - o["lse"]) <= own + 1e-6 + 3 * U * np.maximum(np.abs(o["lse"]), l))
+    assert err.mean() <= (3.5e-7 if t <= 32 else 1e-6)
+
+
 def test_linear_ce_empty_batch():
     w = torch.randn(50, 64, device="cuda").to(torch.bfloat16)
     x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
@@ -655,7 +714,7 @@ def test_results_are_not_written_by_an_earlier_call_on_the_current_stream():
     for name, call in calls.items():
         want = [r.clone() for r in call(b)]
         torch.cuda.synchronize()
-        torch.cuda._sleep(50_000_000)
+        torch.cuda._sleep(400_000_000)   # 0.2 s: new memory for the other stream may take tens of ms
         call(a)
         got = call(b, stream=s)
         s.synchronize()
@@ -678,7 +737,7 @@ def test_dropped_results_of_a_given_stream():
     s = torch.cuda.Stream()
     torch.cuda.synchronize()
     with torch.cuda.stream(s):
-        torch.cuda._sleep(50_000_000)
+        torch.cuda._sleep(400_000_000)
     loss, _ = B.bitlinear_linear_ce_fwd(x, head, y, stream=s)
     waiting = not s.query()
     _ = None
