@@ -434,8 +434,10 @@ bl_status bitlinear_linear_ce_fwd(const uint16_t* x, const uint16_t* w, const in
  * without a loss contributes nothing, whatever its x, lse and grad_loss hold, and costs
  * nothing in the products.
  * The logits are computed again, one piece of the vocabulary after another; the workspace
- * holds two pieces of dl, an fp32 sum of grad_x and a copy of x, and all of dl [t, v] only
- * where that is below 64 MB. Sums are fp32 and in a fixed order.
+ * holds an fp32 sum of grad_x, a copy of x and two pieces of dl, each of at most 112 MB, or of
+ * 1024 of the vocabulary where those take more (2048 bytes a token: above 57344 tokens). All
+ * of dl [t, v] at once where that is below 64 MB or v is at most 1024. Sums are fp32 and in a
+ * fixed order.
  */
 size_t bitlinear_linear_ce_bwd_workspace_size(int64_t t, int64_t k_in, int64_t v, int want_grad_x);
 bl_status bitlinear_linear_ce_bwd(const uint16_t* x, const uint16_t* w, const int64_t* targets, const float* lse,

@@ -340,16 +340,22 @@ int64_t ce_dl_rows(int64_t t) { return t >= 2 * bl::kCeSplitTokens ? t : t <= bl
 // (8192 x 2048 x 65536 backward: pieces of 32 MB 5.13 ms, 64 MB 5.00, 128 MB 4.55, 256 MB
 // 4.61; 112 MB keeps the workspace below a third of the logits there).
 constexpr int64_t kCeWholeBytes = int64_t(64) << 20, kCePieceBytes = int64_t(112) << 20;
+// But never of fewer rows of the vocabulary than these: grad_W's product has a tile for 256 of
+// them and 256 columns, each over all tokens, and below four rows of tiles most SMs have none
+// (backward, pieces of at least 1024 / 512 / 256 rows: 65536 x 2048 x 1000 0.99 / 1.31 / 2.03
+// ms, x 4000 2.87 / 3.51 / 3.52; 131072 x 1024 x 32768 30 / 47 / 89). So a piece of more than
+// 57344 tokens exceeds kCePieceBytes, and a vocabulary of up to 1024 is never divided.
+constexpr int64_t kCePieceRows = 1024;
 
-// Vocabulary rows per piece of the backward pass: all of them, or a multiple of 256 and a
-// quarter of the vocabulary at most, so that the two pieces held at a time stay well below
-// the logits.
+// Vocabulary rows per piece of the backward pass: all of them, or a multiple of 256 and, above
+// kCePieceRows, a quarter of the vocabulary at most, so that the two pieces held at a time
+// stay well below the logits.
 int64_t ce_piece(int64_t t, int64_t v) {
   const int64_t all = round_up(v, 256), row = 2 * (t > 0 ? ce_dl_rows(t) : 1);
   if (row * all <= kCeWholeBytes) return all;
   const int64_t fit = kCePieceBytes / row / 256 * 256, quarter = round_up((v + 3) / 4, 256);
   const int64_t p = fit < quarter ? fit : quarter;
-  return p >= 1024 ? p : all < 1024 ? all : 1024;
+  return p >= kCePieceRows ? p : all < kCePieceRows ? all : kCePieceRows;
 }
 
 // The few tokens' plan of the forward pass, if it takes that kernel.

@@ -123,6 +123,19 @@ def test_linear_ce_workspace_is_far_from_the_logits(L):
     assert L.bitlinear_linear_ce_fwd_workspace_size(0, v) == 0 and L.bitlinear_linear_ce_bwd_workspace_size(0, k, v, 1) == 0
 
 
+@pytest.mark.parametrize("v", [1, 1000, 1024, 1025, 2000, 4000, 32003, 65536])
+@pytest.mark.parametrize("t", [1, 33, 8192, 16384, 57344, 65536, 1 << 20])
+def test_linear_ce_workspace_is_what_the_header_states(L, t, v):
+    # besides dl: a copy of x, six words a token and, with grad_x, its fp32 sum
+    k, rows = 64, (t + 255) // 256 * 256
+    dl = L.bitlinear_linear_ce_bwd_workspace_size(t, k, v, 0) - rows * (2 * k + 24) - 256
+    mib, padded = 1 << 20, (v + 255) // 256 * 256
+    whole = 2 * max(t, 64) * padded
+    assert dl <= (whole if whole <= 64 * mib or v <= 1024 else 2 * max(112 * mib, 2048 * t)) + 1024
+    sums = L.bitlinear_linear_ce_bwd_workspace_size(t, k, v, 1) - L.bitlinear_linear_ce_bwd_workspace_size(t, k, v, 0)
+    assert sums % (rows * k * 4) == 0 and sums > 0 and (t < 74 * 256 or sums == rows * k * 4)
+
+
 # ------------------------------------------------------------------ the binding
 
 def test_binding_refuses_host_and_mistyped_tensors():
