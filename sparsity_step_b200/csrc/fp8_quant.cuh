@@ -23,7 +23,6 @@
 
 namespace bl {
 
-constexpr int kFp8Block = 128;   // values per scale along the reduction
 enum : int { FP8_E4M3 = 0, FP8_E5M2 = 1 };
 
 __host__ __device__ constexpr int fp8_top_exponent(int fmt) { return fmt == FP8_E5M2 ? 15 : 8; }
@@ -54,10 +53,6 @@ __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&a)),
                                        __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
   return *reinterpret_cast<const uint32_t*>(&r);
-}
-// 2^e of a scale byte; byte 0 is 2^-127, a subnormal.
-__device__ __forceinline__ float fp8_scale(uint32_t byte) {
-  return __uint_as_float(byte == 255u ? 0x7FFFFFFFu : byte == 0u ? 0x00400000u : byte << 23);
 }
 
 // Two codes, `lo` in the low byte.
@@ -104,7 +99,7 @@ constexpr int kFp8QuantThreads = 256;
 template <bool kWeight, bool kE5M2, bool kT>
 __global__ void __launch_bounds__(kFp8QuantThreads) fp8_quant_kernel(const Fp8QuantArgs a) {
   constexpr int kTop = fp8_top_exponent(kE5M2 ? FP8_E5M2 : FP8_E4M3);
-  __shared__ uint32_t s_max[8][64];                          // per warp: column maxima (bf16 pairs) or one block maximum
+  __shared__ __align__(16) uint32_t s_max[8][64];            // per warp: column maxima (bf16 pairs) or one block maximum
   __shared__ __align__(16) uint32_t s_inv[64];               // column pairs' 2^-e
   __shared__ __align__(16) uint8_t s_t[kT ? 128 * 128 : 16];   // transposed codes
   __shared__ uint8_t s_row[128];                             // row scale bytes
