@@ -255,6 +255,73 @@ def test_fp8_empty_batch():
     assert gx.shape == (0, 128) and not gw.any()
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_quant_extremes_of_both_formats(fmt):
+    # as above, against each format's own ends: its largest values and the next above, the
+    # scale's least byte and the fp32 values below it, an infinity, a NaN of either sign
+    top = H.TOP[fmt]
+    x = np.zeros((12, 272), np.float32)
+    x[0, :2], x[1, :2] = [top, -top], [top * (1 + 2.0 ** -7), 1.0]
+    x[2, 0], x[3, 0] = 1.75, 1.7578125
+    x[4, 0], x[5, 3], x[6, 0] = 2.0 ** -133, 2.0 ** -126, top * 2.0 ** -127
+    x[7, :128] = 3.3895314e38
+    x[8, 7], x[9, 200], x[10, 260], x[11, 130] = np.inf, np.nan, -np.inf, -np.nan
+    x = torch.from_numpy(x).to(torch.bfloat16).float().numpy()
+    got = B.bitlinear_fp8_quant(dev(x, torch.bfloat16), want_t=True, fmt=FMT[fmt])
+    want = H.fp8_quant_both(x, fmt)
+    check_quant(got, want, False)
+    assert np.array_equal(u8(got["scales_t"]), want["scales_t"])
+    fine = want["scales_t"][0, :, 0] != 255
+    assert np.array_equal(u8(got["qt"])[fine], want["qt"][fine]) and np.all(u8(got["qt"])[~fine][:, :12] == H.NAN_CODE)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_quant_weight_extremes(fmt):
+    # one block of weights each: an infinity, a NaN, zeros, the largest fp32 values, values
+    # around the least scale and below fp32's normal ones, the format's own ends
+    top = H.TOP[fmt]
+    w = np.zeros((144, 1088), np.float32)
+    w[3, 5], w[140, 130] = np.inf, np.nan
+    w[:, 256:384] = 3.4028235e38 * np.linspace(-1, 1, 144, dtype=np.float32)[:, None]
+    w[7, 384:387] = [top * 2.0 ** -127, 2.0 ** -130, -2.0 ** -149]
+    w[9, 512:514] = [2.0 ** -140, 2.0 ** -149]
+    w[130, 640:642], w[5, 640:642] = [top, -top], [np.nextafter(np.float32(top), np.float32(np.inf)), 1.0]
+    w[:, 768:896] = -np.nan
+    w[143, 1087] = -np.inf
+    got, want = B.bitlinear_fp8_quant_weight(dev(w), want_t=True, fmt=FMT[fmt]), H.fp8_quant_both(w, fmt, 128)
+    check_quant(got, want, True)
+
+
+@pytest.mark.parametrize("xf,wf", [("e4m3", "e4m3"), ("e5m2", "e5m2"), ("e4m3", "e5m2")])
+@pytest.mark.parametrize("t", [2, 20, 64, 300])
+def test_products_of_not_finite_blocks(t, xf, wf):
+    # forward and both gradients: what a block with an infinity or NaN enters is NaN, in either
+    # operand and format, and the rest is what it is without it
+    k, n = 640, 272
+    rng = np.random.default_rng(21)
+    x, dy = bf16(rng, t, k), bf16(rng, t, n, outliers=False)
+    w = rng.normal(size=(n, k)).astype(np.float32)
+
+    def run(x, w, dy):
+        xq = B.bitlinear_fp8_quant(dev(x, torch.bfloat16), want_t=True, fmt=FMT[xf])
+        wq = B.bitlinear_fp8_quant_weight(dev(w), want_t=True, fmt=FMT[wf])
+        dq = B.bitlinear_fp8_quant(dev(dy, torch.bfloat16), want_t=True, fmt=FMT[xf])
+        y = B.bitlinear_fp8_fwd(xq["q"], wq["q"], wq["scales"], x_scales=xq["scales"], y_dtype=torch.float32)
+        return [f64(a) for a in (y, *B.bitlinear_fp8_bwd(dq, xq, wq, grad_w_dtype=torch.float32))]
+
+    clean = run(x, w, dy)
+    x[1, 300], dy[0, 17], w[130, 5] = np.inf, np.nan, -np.inf
+    got = run(x, w, dy)
+    y, gx, gw = (np.isnan(a) for a in got)
+    rows, cols = np.arange(t), np.arange(n)
+    assert np.array_equal(y, (rows == 1)[:, None] | ((cols >= 128) & (cols < 256))[None, :])
+    # w's block (rows 128 to 255, columns 0 to 127) enters grad_x's columns 0 to 127
+    assert np.array_equal(gx, (rows == 0)[:, None] | (np.arange(k) < 128)[None, :])
+    assert np.array_equal(gw, (cols == 17)[:, None] | (np.arange(k) == 300)[None, :])
+    for a, b in zip(got, clean):
+        assert np.array_equal(a[~np.isnan(a)], b[~np.isnan(a)])
+
+
 # ------------------------------------------------------------------ linear cross entropy
 
 def ce_inputs(t, k, v, seed, logit_std=2.0):
