@@ -5,7 +5,10 @@ allocates missing outputs with torch (device memory is PyTorch's job here), and
 passes raw pointers plus a CUDA stream of the tensors' device (its current stream
 unless one is given) to the library, with that device current. Every step of the
 computation runs in the library's CUDA kernels; there is no other code path.
-"""
+
+A call with ``stream`` runs on that stream and orders it with no other: the caller lets it
+wait for the inputs, keeps them until it is through, and lets the current stream wait for the
+results. What the call allocates itself may be dropped at any time."""
 from __future__ import annotations
 
 import ctypes
@@ -32,6 +35,24 @@ def _call(fn, dev: torch.device, stream, *args) -> int:
 
 def _ptr(t) -> int | None:
     return None if t is None else int(t.data_ptr())
+
+
+def _empty(x: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """Memory on ``x``'s device for a call on ``stream``, out of that stream's pool. The current
+    stream's pool may hold memory that earlier calls there have yet to write, and hands this
+    call's on as soon as it is dropped: a given stream waits for neither."""
+    if stream is None or x.device.type != "cuda":
+        return x.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return x.new_empty(shape, dtype=dtype)
+
+
+def _result(x: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """``_empty``, for what the caller goes on using on the current stream."""
+    out = _empty(x, shape, dtype, stream)
+    if stream is not None:
+        out.record_stream(torch.cuda.current_stream(x.device))
+    return out
 
 
 def _need(t, dtype, shape, name, device=None):
@@ -101,22 +122,22 @@ def bitlinear_quant_mask(w: torch.Tensor, n_keep: int, m_group: int, *, want_mas
     dev = w.device
     o = dict(out or {})
     if "codes" not in o:
-        o["codes"] = torch.empty((n_out, k_in // 4), dtype=torch.uint8, device=dev)
+        o["codes"] = _result(w, (n_out, k_in // 4), torch.uint8, stream)
     if "w_scale" not in o:
-        o["w_scale"] = torch.empty((4,), dtype=torch.float32, device=dev)[:1]
+        o["w_scale"] = _result(w, (4,), torch.float32, stream)[:1]
     if want_mask and "mask" not in o:
-        o["mask"] = torch.empty((n_out, k_in // m_group), dtype=torch.uint8, device=dev)
+        o["mask"] = _result(w, (n_out, k_in // m_group), torch.uint8, stream)
     if want_w_i8 and "w_i8" not in o:
-        o["w_i8"] = torch.empty((n_out, k_in), dtype=torch.int8, device=dev)
+        o["w_i8"] = _result(w, (n_out, k_in), torch.int8, stream)
     if want_sp and "sp_values" not in o:
-        o["sp_values"] = torch.empty((n_out, k_in // 2), dtype=torch.int8, device=dev)
-        o["sp_meta"] = torch.empty(sp_meta_shape(n_out, k_in), dtype=torch.uint8, device=dev)
+        o["sp_values"] = _result(w, (n_out, k_in // 2), torch.int8, stream)
+        o["sp_meta"] = _result(w, sp_meta_shape(n_out, k_in), torch.uint8, stream)
     if m_group not in (4, 8) or k_in % m_group:
         raise ValueError(f"m_group must be 4 or 8 and divide k_in (got {m_group})")
     _check_qm_outputs(o, n_out, k_in, m_group, dev)
     ws_bytes = bitlinear_quant_mask_workspace_size(n_out, k_in)
     if workspace is None:
-        workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=dev)
+        workspace = _result(w, (ws_bytes,), torch.uint8, stream)
     _need_bytes(workspace, ws_bytes, "workspace", dev)
     st = _call(lib().bitlinear_quant_mask, dev, stream, _ptr(w), n_out, k_in, n_keep, m_group, _ptr(o.get("mask")),
                _ptr(o["codes"]), _ptr(o.get("w_i8")), _ptr(o.get("sp_values")), _ptr(o.get("sp_meta")),
@@ -138,22 +159,22 @@ def bitlinear_sgd_quant_mask(w: torch.Tensor, grad_w: torch.Tensor, lr: float, n
     dev = w.device
     o = dict(out or {})
     if "codes" not in o:
-        o["codes"] = torch.empty((n_out, k_in // 4), dtype=torch.uint8, device=dev)
+        o["codes"] = _result(w, (n_out, k_in // 4), torch.uint8, stream)
     if "w_scale" not in o:
-        o["w_scale"] = torch.empty((4,), dtype=torch.float32, device=dev)[:1]
+        o["w_scale"] = _result(w, (4,), torch.float32, stream)[:1]
     if want_mask and "mask" not in o:
-        o["mask"] = torch.empty((n_out, k_in // m_group), dtype=torch.uint8, device=dev)
+        o["mask"] = _result(w, (n_out, k_in // m_group), torch.uint8, stream)
     if want_w_i8 and "w_i8" not in o:
-        o["w_i8"] = torch.empty((n_out, k_in), dtype=torch.int8, device=dev)
+        o["w_i8"] = _result(w, (n_out, k_in), torch.int8, stream)
     if want_sp and "sp_values" not in o:
-        o["sp_values"] = torch.empty((n_out, k_in // 2), dtype=torch.int8, device=dev)
-        o["sp_meta"] = torch.empty(sp_meta_shape(n_out, k_in), dtype=torch.uint8, device=dev)
+        o["sp_values"] = _result(w, (n_out, k_in // 2), torch.int8, stream)
+        o["sp_meta"] = _result(w, sp_meta_shape(n_out, k_in), torch.uint8, stream)
     if m_group not in (4, 8) or k_in % m_group:
         raise ValueError(f"m_group must be 4 or 8 and divide k_in (got {m_group})")
     _check_qm_outputs(o, n_out, k_in, m_group, dev)
     ws_bytes = bitlinear_quant_mask_workspace_size(n_out, k_in)
     if workspace is None:
-        workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=dev)
+        workspace = _result(w, (ws_bytes,), torch.uint8, stream)
     _need_bytes(workspace, ws_bytes, "workspace", dev)
     st = _call(lib().bitlinear_sgd_quant_mask, dev, stream, _ptr(w), _ptr(grad_w), float(lr), n_out, k_in, n_keep,
                m_group, _ptr(o.get("mask")), _ptr(o["codes"]), _ptr(o.get("w_i8")), _ptr(o.get("sp_values")),
@@ -194,9 +215,9 @@ def bitlinear_act_quant(x: torch.Tensor, *, xq: torch.Tensor | None = None, absm
     t, k_in = x.shape
     _need(x, torch.bfloat16, None, "x")
     if xq is None:
-        xq = torch.empty((t, k_in), dtype=torch.int8, device=x.device)
+        xq = _result(x, (t, k_in), torch.int8, stream)
     if absmax is None:
-        absmax = torch.empty((max(t, 1) + 3) // 4 * 4, dtype=torch.float32, device=x.device)[:t]
+        absmax = _result(x, (max(t, 1) + 3) // 4 * 4, torch.float32, stream)[:t]
     _need(xq, torch.int8, (t, k_in), "xq", x.device)
     _need_vec(absmax, torch.float32, t, "absmax", x.device)
     st = _call(lib().bitlinear_act_quant, x.device, stream, _ptr(x), t, k_in, _ptr(xq), _ptr(absmax))
@@ -233,12 +254,12 @@ def bitlinear_fwd(xq: torch.Tensor, absmax: torch.Tensor, w_scale: torch.Tensor,
     _need_vec(absmax, torch.float32, t, "absmax", dev)
     _need_vec(w_scale, torch.float32, 1, "w_scale", dev)
     if y is None:
-        y = torch.empty((t, n_out), dtype=y_dtype, device=dev)
+        y = _result(xq, (t, n_out), y_dtype, stream)
     if y.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"y: expected bfloat16 or float32, got {y.dtype}")
     _need(y, y.dtype, (t, n_out), "y", dev)
     if want_acc and acc is None:
-        acc = torch.empty((t, n_out), dtype=torch.int32, device=dev)
+        acc = _result(xq, (t, n_out), torch.int32, stream)
     if acc is not None:
         _need(acc, torch.int32, (t, n_out), "acc", dev)
     ydt = BL_OUT_F32 if y.dtype == torch.float32 else BL_OUT_BF16
@@ -270,11 +291,11 @@ def bitlinear_fwd_grouped(problems: list[dict], *, y_dtype=torch.bfloat16, strea
         _need_vec(p["w_scale"], torch.float32, 1, f"problem {i} w_scale", dev)
         y = p.get("y")
         if y is None:
-            y = torch.empty((t, n_out), dtype=y_dtype, device=dev)
+            y = _result(xq, (t, n_out), y_dtype, stream)
         _need(y, y_dtype, (t, n_out), f"problem {i} y", dev)
         acc = p.get("acc")
         if acc is None and p.get("want_acc"):
-            acc = torch.empty((t, n_out), dtype=torch.int32, device=dev)
+            acc = _result(xq, (t, n_out), torch.int32, stream)
         if acc is not None:
             _need(acc, torch.int32, (t, n_out), f"problem {i} acc", dev)
         arr[i] = _lib.BlFwdProblem(_ptr(xq), _ptr(p["absmax"]), _ptr(codes), _ptr(p["w_scale"]), t, k_in, n_out,
@@ -308,7 +329,7 @@ def bitlinear_grad_w_grouped(problems: list[dict], *, grad_w_dtype=torch.bfloat1
         k_in = x.shape[1]
         gw = p.get("grad_w")
         if gw is None:
-            gw = torch.empty((n_out, k_in), dtype=grad_w_dtype, device=dev)
+            gw = _result(dy, (n_out, k_in), grad_w_dtype, stream)
         _need(gw, grad_w_dtype, (n_out, k_in), f"problem {i} grad_w", dev)
         arr[i] = _lib.BlGradWProblem(_ptr(dy), _ptr(x), k_in, n_out, _ptr(gw),
                                      BL_OUT_F32 if grad_w_dtype == torch.float32 else BL_OUT_BF16)
@@ -344,9 +365,9 @@ def bitlinear_bwd(dy: torch.Tensor, x: torch.Tensor | None, codes: torch.Tensor 
         k_in = (xq.shape[1] if deq and xq is not None else
                 x.shape[1] if x is not None else codes.shape[1] * 4)
     if want_grad_x and grad_x is None:
-        grad_x = torch.empty((t, k_in), dtype=torch.bfloat16, device=dev)
+        grad_x = _result(dy, (t, k_in), torch.bfloat16, stream)
     if want_grad_w and grad_w is None:
-        grad_w = torch.empty((n_out, k_in), dtype=grad_w_dtype, device=dev)
+        grad_w = _result(dy, (n_out, k_in), grad_w_dtype, stream)
     if grad_x is not None:
         _need(grad_x, torch.bfloat16, (t, k_in), "grad_x", dev)
         if codes is None or w_scale is None:
@@ -369,7 +390,7 @@ def bitlinear_bwd(dy: torch.Tensor, x: torch.Tensor | None, codes: torch.Tensor 
     gwdt = BL_OUT_F32 if (grad_w is not None and grad_w.dtype == torch.float32) else BL_OUT_BF16
     need = bitlinear_bwd_workspace_size(t, k_in, n_out, grad_x is not None, flags if grad_w is not None else 0)
     if need and workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = _empty(dy, (need,), torch.uint8, stream)
     if workspace is not None:
         _need_bytes(workspace, need, "workspace", dev)
     st = _call(lib().bitlinear_bwd, dev, stream, _ptr(dy), _ptr(x), _ptr(xq), _ptr(absmax), _ptr(codes),
@@ -395,13 +416,13 @@ def bitlinear_grad_x_i8(dy: torch.Tensor, codes: torch.Tensor, w_scale: torch.Te
         k_in = codes.shape[1] * 4
     _need(codes, torch.uint8, (n_out, k_in // 4), "codes", dev)
     if grad_x is None:
-        grad_x = torch.empty((t, k_in), dtype=torch.bfloat16, device=dev)
+        grad_x = _result(dy, (t, k_in), torch.bfloat16, stream)
     _need(grad_x, torch.bfloat16, (t, k_in), "grad_x", dev)
-    acc = torch.empty((t, k_in), dtype=torch.int32, device=dev) if want_acc else None
+    acc = _result(dy, (t, k_in), torch.int32, stream) if want_acc else None
     _need_vec(w_scale, torch.float32, 1, "w_scale", dev)
     need = bitlinear_grad_x_i8_workspace_size(t, k_in, n_out)
     if workspace is None and need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = _empty(dy, (need,), torch.uint8, stream)
     if workspace is not None:
         _need_bytes(workspace, need, "workspace", dev)
     st = _call(lib().bitlinear_grad_x_i8, dev, stream, _ptr(dy), _ptr(codes), _ptr(w_scale), t, k_in, n_out,
@@ -421,7 +442,7 @@ def bitlinear_mask_threshold_hist(w: torch.Tensor, mask: torch.Tensor, w_scale: 
     _need(mask, torch.uint8, (n_out, k_in // m_group), "mask", w.device)
     _need_vec(w_scale, torch.float32, 1, "w_scale", w.device)
     if out is None:
-        out = torch.empty((19,), dtype=torch.int64, device=w.device)
+        out = _result(w, (19,), torch.int64, stream)
     _need(out, torch.int64, (19,), "out", w.device)
     st = _call(lib().bitlinear_mask_threshold_hist, w.device, stream, _ptr(w), _ptr(mask), _ptr(w_scale), n_out,
                k_in, m_group, _ptr(out))

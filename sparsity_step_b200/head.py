@@ -1,10 +1,6 @@
 """Python binding of the head's operators (include/bitlinear.h): the block-scaled 8-bit
 float linear and the linear cross entropy. Argument checks and marshalling only, as in
-``bitlinear.py``.
-
-A call with ``stream`` runs on that stream and orders it with no other: the caller lets it
-wait for the inputs, keeps them until it is through, and lets the current stream wait for the
-results. What the call allocates itself may be dropped at any time."""
+``bitlinear.py``."""
 from __future__ import annotations
 
 import functools
@@ -12,7 +8,7 @@ import functools
 import torch
 
 from ._lib import BL_OUT_BF16, BL_OUT_F32, check, lib
-from .bitlinear import _call, _need, _need_bytes, _ptr
+from .bitlinear import _call, _empty, _need, _need_bytes, _ptr, _result
 
 BL_FP8_E4M3 = 0
 BL_FP8_E5M2 = 1
@@ -56,24 +52,6 @@ def _matrix(t, name: str) -> tuple[int, int]:
 def _size(fn: str, *args) -> int:
     """A workspace size (a function of the arguments alone)."""
     return int(getattr(lib(), fn)(*args))
-
-
-def _empty(x: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
-    """Memory on ``x``'s device for a call on ``stream``, out of that stream's pool. The current
-    stream's pool may hold memory that earlier calls there have yet to write, and hands this
-    call's on as soon as it is dropped: a given stream waits for neither."""
-    if stream is None or x.device.type != "cuda":
-        return x.new_empty(shape, dtype=dtype)
-    with torch.cuda.stream(stream):
-        return x.new_empty(shape, dtype=dtype)
-
-
-def _result(x: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
-    """``_empty``, for what the caller goes on using on the current stream."""
-    out = _empty(x, shape, dtype, stream)
-    if stream is not None:
-        out.record_stream(torch.cuda.current_stream(x.device))
-    return out
 
 
 def _workspace(given, need: int, x: torch.Tensor, stream):

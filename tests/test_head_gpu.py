@@ -813,6 +813,30 @@ def test_dropped_results_of_a_given_stream():
     assert waiting and torch.equal(loss, want) and all(bool((j == 7.0).all()) for j in junk)
 
 
+def test_given_stream_in_a_captured_graph():
+    # a call on a stream that joined the capture, its results and workspace its own
+    t, k, v = 300, 512, 700
+    gen = torch.Generator(device="cuda").manual_seed(24)
+    x = torch.randn(t, k, generator=gen, device="cuda").to(torch.bfloat16)
+    head = (torch.randn(v, k, generator=gen, device="cuda") * 0.1).to(torch.bfloat16)
+    y, g = torch.randint(0, v, (t,), generator=gen, device="cuda"), torch.randn(t, generator=gen, device="cuda")
+    loss, lse = B.bitlinear_linear_ce_fwd(x, head, y)
+    want = [loss, *B.bitlinear_linear_ce_bwd(x, head, y, lse, g)]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        loss, lse = B.bitlinear_linear_ce_fwd(x, head, y, stream=side)
+        got = [loss, *B.bitlinear_linear_ce_bwd(x, head, y, lse, g, stream=side)]
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        for a in got:
+            a.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_more_than_2_to_31_elements():
     # 384 rows over and over: the last copy, whose offsets pass 32 bits, comes out as the first
     reps, rows, k, n = 2732, 384, 2048, 16

@@ -619,6 +619,41 @@ def test_grad_x_int8_dy_training_shape():
     assert_bf16_within_ulp(bf16_dev_to_bits(out["grad_x"])[rows], y_ref, "grad_x_i8 training shape")
 
 
+# ------------------------------------------------------------------ streams
+
+
+def test_results_on_a_given_stream_are_not_written_by_earlier_calls():
+    # the current stream has yet to write the dropped results of its calls; the same calls on
+    # another stream must not be handed their memory
+    t, k, n = 300, 512, 256
+    gen = torch.Generator(device="cuda").manual_seed(23)
+    sets = []
+    for _ in range(2):
+        w = torch.randn(n, k, generator=gen, device="cuda")
+        x, dy = (torch.randn(t, c, generator=gen, device="cuda").to(torch.bfloat16) for c in (k, n))
+        sets.append((w, x, dy, B.bitlinear_quant_mask(w, 6, 8), B.bitlinear_act_quant(x)))
+    calls = {
+        "quant_mask": lambda w, x, dy, qm, aq, **o: [B.bitlinear_quant_mask(w, 6, 8, **o)[key] for key in ("codes", "w_i8", "mask")],
+        "act_quant": lambda w, x, dy, qm, aq, **o: list(B.bitlinear_act_quant(x, **o)),
+        "fwd": lambda w, x, dy, qm, aq, **o: [B.bitlinear_fwd(*aq, qm["w_scale"], w_i8=qm["w_i8"], **o)[0]],
+        "bwd": lambda w, x, dy, qm, aq, **o: list(B.bitlinear_bwd(dy, x, qm["codes"], qm["w_scale"], **o)),
+        "grad_w_grouped": lambda w, x, dy, qm, aq, **o: B.bitlinear_grad_w_grouped([{"dy": dy, "x": x}], **o),
+        "grad_x_i8": lambda w, x, dy, qm, aq, **o: [B.bitlinear_grad_x_i8(dy, qm["codes"], qm["w_scale"], **o)["grad_x"]],
+    }
+    s = torch.cuda.Stream()
+    for name, call in calls.items():
+        want = [r.clone() for r in call(*sets[1])]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(400_000_000)
+        call(*sets[0])
+        got = call(*sets[1], stream=s)
+        s.synchronize()
+        waiting = not torch.cuda.current_stream().query()
+        torch.cuda.synchronize()
+        assert waiting, name
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+
+
 # ------------------------------------------------------------------ failure detection
 
 
