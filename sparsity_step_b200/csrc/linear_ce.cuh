@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
 // the outputs alone: 1.7e-3), while over many tokens the errors meet the outputs' rounding
 // (2.0e-3 to 2.2e-3). So where there are few tokens dl is carried as the sum of two bf16
 // numbers. Up to 32 tokens their 64 rows are one K block of grad_W and part of one tile of
-// the other products: 32 x 1536 x 32003 takes 99 us, 33 tokens 91 (up to 128 tokens it cost
+// the other products: 32 x 1536 x 32003 takes 105 us, 33 tokens 95 (up to 128 tokens it cost
 // 10 to 20%).
 constexpr int kCeSplitTokens = 32;
 

@@ -566,7 +566,7 @@ def sure_inputs(t, k, v, seed, top=18.0):
 
 
 @pytest.mark.parametrize("t,k,v", [(1, 2048, 1000), (32, 2048, 1000), (33, 2048, 1000), (200, 2048, 1000), (20, 8192, 1000),
-                                   (100, 8192, 700), (40, 512, 5003), (64, 2048, 9001)])
+                                   (100, 8192, 700), (40, 512, 5003), (64, 2048, 9001), (20, 16448, 700)])
 def test_linear_ce_gradient_of_sure_tokens(t, k, v):
     """dl of tokens that are nearly sure of their target, one at a time (g is 0 elsewhere, so
     that grad_w of row u is dl_u x): with 1 - p down to 1e-5 it has to come from l_y - lse as
